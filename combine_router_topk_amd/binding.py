@@ -28,6 +28,7 @@ MOE_FLAG_OUT_F32 = 1 << 1
 MOE_MAX_E, MOE_MAX_K, MOE_MAX_R, MOE_MAX_REP = 1024, 16, 1024, 16
 MOE_MAX_ROWS = (1 << 24) - 1
 MOE_NOALLOC_SCRATCH_BYTES = 2 << 20
+MOE_SCALE_BLOCK, MOE_MAX_NORM_H, MOE_MAX_FEW_TOKENS = 128, 16384, 64
 
 EXPORTED = ("moe_version", "moe_build_id", "moe_status_string", "moe_last_error", "moe_workspace_bytes",
             "moe_route", "moe_assign_replicas", "moe_layout", "moe_route_assign_layout",
@@ -35,9 +36,13 @@ EXPORTED = ("moe_version", "moe_build_id", "moe_status_string", "moe_last_error"
             "moe_layout_single_send",
             "moe_single_send_dispatch", "moe_single_send_expand", "moe_dispatch",
             "moe_expert_standin", "moe_combine", "moe_combine_backward", "moe_dispatch_backward",
-            "moe_routing_stats", "moe_token_balanced_split")
+            "moe_routing_stats", "moe_token_balanced_split",
+           "moe_rms_norm", "moe_rms_norm_workspace_bytes", "moe_rms_norm_backward",
+           "moe_expert_gemm", "moe_expert_gemm_swiglu", "moe_layer_workspace_bytes",
+           "moe_layer_few_tokens")
 
 _TORCH_ACT = {MOE_F16: torch.float16, MOE_BF16: torch.bfloat16}
+E4M3 = torch.float8_e4m3fn
 
 
 class MoeError(RuntimeError):
@@ -88,6 +93,13 @@ def _load() -> ctypes.CDLL:
         "moe_dispatch_backward": (i32, [P, vp, vp, vp, vp]),
         "moe_routing_stats": (i32, [P, vp, vp, vp, vp, vp, vp, vp]),
         "moe_token_balanced_split": (i32, [P, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp]),
+        "moe_rms_norm": (i32, [P, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp, vp]),
+        "moe_rms_norm_workspace_bytes": (i32, [P, ctypes.POINTER(sz)]),
+        "moe_rms_norm_backward": (i32, [P, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "moe_expert_gemm": (i32, [P, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "moe_expert_gemm_swiglu": (i32, [P, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "moe_layer_workspace_bytes": (i32, [P, i32, ctypes.POINTER(sz)]),
+        "moe_layer_few_tokens": (i32, [P, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -370,3 +382,109 @@ def moe_token_balanced_split(p: Problem, idx, counts, pos, expert_offsets, rep, 
         _ptr(rep, torch.int32, p.E * maxrep if rep is not None else 0, "rep"), maxrep,
         _ptr(gpu_of_pair, torch.int32, n, "gpu_of_pair"), _ptr(active, torch.int32, p.R, "active"),
         _ptr(tokens, torch.int32, p.R, "tokens"), _stream(stream)), "moe_token_balanced_split")
+
+
+def scale_blocks(cols: int) -> int:
+    """Scales of an 8-bit row of `cols` columns."""
+    return -(-cols // MOE_SCALE_BLOCK)
+
+
+def _call(name: str, stream, tensors, args) -> None:
+    """The library's call on the device that all tensors share, on that
+    device's current stream unless one is given."""
+    dev = None
+    for t in tensors:
+        if isinstance(t, torch.Tensor):
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"{name}: tensors on {dev} and on {t.device}")
+    f = getattr(_lib, name)
+    if dev is None or dev.index == torch.cuda.current_device():
+        _check(f(*args, _stream(stream)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args, _stream(stream)), name)
+
+
+def moe_rms_norm(p: Problem, x, residual, gamma, eps: float, h, y, q, q_scale, rstd, stream=None) -> None:
+    """residual and h go together, q and q_scale too (None to leave them out);
+    y may be None beside q, rstd too. q holds float8_e4m3fn."""
+    act, n = _TORCH_ACT.get(p.act_dtype), p.T * p.H
+    _call("moe_rms_norm", stream, (x, residual, gamma, h, y, q, q_scale, rstd),
+          (ctypes.byref(p), _ptr(x, act, n, "x"), _ptr(residual, act, n, "residual"),
+           _ptr(gamma, act, p.H, "gamma"), eps, _ptr(h, act, n, "h"), _ptr(y, act, n, "y"),
+           _ptr(q, E4M3, n, "q"), _ptr(q_scale, torch.float32, p.T * scale_blocks(p.H), "q_scale"),
+           _ptr(rstd, torch.float32, p.T, "rstd")))
+
+
+def moe_rms_norm_workspace_bytes(p: Problem) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.moe_rms_norm_workspace_bytes(ctypes.byref(p), ctypes.byref(n)),
+           "moe_rms_norm_workspace_bytes")
+    return n.value
+
+
+def moe_rms_norm_backward(p: Problem, dy, dh, h, gamma, rstd, dx, dgamma, ws, stream=None) -> None:
+    """dh may be None (no gradient along the residual stream)."""
+    act, n = _TORCH_ACT.get(p.act_dtype), p.T * p.H
+    _call("moe_rms_norm_backward", stream, (dy, dh, h, gamma, rstd, dx, dgamma, ws),
+          (ctypes.byref(p), _ptr(dy, act, n, "dy"), _ptr(dh, act, n, "dh"), _ptr(h, act, n, "h"),
+           _ptr(gamma, act, p.H, "gamma"), _ptr(rstd, torch.float32, p.T, "rstd"),
+           _ptr(dx, act, n, "dx"), _ptr(dgamma, torch.float32, p.H, "dgamma"),
+           _ptr(ws, None, None, "ws"), _nbytes(ws)))
+
+
+def _gemm_args(p: Problem, K: int, rows: int, a, a_scale, src, w, w_scale, counts, expert_offsets):
+    """The arguments that both experts' products share; `rows` of weights."""
+    n = p.T * p.k
+    a_rows = n if src is None else p.T
+    nb = scale_blocks(K)
+    return (_ptr(a, E4M3, a_rows * K, "a"), _ptr(a_scale, torch.float32, a_rows * nb, "a_scale"),
+            _ptr(src, torch.int32, n, "src"), _ptr(w, E4M3, p.E * rows * K, "w"),
+            _ptr(w_scale, torch.float32, p.E * scale_blocks(rows) * nb, "w_scale"),
+            _ptr(counts, torch.int32, p.E, "counts"),
+            _ptr(expert_offsets, torch.int32, p.E, "expert_offsets"))
+
+
+def moe_expert_gemm(p: Problem, K: int, N: int, a, a_scale, src, w, w_scale, counts, expert_offsets,
+                    y, stream=None) -> None:
+    """src None: a holds the T k rows in send order; given: the T token rows."""
+    out_dt = torch.float32 if p.flags & MOE_FLAG_OUT_F32 else _TORCH_ACT.get(p.act_dtype)
+    _call("moe_expert_gemm", stream, (a, a_scale, src, w, w_scale, counts, expert_offsets, y),
+          (ctypes.byref(p), K, N, *_gemm_args(p, K, N, a, a_scale, src, w, w_scale, counts, expert_offsets),
+           _ptr(y, out_dt, p.T * p.k * N, "y")))
+
+
+def moe_expert_gemm_swiglu(p: Problem, K: int, I: int, a, a_scale, src, w, w_scale, counts,
+                           expert_offsets, q, q_scale, stream=None) -> None:
+    """w holds 2 I rows an expert, the gate's first; src as in moe_expert_gemm."""
+    n = p.T * p.k
+    _call("moe_expert_gemm_swiglu", stream,
+          (a, a_scale, src, w, w_scale, counts, expert_offsets, q, q_scale),
+          (ctypes.byref(p), K, I,
+           *_gemm_args(p, K, 2 * I, a, a_scale, src, w, w_scale, counts, expert_offsets),
+           _ptr(q, E4M3, n * I, "q"), _ptr(q_scale, torch.float32, n * scale_blocks(I), "q_scale")))
+
+
+def moe_layer_workspace_bytes(p: Problem, I: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.moe_layer_workspace_bytes(ctypes.byref(p), I, ctypes.byref(n)), "moe_layer_workspace_bytes")
+    return n.value
+
+
+def moe_layer_few_tokens(p: Problem, I: int, logits, x, w_up, s_up, w_down, s_down, idx, w, out, ws,
+                         stream=None) -> None:
+    """s_up and s_down None: weights in the activation format; given: e4m3."""
+    act, n = _TORCH_ACT.get(p.act_dtype), p.T * p.k
+    out_dt = torch.float32 if p.flags & MOE_FLAG_OUT_F32 else act
+    w_dt = act if s_up is None else E4M3
+    nh, ni = scale_blocks(p.H), scale_blocks(I)
+    _call("moe_layer_few_tokens", stream, (logits, x, w_up, s_up, w_down, s_down, idx, w, out, ws),
+          (ctypes.byref(p), I, _ptr(logits, torch.float32, p.T * p.E, "logits"),
+           _ptr(x, act, p.T * p.H, "x"), _ptr(w_up, w_dt, p.E * 2 * I * p.H, "w_up"),
+           _ptr(s_up, torch.float32, p.E * scale_blocks(2 * I) * nh, "s_up"),
+           _ptr(w_down, w_dt, p.E * p.H * I, "w_down"),
+           _ptr(s_down, torch.float32, p.E * nh * ni, "s_down"), _ptr(idx, torch.int32, n, "idx"),
+           _ptr(w, torch.float32, n, "w"), _ptr(out, out_dt, p.T * p.H, "out"),
+           _ptr(ws, None, None, "ws"), _nbytes(ws)))

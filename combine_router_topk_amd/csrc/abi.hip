@@ -138,11 +138,51 @@ moe_status check_route_assign_layout(const moe_problem* p, const float* logits, 
   return MOE_OK;
 }
 
+moe_status check_norm(const moe_problem* p, const char* fn) {
+  CHECK(check_problem(p, fn));
+  if (p->H > MOE_MAX_NORM_H)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d is over %d", fn, p->H, MOE_MAX_NORM_H);
+  return MOE_OK;
+}
+
+size_t norm_ws_bytes(const moe_problem* p) {
+  return static_cast<size_t>(moe::rms_norm_backward_blocks(p->T)) * p->H * sizeof(float);
+}
+
+// Checks shared by the two experts' products; n is the weight rows of an expert.
+moe_status check_expert_gemm(const moe_problem* p, int32_t K, int64_t n, const void* a,
+                             const float* a_scale, const int32_t* src, const void* w,
+                             const float* w_scale, const int32_t* counts, const int32_t* expert_offsets,
+                             const char* fn) {
+  if (K <= 0 || K % 16 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: K=%d is not a positive multiple of 16", fn, K);
+  if (n > INT32_MAX || !moe::expert_gemm_fits(p->T, p->E, p->k, K, static_cast<int>(n), src != nullptr))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: T*k=%d rows, K=%d, %lld weight rows are beyond 32-bit offsets", fn,
+                p->T * p->k, K, static_cast<long long>(n));
+  if (p->T == 0) return MOE_OK;
+  CHECK(need(a, 16, fn, "a"));
+  CHECK(need(a_scale, 4, fn, "a_scale"));
+  if (src != nullptr) CHECK(need(src, 4, fn, "src"));
+  CHECK(need(w, 16, fn, "w"));
+  CHECK(need(w_scale, 4, fn, "w_scale"));
+  CHECK(need(counts, 4, fn, "counts"));
+  return need(expert_offsets, 4, fn, "expert_offsets");
+}
+
+moe_status check_layer(const moe_problem* p, int32_t I, const char* fn) {
+  CHECK(check_problem(p, fn));
+  if (p->H % 16 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: H=%d is not a multiple of 16", fn, p->H);
+  if (I <= 0 || I % 16 != 0 || I > (1 << 24))
+    return fail(MOE_ERR_INVALID_ARG, "%s: I=%d is not a multiple of 16 in [16, 2^24]", fn, I);
+  if (p->T > MOE_MAX_FEW_TOKENS)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: T=%d is over %d", fn, p->T, MOE_MAX_FEW_TOKENS);
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
 
-int32_t moe_version(void) { return 1 * 10000 + 2 * 100 + 0; }
+int32_t moe_version(void) { return 1 * 10000 + 3 * 100 + 0; }
 
 const char* moe_build_id(void) { return MOE_BUILD_ID; }
 
@@ -493,6 +533,146 @@ moe_status moe_token_balanced_split(const moe_problem* p, const int32_t* idx,
                                                      rep ? maxrep : 1, p->T, p->E, p->k, p->R,
                                                      gpu_of_pair, active, tokens,
                                                      static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+moe_status moe_rms_norm(const moe_problem* p, const void* x, const void* residual,
+                        const void* gamma, float eps, void* h, void* y, void* q, float* q_scale,
+                        float* rstd, void* stream) {
+  const char* fn = "moe_rms_norm";
+  CHECK(check_norm(p, fn));
+  if (!(eps >= 0.0f) || eps > 3.4e38f) return fail(MOE_ERR_INVALID_ARG, "%s: eps=%g is not finite and >= 0", fn, eps);
+  if (p->T == 0) return MOE_OK;
+  if ((residual == nullptr) != (h == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "%s: residual and h go together", fn);
+  if ((q == nullptr) != (q_scale == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "%s: q and q_scale go together", fn);
+  if (y == nullptr && q == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: y and q are both NULL", fn);
+  if (y != nullptr && y == h) return fail(MOE_ERR_INVALID_ARG, "%s: y and h are the same buffer", fn);
+  CHECK(need(x, 16, fn, "x"));
+  if (residual != nullptr) {
+    CHECK(need(residual, 16, fn, "residual"));
+    CHECK(need(h, 16, fn, "h"));
+  }
+  CHECK(need(gamma, 16, fn, "gamma"));
+  if (y != nullptr) CHECK(need(y, 16, fn, "y"));
+  if (q != nullptr) {
+    CHECK(need(q, 8, fn, "q"));
+    CHECK(need(q_scale, 4, fn, "q_scale"));
+  }
+  if (rstd != nullptr) CHECK(need(rstd, 4, fn, "rstd"));
+  clear_stale_error();
+  return hip_status(moe::launch_rms_norm(x, residual, gamma, eps, h, y, q, q_scale, rstd, p->T, p->H,
+                                         p->act_dtype, static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+moe_status moe_rms_norm_workspace_bytes(const moe_problem* p, size_t* bytes) {
+  const char* fn = "moe_rms_norm_workspace_bytes";
+  CHECK(check_norm(p, fn));
+  if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is NULL", fn);
+  *bytes = norm_ws_bytes(p);
+  return MOE_OK;
+}
+
+moe_status moe_rms_norm_backward(const moe_problem* p, const void* dy, const void* dh,
+                                 const void* h, const void* gamma, const float* rstd, void* dx,
+                                 float* dgamma, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_rms_norm_backward";
+  CHECK(check_norm(p, fn));
+  CHECK(need(dgamma, 4, fn, "dgamma"));
+  if (p->T > 0) {
+    CHECK(need(dy, 16, fn, "dy"));
+    if (dh != nullptr) CHECK(need(dh, 16, fn, "dh"));
+    CHECK(need(h, 16, fn, "h"));
+    CHECK(need(gamma, 16, fn, "gamma"));
+    CHECK(need(rstd, 4, fn, "rstd"));
+    CHECK(need(dx, 16, fn, "dx"));
+    CHECK(need(ws, 256, fn, "ws"));
+  }
+  const size_t req = norm_ws_bytes(p);
+  if (ws_bytes < req) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, req);
+  clear_stale_error();
+  return hip_status(moe::launch_rms_norm_backward(dy, dh, h, gamma, rstd, dx, dgamma,
+                                                  static_cast<float*>(ws), p->T, p->H, p->act_dtype,
+                                                  static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+moe_status moe_expert_gemm(const moe_problem* p, int32_t K, int32_t N, const void* a,
+                           const float* a_scale, const int32_t* src, const void* w,
+                           const float* w_scale, const int32_t* counts,
+                           const int32_t* expert_offsets, void* y, void* stream) {
+  const char* fn = "moe_expert_gemm";
+  CHECK(check_problem(p, fn));
+  if (N <= 0 || N % 8 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: N=%d is not a positive multiple of 8", fn, N);
+  CHECK(check_expert_gemm(p, K, N, a, a_scale, src, w, w_scale, counts, expert_offsets, fn));
+  if (p->T == 0) return MOE_OK;
+  CHECK(need(y, 16, fn, "y"));
+  clear_stale_error();
+  return hip_status(moe::launch_expert_gemm(a, a_scale, src, w, w_scale, counts, expert_offsets, p->T,
+                                            p->E, p->k, K, N, y, p->act_dtype,
+                                            (p->flags & MOE_FLAG_OUT_F32) != 0,
+                                            static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+moe_status moe_expert_gemm_swiglu(const moe_problem* p, int32_t K, int32_t I, const void* a,
+                                  const float* a_scale, const int32_t* src, const void* w,
+                                  const float* w_scale, const int32_t* counts,
+                                  const int32_t* expert_offsets, void* q, float* q_scale,
+                                  void* stream) {
+  const char* fn = "moe_expert_gemm_swiglu";
+  CHECK(check_problem(p, fn));
+  if (I <= 0 || I % 16 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: I=%d is not a positive multiple of 16", fn, I);
+  CHECK(check_expert_gemm(p, K, 2 * static_cast<int64_t>(I), a, a_scale, src, w, w_scale, counts,
+                          expert_offsets, fn));
+  if (p->T == 0) return MOE_OK;
+  CHECK(need(q, 16, fn, "q"));
+  CHECK(need(q_scale, 4, fn, "q_scale"));
+  clear_stale_error();
+  return hip_status(moe::launch_expert_gemm_swiglu(a, a_scale, src, w, w_scale, counts, expert_offsets,
+                                                   p->T, p->E, p->k, K, I, q, q_scale,
+                                                   static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+moe_status moe_layer_workspace_bytes(const moe_problem* p, int32_t I, size_t* bytes) {
+  const char* fn = "moe_layer_workspace_bytes";
+  CHECK(check_layer(p, I, fn));
+  if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is NULL", fn);
+  *bytes = moe::layer_ws_bytes(p->T, p->k, I);
+  return MOE_OK;
+}
+
+moe_status moe_layer_few_tokens(const moe_problem* p, int32_t I, const float* logits, const void* x,
+                                const void* w_up, const float* s_up, const void* w_down,
+                                const float* s_down, int32_t* idx, float* w, void* out, void* ws,
+                                size_t ws_bytes, void* stream) {
+  const char* fn = "moe_layer_few_tokens";
+  CHECK(check_layer(p, I, fn));
+  if ((s_up == nullptr) != (s_down == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "%s: s_up and s_down go together", fn);
+  if (p->T == 0) return MOE_OK;
+  CHECK(need(logits, 4, fn, "logits"));
+  CHECK(need(x, 16, fn, "x"));
+  CHECK(need(w_up, 16, fn, "w_up"));
+  CHECK(need(w_down, 16, fn, "w_down"));
+  if (s_up != nullptr) {
+    CHECK(need(s_up, 4, fn, "s_up"));
+    CHECK(need(s_down, 4, fn, "s_down"));
+  }
+  CHECK(need(idx, 4, fn, "idx"));
+  CHECK(need(w, 4, fn, "w"));
+  CHECK(need(out, 16, fn, "out"));
+  CHECK(need(ws, 256, fn, "ws"));
+  const size_t req = moe::layer_ws_bytes(p->T, p->k, I);
+  if (ws_bytes < req) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, req);
+  clear_stale_error();
+  return hip_status(moe::launch_layer_few_tokens(logits, x, w_up, s_up, w_down, s_down, p->T, p->E, p->k,
+                                                 p->H, I, idx, w, out, ws, p->act_dtype,
+                                                 (p->flags & MOE_FLAG_OUT_F32) != 0,
+                                                 static_cast<hipStream_t>(stream)),
                     fn);
 }
 

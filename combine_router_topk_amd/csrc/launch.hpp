@@ -142,4 +142,34 @@ hipError_t launch_token_balanced_split(const int32_t* idx, const int32_t* counts
                                        int32_t* gpu_of_pair, int32_t* active, int32_t* tokens,
                                        hipStream_t s);
 
+hipError_t launch_rms_norm(const void* x, const void* residual, const void* gamma, float eps, void* h,
+                           void* y, void* q, float* q_scale, float* rstd, int T, int H, int act,
+                           hipStream_t s);
+// Blocks of the backward's first kernel: its workspace holds one fp32 row of
+// H for each.
+int rms_norm_backward_blocks(int T);
+hipError_t launch_rms_norm_backward(const void* dy, const void* dh, const void* h, const void* gamma,
+                                    const float* rstd, void* dx, float* dgamma, float* ws, int T, int H,
+                                    int act, hipStream_t s);
+
+// Whether the 32-bit offsets and tile numbers of the experts' products hold
+// a problem of these sizes (n: weight rows of an expert; gather: the rows are
+// found through src).
+bool expert_gemm_fits(int T, int E, int k, int K, int n, bool gather);
+hipError_t launch_expert_gemm(const void* a, const float* a_scale, const int32_t* src, const void* w,
+                              const float* w_scale, const int32_t* counts, const int32_t* offsets,
+                              int T, int E, int k, int K, int N, void* y, int act, bool out_f32,
+                              hipStream_t s);
+hipError_t launch_expert_gemm_swiglu(const void* a, const float* a_scale, const int32_t* src, const void* w,
+                                     const float* w_scale, const int32_t* counts, const int32_t* offsets,
+                                     int T, int E, int k, int K, int I, void* q, float* q_scale,
+                                     hipStream_t s);
+
+size_t layer_ws_bytes(int T, int k, int I);
+// s_up and s_down null: weights in the activation format, else e4m3.
+hipError_t launch_layer_few_tokens(const float* logits, const void* x, const void* w_up, const float* s_up,
+                                   const void* w_down, const float* s_down, int T, int E, int k, int H, int I,
+                                   int32_t* idx, float* w, void* out, void* ws, int act, bool out_f32,
+                                   hipStream_t s);
+
 }  // namespace moe

@@ -1,0 +1,419 @@
+// A whole mixture-of-experts layer for at most 64 tokens, in two launches:
+// top-k and gate weights, gate and up products with SwiGLU, then the down
+// product with the weighted combine.
+//
+//   h[t, j] = round16(silu(Wg x[t]) * (Wu x[t])),  (Wg; Wu) = expert idx[t, j]'s
+//   out[t]  = round(sum over j of w[t, j] (Wd h[t, j])), summed in fp32
+//
+// The time is that of reading the chosen experts' weights once: nothing is
+// dispatched, rows are read where they are, and the weights go from memory
+// to registers in the matrix instruction's layout (16 weight rows as its
+// first operand, up to 16 tokens as its second). Activations stay in 16
+// bits, as a few rows are not worth rounding to 8; e4m3 weights become 16-bit
+// numbers in registers, exactly, and a block's scale is applied to the fp32
+// sum of its 128 products.
+#include "device.hpp"
+#include "launch.hpp"
+#include "quant.hpp"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMaxTokens = 64;
+constexpr int kMaxPairs = kMaxTokens * kMaxK;
+constexpr int kUpThreads = 256, kUpWaves = kUpThreads / kWave;
+constexpr int kUpBlocks = 1024;  // at most; four a CU
+constexpr int kDownThreads = 512, kDownWaves = kDownThreads / kWave;
+constexpr int kRowsPerTile = 16;
+
+struct LayerArgs {
+  const float* logits;
+  const void* x;
+  const void* w_up;
+  const float* s_up;
+  const void* w_down;
+  const float* s_down;
+  int T, E, k, H, I;
+  int32_t* idx;
+  float* w;
+  void* h;
+  void* out;
+  bool out_f32;
+};
+
+// One step of K for a tile of 16 weight rows and 16 tokens: 128 bytes of each
+// weight row (128 codes, or 64 values in 16 bits). Lane (r, g) = (lane % 16,
+// lane / 16) holds chunk g and chunk 4 + g of row r's eight 16-byte chunks, and
+// the same columns of its token; both operands place their columns alike, so
+// their order inside the instruction does not matter.
+template <int ACT, bool F8>
+struct Step {
+  static constexpr int kCols = F8 ? 128 : 64;  // columns of K
+  static constexpr int kPer = F8 ? 16 : 8;     // columns of a chunk
+  static constexpr int kB = F8 ? 2 : 1;        // 16-byte chunks of a token for one of weights
+  struct Rows { uint4 v[2]; };
+  struct Cols { uint4 v[2 * kB]; };
+
+  // columns lane chunk j starts at
+  static __device__ __forceinline__ int col(int kb, int j, int grp) { return kb * kCols + (j * 4 + grp) * kPer; }
+
+  // `row` is the lane's weight row; columns from K on are zeros
+  static __device__ __forceinline__ void load_rows(Rows& r, const unsigned char* row, int kb, int grp, int K) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c = col(kb, j, grp);
+      r.v[j] = make_uint4(0, 0, 0, 0);
+      if (c < K) r.v[j] = *reinterpret_cast<const uint4*>(row + static_cast<size_t>(c) * (F8 ? 1 : 2));
+    }
+  }
+  static __device__ __forceinline__ void load_cols(Cols& b, const uint16_t* tok, int kb, int grp, int K) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c = col(kb, j, grp);
+#pragma unroll
+      for (int i = 0; i < kB; ++i) {
+        b.v[j * kB + i] = make_uint4(0, 0, 0, 0);
+        if (c < K) b.v[j * kB + i] = *reinterpret_cast<const uint4*>(tok + c + i * 8);
+      }
+    }
+  }
+  static __device__ __forceinline__ v4f product(const Rows& r, const Cols& b) {
+    v4f p = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (F8) {
+        const uint2 a0 = widen4<ACT>(r.v[j].x), a1 = widen4<ACT>(r.v[j].y);
+        const uint2 a2 = widen4<ACT>(r.v[j].z), a3 = widen4<ACT>(r.v[j].w);
+        p = mfma16<ACT>(make_uint4(a0.x, a0.y, a1.x, a1.y), b.v[j * 2], p);
+        p = mfma16<ACT>(make_uint4(a2.x, a2.y, a3.x, a3.y), b.v[j * 2 + 1], p);
+      } else {
+        p = mfma16<ACT>(r.v[j], b.v[j], p);
+      }
+    }
+    return p;
+  }
+};
+
+// The k best experts of one token, by one wave: slot j's expert and logit key
+// end in lane j. Lane l holds experts l V .. l V + V - 1, so among equal keys
+// the lowest expert sits in the lowest lane, at that lane's lowest slot.
+template <int V>
+__device__ __forceinline__ void topk_wave(const float* __restrict__ row, int E, int k, int lane, int& my_e,
+                                          uint32_t& my_key, uint32_t& top_key) {
+  uint32_t key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = lane * V + v;
+    key[v] = e < E ? logit_key(row[e]) : 0u;
+  }
+  my_e = 0;
+  my_key = top_key = 0u;
+  for (int j = 0; j < k; ++j) {
+    uint32_t lm = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) lm = umax(lm, key[v]);
+    const uint32_t best = wave_max_u32(lm);
+    const int l = __builtin_ctzll(ballot(lm == best));
+    int fv = V - 1;
+#pragma unroll
+    for (int v = V - 2; v >= 0; --v) fv = key[v] == best ? v : fv;
+    const int fvs = __builtin_amdgcn_readlane(fv, l);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v == fvs) key[v] = lane == l ? 0u : key[v];
+    if (lane == j) {
+      my_e = l * V + fvs;
+      my_key = best;
+    }
+    if (j == 0) top_key = best;
+  }
+}
+
+// ---- launch 1: top-k, gate and up products, SwiGLU ---------------------------
+
+struct UpShared {
+  int idx[kMaxPairs];         // expert of each (token, slot) pair
+  int order[kMaxPairs];       // pairs by expert, then by token
+  int item[kMaxPairs];        // (expert, group of 16 of its pairs)
+  int count[kMaxE];
+  int offset[kMaxE];
+  int items;
+  float4 part[2][kUpWaves][2][kWave];
+};
+
+template <int ACT, bool F8, int V>
+__global__ __launch_bounds__(kUpThreads, 4) void layer_up_kernel(LayerArgs g) {
+  __shared__ UpShared sh;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int pairs = g.T * g.k;
+
+  for (int t = wave; t < g.T; t += kUpWaves) {
+    int e;
+    uint32_t key, top;
+    topk_wave<V>(g.logits + static_cast<size_t>(t) * g.E, g.E, g.k, lane, e, key, top);
+    if (lane < g.k) sh.idx[t * g.k + lane] = e;
+    if (blockIdx.x == 0) {  // gate weights: softmax over the chosen logits in fp64
+      double ex = 0.0;
+      if (lane < g.k) ex = exp(static_cast<double>(key_logit(key)) - static_cast<double>(key_logit(top)));
+      const double sum = group_sum16_f64<kWave>(ex);
+      if (lane < g.k) {
+        g.idx[t * g.k + lane] = e;
+        g.w[t * g.k + lane] = static_cast<float>(ex / sum);
+      }
+    }
+  }
+  for (int e = tid; e < g.E; e += kUpThreads) sh.count[e] = 0;
+  __syncthreads();
+  for (int p = tid; p < pairs; p += kUpThreads) atomicAdd(&sh.count[sh.idx[p]], 1);
+  __syncthreads();
+  if (wave == 0) {
+    int off = 0, it = 0;
+    for (int e0 = 0; e0 < g.E; e0 += kWave) {
+      const int e = e0 + lane;
+      const int c = e < g.E ? sh.count[e] : 0;
+      const int n = (c + kRowsPerTile - 1) / kRowsPerTile;
+      const int o = off + wave_incl_scan(c, lane) - c;
+      const int i0 = it + wave_incl_scan(n, lane) - n;
+      if (e < g.E) sh.offset[e] = o;
+      for (int i = 0; i < n; ++i) sh.item[i0 + i] = e | (i << 16);
+      off = __builtin_amdgcn_readlane(o + c, kWave - 1);
+      it = __builtin_amdgcn_readlane(i0 + n, kWave - 1);
+    }
+    if (lane == 0) sh.items = it;
+  }
+  __syncthreads();
+  for (int p = tid; p < pairs; p += kUpThreads) {
+    const int e = sh.idx[p];
+    int rank = 0;
+    for (int o = 0; o < p; ++o) rank += sh.idx[o] == e ? 1 : 0;
+    sh.order[sh.offset[e] + rank] = p;
+  }
+  __syncthreads();
+
+  using S = Step<ACT, F8>;
+  const int r = lane & 15, grp = lane >> 4;
+  const int n_tiles = g.I / kRowsPerTile;
+  const int steps = (g.H + S::kCols - 1) / S::kCols;
+  const int nbK = scale_blocks(g.H), nbN = scale_blocks(2 * g.I);
+  const size_t row_bytes = static_cast<size_t>(g.H) * (F8 ? 1 : 2);
+  const int work = sh.items * n_tiles;
+  int turn = 0;
+  for (int i = blockIdx.x; i < work; i += gridDim.x, turn ^= 1) {
+    const int it = sh.item[i / n_tiles];
+    const int n0 = (i % n_tiles) * kRowsPerTile;
+    const int e = __builtin_amdgcn_readfirstlane(it & 0xffff), first = (it >> 16) * kRowsPerTile;
+    const int have = sh.count[e] - first, off = sh.offset[e] + first;
+    const unsigned char* gate_row = static_cast<const unsigned char*>(g.w_up) +
+                                    (static_cast<size_t>(e) * 2 * g.I + n0 + r) * row_bytes;
+    const unsigned char* up_row = gate_row + g.I * row_bytes;
+    const int my_pair = sh.order[off + min(r, have - 1)];
+    const uint16_t* tok = static_cast<const uint16_t*>(g.x) + static_cast<size_t>(my_pair / g.k) * g.H;
+    const float* s_gate = g.s_up + (static_cast<size_t>(e) * nbN + n0 / kScaleBlock) * nbK;
+    const float* s_upr = g.s_up + (static_cast<size_t>(e) * nbN + (g.I + n0) / kScaleBlock) * nbK;
+
+    v4f gate = {0, 0, 0, 0}, up = {0, 0, 0, 0};
+    constexpr int D = F8 ? 2 : 4;  // steps in flight
+    for (int kb0 = wave; kb0 < steps; kb0 += kUpWaves * D) {
+      typename S::Rows a[D], b[D];
+      typename S::Cols c[D];
+      float sg[D], su[D];
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const int kb = kb0 + d * kUpWaves;
+        S::load_rows(a[d], gate_row, kb, grp, g.H);
+        S::load_rows(b[d], up_row, kb, grp, g.H);
+        S::load_cols(c[d], tok, kb, grp, g.H);
+        if constexpr (F8) {
+          sg[d] = kb < steps ? s_gate[kb] : 0.0f;
+          su[d] = kb < steps ? s_upr[kb] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const v4f pg = S::product(a[d], c[d]), pu = S::product(b[d], c[d]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if constexpr (F8) {
+            gate[q] = fmaf(pg[q], sg[d], gate[q]);
+            up[q] = fmaf(pu[q], su[d], up[q]);
+          } else {
+            gate[q] += pg[q];
+            up[q] += pu[q];
+          }
+        }
+      }
+    }
+    sh.part[turn][wave][0][lane] = make_float4(gate[0], gate[1], gate[2], gate[3]);
+    sh.part[turn][wave][1][lane] = make_float4(up[0], up[1], up[2], up[3]);
+    __syncthreads();
+    // thread tid sums value tid % 4 of lane tid / 4
+    const int c = (tid >> 2) & 15, n = (tid >> 6) * 4 + (tid & 3);
+    float zg = 0.0f, zu = 0.0f;
+#pragma unroll
+    for (int wv = 0; wv < kUpWaves; ++wv) {
+      zg += reinterpret_cast<const float*>(sh.part[turn][wv][0])[tid];
+      zu += reinterpret_cast<const float*>(sh.part[turn][wv][1])[tid];
+    }
+    if (c < have) {
+      const float h = zg / (1.0f + expf(-zg)) * zu;
+      static_cast<uint16_t*>(g.h)[static_cast<size_t>(sh.order[off + c]) * g.I + n0 + n] =
+          static_cast<uint16_t>(pack2<ACT>(h, 0.0f));
+    }
+  }
+}
+
+// ---- launch 2: down product and weighted combine ------------------------------
+
+template <int TT>
+struct DownShared {
+  int idx[kMaxPairs];
+  float w[kMaxPairs];
+  int flag[kMaxE];
+  int active[kMaxPairs];
+  int n_active;
+  float4 part[kDownWaves][TT][kWave];
+};
+
+// Each block owns 16 columns of the output for every token (TT groups of 16
+// tokens: column c of a group's instruction is token c), its waves contiguous
+// shares of the (expert, step of K) sequence.
+template <int ACT, bool F8, int TT>
+__global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs g) {
+  __shared__ DownShared<TT> sh;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int pairs = g.T * g.k;
+  for (int e = tid; e < g.E; e += kDownThreads) sh.flag[e] = 0;
+  __syncthreads();
+  for (int p = tid; p < pairs; p += kDownThreads) {
+    const int e = min(max(g.idx[p], 0), g.E - 1);
+    sh.idx[p] = e;
+    sh.w[p] = g.w[p];
+    sh.flag[e] = 1;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    int n = 0;
+    for (int e0 = 0; e0 < g.E; e0 += kWave) {
+      const int e = e0 + lane;
+      const bool on = e < g.E && sh.flag[e] != 0;
+      const uint64_t m = ballot(on);
+      if (on) sh.active[n + __builtin_popcountll(m & lanemask_lt(lane))] = e;
+      n += __builtin_popcountll(m);
+    }
+    if (lane == 0) sh.n_active = n;
+  }
+  __syncthreads();
+
+  using S = Step<ACT, F8>;
+  const int r = lane & 15, grp = lane >> 4;
+  const int n0 = blockIdx.x * kRowsPerTile;
+  const int steps = (g.I + S::kCols - 1) / S::kCols;
+  const int nbK = scale_blocks(g.I), nbN = scale_blocks(g.H);
+  const size_t row_bytes = static_cast<size_t>(g.I) * (F8 ? 1 : 2);
+  const int total = sh.n_active * steps;
+  int q = total / kDownWaves * wave + min(wave, total % kDownWaves);
+  const int q_end = q + total / kDownWaves + (wave < total % kDownWaves ? 1 : 0);
+
+  v4f acc[TT];
+#pragma unroll
+  for (int u = 0; u < TT; ++u) acc[u] = v4f{0, 0, 0, 0};
+  while (q < q_end) {
+    const int ei = q / steps, k0 = q % steps, k1 = min(steps, k0 + q_end - q);
+    q += k1 - k0;
+    const int e = __builtin_amdgcn_readfirstlane(sh.active[ei]);
+    const unsigned char* row = static_cast<const unsigned char*>(g.w_down) +
+                               (static_cast<size_t>(e) * g.H + n0 + r) * row_bytes;
+    const float* s_row = g.s_down + (static_cast<size_t>(e) * nbN + n0 / kScaleBlock) * nbK;
+    const uint16_t* tok[TT];
+    float wt[TT];
+    bool on[TT], any[TT];
+#pragma unroll
+    for (int u = 0; u < TT; ++u) {
+      const int t = u * kRowsPerTile + r;
+      int pair = -1;
+      if (t < g.T)
+        for (int j = 0; j < g.k; ++j)
+          if (sh.idx[t * g.k + j] == e) pair = t * g.k + j;
+      on[u] = pair >= 0;
+      any[u] = ballot(on[u]) != 0;
+      wt[u] = on[u] ? sh.w[pair] : 0.0f;
+      tok[u] = static_cast<const uint16_t*>(g.h) + static_cast<size_t>(on[u] ? pair : 0) * g.I;
+    }
+    constexpr int D = TT == 1 ? 4 : 2;  // steps in flight
+    for (int kb0 = k0; kb0 < k1; kb0 += D) {
+      typename S::Rows a[D];
+      float s[D];
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const int kb = kb0 + d;
+        S::load_rows(a[d], row, kb, grp, kb < k1 ? g.I : 0);
+        if constexpr (F8) s[d] = s_row[min(kb, nbK - 1)];
+        else s[d] = 1.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < TT; ++u) {
+        if (!any[u]) continue;
+        typename S::Cols c[D];
+#pragma unroll
+        for (int d = 0; d < D; ++d) S::load_cols(c[d], tok[u], kb0 + d, grp, kb0 + d < k1 ? g.I : 0);
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          const v4f p = S::product(a[d], c[d]);
+          const float f = s[d] * wt[u];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[u][i] = on[u] && kb0 + d < k1 ? fmaf(p[i], f, acc[u][i]) : acc[u][i];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < TT; ++u)
+    sh.part[wave][u][lane] = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
+  __syncthreads();
+  for (int o = tid; o < TT * 256; o += kDownThreads) {
+    const int u = o >> 8, v = o & 255;
+    const int t = u * kRowsPerTile + ((v >> 2) & 15), n = n0 + (v >> 6) * 4 + (v & 3);
+    float z = 0.0f;
+#pragma unroll
+    for (int wv = 0; wv < kDownWaves; ++wv) z += reinterpret_cast<const float*>(sh.part[wv][u])[v];
+    if (t < g.T) {
+      const size_t at = static_cast<size_t>(t) * g.H + n;
+      if (g.out_f32) static_cast<float*>(g.out)[at] = z;
+      else static_cast<uint16_t*>(g.out)[at] = static_cast<uint16_t>(pack2<ACT>(z, 0.0f));
+    }
+  }
+}
+
+template <int ACT, bool F8>
+hipError_t launch(const LayerArgs& g, hipStream_t s) {
+  const int items = (g.T * g.k < g.E * ((g.T + 15) / 16) ? g.T * g.k : g.E * ((g.T + 15) / 16)) * (g.I / kRowsPerTile);
+  const int blocks = items < kUpBlocks ? items : kUpBlocks;
+  if (g.E <= 64) layer_up_kernel<ACT, F8, 1><<<blocks, kUpThreads, 0, s>>>(g);
+  else if (g.E <= 256) layer_up_kernel<ACT, F8, 4><<<blocks, kUpThreads, 0, s>>>(g);
+  else layer_up_kernel<ACT, F8, 16><<<blocks, kUpThreads, 0, s>>>(g);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const int tiles = g.H / kRowsPerTile;
+  if (g.T <= 16) layer_down_kernel<ACT, F8, 1><<<tiles, kDownThreads, 0, s>>>(g);
+  else if (g.T <= 32) layer_down_kernel<ACT, F8, 2><<<tiles, kDownThreads, 0, s>>>(g);
+  else layer_down_kernel<ACT, F8, 4><<<tiles, kDownThreads, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t layer_ws_bytes(int T, int k, int I) {
+  return (static_cast<size_t>(T) * k * I * 2 + 255) / 256 * 256;
+}
+
+hipError_t launch_layer_few_tokens(const float* logits, const void* x, const void* w_up, const float* s_up,
+                                   const void* w_down, const float* s_down, int T, int E, int k, int H, int I,
+                                   int32_t* idx, float* w, void* out, void* ws, int act, bool out_f32,
+                                   hipStream_t s) {
+  LayerArgs g{logits, x, w_up, s_up, w_down, s_down, T, E, k, H, I, idx, w, ws, out, out_f32};
+  if (act == 1) return s_up ? launch<1, true>(g, s) : launch<1, false>(g, s);
+  return s_up ? launch<2, true>(g, s) : launch<2, false>(g, s);
+}
+
+}  // namespace moe

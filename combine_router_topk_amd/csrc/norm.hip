@@ -1,0 +1,272 @@
+// Root-mean-square norm of the rows in front of the router, with the
+// residual's addition and 8-bit output, and its gradient.
+//
+// Forward, per row: h = round16(x + r), rstd = 1 / sqrt(mean(h^2) + eps),
+// v = h rstd g; y = round16(v), and 8-bit rows of v (see quant.hpp). The
+// residual stream that is stored is the rounded one, so the norm and its
+// gradient use that.
+// Backward, with n = h rstd and t = dy g: dx = rstd (t - n mean(t n)) + dh,
+// dgamma = sum over rows of dy n.
+//
+// Both are bound by HBM: the forward reads 4 and writes 5 bytes an element
+// (with residual, y and q), the backward reads 6 and writes 2. A row is held
+// in registers by one block, each lane owning 16-byte chunks (8 elements), so
+// every input is read once; a scale block of 128 elements is 16 lanes, one
+// DPP row, and its maximum never leaves the registers.
+#include <algorithm>
+
+#include "device.hpp"
+#include "launch.hpp"
+#include "quant.hpp"
+
+namespace moe {
+
+namespace {
+
+// Rows of one forward launch at most: with 1024 threads a row a launch stays
+// below 2^32 work-items.
+constexpr int kNormRows = 1 << 21;
+
+// Sum over the block in a fixed order: a butterfly in the wave, then the
+// waves' sums in order. Uses one slot of `part` per wave; the caller puts a
+// barrier between two uses of the same slots.
+template <int NT, typename F>
+__device__ __forceinline__ F block_sum(F v, F* part) {
+#pragma unroll
+  for (int off = kWave / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+  if constexpr (NT == kWave) return v;
+  if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = v;
+  __syncthreads();
+  F s = 0;
+#pragma unroll
+  for (int i = 0; i < NT / kWave; ++i) s += part[i];
+  return s;
+}
+
+// One row per block; lane i of the block owns chunks i, i + NT, ... (U of
+// them at most). h_out and y may be x or res themselves: a lane reads its
+// chunks before it writes them, and nobody else does either.
+template <int ACT, int NT, int U>
+__global__ __launch_bounds__(NT) void rms_norm_kernel(
+    const uint4* x, const uint4* res, const uint4* __restrict__ gamma,
+    float eps, int first, int H, uint4* h_out, uint4* y, uint2* __restrict__ q,
+    float* __restrict__ q_scale, float* __restrict__ rstd_out) {
+  __shared__ double part[NT / kWave];
+  const int cpr = H / 8;
+  const size_t row = static_cast<size_t>(first) + blockIdx.x;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 xv[U], rv[U], gv[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = static_cast<int>(threadIdx.x) + u * NT;
+    xv[u] = c < cpr ? x[row * cpr + c] : zero;
+  }
+  if (res != nullptr) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = static_cast<int>(threadIdx.x) + u * NT;
+      rv[u] = c < cpr ? res[row * cpr + c] : zero;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = static_cast<int>(threadIdx.x) + u * NT;
+    gv[u] = c < cpr ? gamma[c] : zero;
+  }
+  float f[U][8];
+  double ss = 0.0;  // in fp32 the squares of large bf16 values overflow
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = static_cast<int>(threadIdx.x) + u * NT;
+    unpack8<ACT>(xv[u], f[u]);
+    if (res != nullptr) {
+      float r[8];
+      unpack8<ACT>(rv[u], r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[u][i] = keep_f32(f[u][i] + r[i]);
+      const uint4 hv = pack8<ACT>(f[u]);
+      if (c < cpr) h_out[row * cpr + c] = hv;
+      unpack8<ACT>(hv, f[u]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fma(static_cast<double>(f[u][i]), static_cast<double>(f[u][i]), ss);
+  }
+  ss = block_sum<NT>(ss, part);
+  const float rstd = static_cast<float>(1.0 / sqrt(ss / H + static_cast<double>(eps)));
+  if (rstd_out != nullptr && threadIdx.x == 0) rstd_out[row] = rstd;
+  const int nb = scale_blocks(H);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = static_cast<int>(threadIdx.x) + u * NT;
+    float g[8];
+    unpack8<ACT>(gv[u], g);
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f[u][i] = keep_f32(f[u][i] * rstd) * g[i];
+      f[u][i] = keep_f32(f[u][i]);
+      top = umax(top, __float_as_uint(f[u][i]) & 0x7fffffffu);
+    }
+    if (y != nullptr && c < cpr) y[row * cpr + c] = pack8<ACT>(f[u]);
+    if (q != nullptr) {
+      if (c >= cpr) top = 0;  // lanes past the row take part in the exchange
+      const float s = block_scale(group_max<16>(top));
+      if (c < cpr) {
+        q[row * cpr + c] = quant8(f[u], s);
+        if ((c & 15) == 0) q_scale[row * nb + c / 16] = s;
+      }
+    }
+  }
+}
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ...; the block's sums of dy n per
+// column stay in registers and end as one row of `part_dg`. dx may be dy or
+// dh: a lane writes a chunk after its only read.
+template <int ACT, int NT, int U>
+__global__ __launch_bounds__(NT) void rms_norm_backward_kernel(
+    const uint4* dy, const uint4* dh, const uint4* __restrict__ h,
+    const uint4* __restrict__ gamma, const float* __restrict__ rstd, int T, int H,
+    uint4* dx, float* __restrict__ part_dg) {
+  __shared__ float part[2][NT / kWave];
+  const int cpr = H / 8;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  float g[U][8], dg[U][8];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = static_cast<int>(threadIdx.x) + u * NT;
+    unpack8<ACT>(c < cpr ? gamma[c] : zero, g[u]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dg[u][i] = 0.0f;
+  }
+  int turn = 0;
+  for (int r = blockIdx.x; r < T; r += gridDim.x, turn ^= 1) {
+    const size_t base = static_cast<size_t>(r) * cpr;
+    uint4 dyv[U], hv[U], dhv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = static_cast<int>(threadIdx.x) + u * NT;
+      dyv[u] = c < cpr ? dy[base + c] : zero;
+      hv[u] = c < cpr ? h[base + c] : zero;
+      dhv[u] = (dh != nullptr && c < cpr) ? dh[base + c] : zero;
+    }
+    const float rs = rstd[r];
+    float t[U][8], n[U][8];
+    float dot = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      unpack8<ACT>(dyv[u], t[u]);
+      unpack8<ACT>(hv[u], n[u]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        n[u][i] *= rs;
+        dg[u][i] += t[u][i] * n[u][i];
+        t[u][i] *= g[u][i];
+        dot += t[u][i] * n[u][i];
+      }
+    }
+    dot = block_sum<NT>(dot, part[turn]) / static_cast<float>(H);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = static_cast<int>(threadIdx.x) + u * NT;
+      float d[8];
+      unpack8<ACT>(dhv[u], d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = keep_f32(rs * (t[u][i] - n[u][i] * dot) + d[i]);
+      if (c < cpr) dx[base + c] = pack8<ACT>(d);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = static_cast<int>(threadIdx.x) + u * NT;
+    if (c < cpr) {
+      float4* o = reinterpret_cast<float4*>(part_dg + static_cast<size_t>(blockIdx.x) * H + c * 8);
+      o[0] = make_float4(dg[u][0], dg[u][1], dg[u][2], dg[u][3]);
+      o[1] = make_float4(dg[u][4], dg[u][5], dg[u][6], dg[u][7]);
+    }
+  }
+}
+
+// dgamma[c] = sum over the blocks' rows, in a fixed order: 16 segments of
+// rows, one per wave, met in LDS. One block per 64 columns.
+__global__ __launch_bounds__(1024) void dgamma_sum_kernel(const float* __restrict__ part_dg, int rows,
+                                                          int H, float* __restrict__ dgamma) {
+  __shared__ float part[16][kWave];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int c = blockIdx.x * kWave + lane;
+  const int seg = (rows + 15) / 16;
+  const int lo = wave * seg, hi = min(rows, lo + seg);
+  float s = 0.0f;
+  if (c < H) {
+#pragma unroll 8
+    for (int r = lo; r < hi; ++r) s += part_dg[static_cast<size_t>(r) * H + c];
+  }
+  part[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < H) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += part[i][lane];
+    dgamma[c] = t;
+  }
+}
+
+// Calls launch(NT, U) as compile-time values for a row of `chunks` chunks.
+template <typename F>
+void by_row(int chunks, F&& launch) {
+  using std::integral_constant;
+#define MOE_NORM_CASE(NT, U) \
+  if (chunks <= NT * U) return launch(integral_constant<int, NT>{}, integral_constant<int, U>{})
+  MOE_NORM_CASE(64, 1);
+  MOE_NORM_CASE(128, 1);
+  MOE_NORM_CASE(256, 1);
+  MOE_NORM_CASE(256, 2);
+  MOE_NORM_CASE(512, 2);
+  MOE_NORM_CASE(1024, 2);
+#undef MOE_NORM_CASE
+}
+
+template <typename F>
+void by_act(int act, F&& launch) {
+  if (act == 1) launch(std::integral_constant<int, 1>{});
+  else launch(std::integral_constant<int, 2>{});
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const void* x, const void* residual, const void* gamma, float eps, void* h,
+                           void* y, void* q, float* q_scale, float* rstd, int T, int H, int act,
+                           hipStream_t s) {
+  by_act(act, [&](auto A) {
+    by_row(H / 8, [&](auto NT, auto U) {
+      for (int first = 0; first < T; first += kNormRows)
+        rms_norm_kernel<A, NT, U><<<std::min(T - first, kNormRows), int(NT), 0, s>>>(
+            static_cast<const uint4*>(x), static_cast<const uint4*>(residual),
+            static_cast<const uint4*>(gamma), eps, first, H, static_cast<uint4*>(h),
+            static_cast<uint4*>(y), static_cast<uint2*>(q), q_scale, rstd);
+    });
+  });
+  return hipGetLastError();
+}
+
+int rms_norm_backward_blocks(int T) { return T < 1024 ? T : 1024; }
+
+hipError_t launch_rms_norm_backward(const void* dy, const void* dh, const void* h, const void* gamma,
+                                    const float* rstd, void* dx, float* dgamma, float* ws, int T, int H,
+                                    int act, hipStream_t s) {
+  const int blocks = rms_norm_backward_blocks(T);
+  if (blocks > 0) {
+    by_act(act, [&](auto A) {
+      by_row(H / 8, [&](auto NT, auto U) {
+        rms_norm_backward_kernel<A, NT, U><<<blocks, int(NT), 0, s>>>(
+            static_cast<const uint4*>(dy), static_cast<const uint4*>(dh), static_cast<const uint4*>(h),
+            static_cast<const uint4*>(gamma), rstd, T, H, static_cast<uint4*>(dx), ws);
+      });
+    });
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  dgamma_sum_kernel<<<(H + kWave - 1) / kWave, 1024, 0, s>>>(ws, blocks, H, dgamma);
+  return hipGetLastError();
+}
+
+}  // namespace moe

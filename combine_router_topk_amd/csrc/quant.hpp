@@ -1,0 +1,83 @@
+// 8-bit rows: e4m3 codes with one fp32 scale for each block of 128 columns.
+// s = max(amax, 2^-100) / 448, code = v / s rounded to nearest even, so a
+// block's largest value takes the largest code. 2^-100 keeps s and v / s
+// ordinary numbers in a block of zeros. A block that holds an infinity or a
+// NaN takes s = NaN: every value of it is NaN.
+#pragma once
+
+#include <type_traits>
+
+#include "device.hpp"
+
+namespace moe {
+
+constexpr int kScaleBlock = 128;
+constexpr float kE4m3Max = 448.0f;
+
+__host__ __device__ constexpr int scale_blocks(int cols) { return (cols + kScaleBlock - 1) / kScaleBlock; }
+
+// The scale of a block from the largest magnitude in it, as bits: among bits
+// without the sign every NaN is above infinity, and that above every number.
+__device__ __forceinline__ float block_scale(uint32_t amax_bits) {
+  if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
+  const float amax = fmaxf(__uint_as_float(amax_bits), 0x1p-100f);
+  return amax / kE4m3Max;
+}
+
+// v / s in e4m3's range: v / s is at most 448 but for the quotient's rounding.
+__device__ __forceinline__ float scaled_for_code(float v, float s) {
+  return fminf(fmaxf(v / s, -kE4m3Max), kE4m3Max);
+}
+
+// Two values in the activation format, the first in the low half; one
+// conversion for both in bf16.
+template <int ACT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (ACT == 1) {
+    return f32_to_f16(a) | (f32_to_f16(b) << 16);
+  } else {
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    const v2bf v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+}
+
+// 4 values as 4 codes, the first in the low byte.
+__device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d, float s) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(scaled_for_code(a, s), scaled_for_code(b, s), 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(scaled_for_code(c, s), scaled_for_code(d, s), w, true);
+  return static_cast<uint32_t>(w);
+}
+
+__device__ __forceinline__ uint2 quant8(const float (&f)[8], float s) {
+  return make_uint2(quant4(f[0], f[1], f[2], f[3], s), quant4(f[4], f[5], f[6], f[7], s));
+}
+
+// 4 e4m3 codes as 4 values of the activation format (1: fp16, 2: bf16); every
+// e4m3 number is one of either.
+template <int ACT>
+__device__ __forceinline__ uint2 widen4(uint32_t codes) {
+  const int c = static_cast<int>(codes);
+  if constexpr (ACT == 1)
+    return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.0f, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.0f, true)));
+  else
+    return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true)));
+}
+
+// c += a b for 16 x 32 by 32 x 16 values in 16 bits: lane (r, g) = (lane % 16,
+// lane / 16) holds 8 values of row r of each operand, the same columns of
+// both, and gets rows 4 g .. 4 g + 3 of column r.
+typedef float v4f __attribute__((ext_vector_type(4)));
+template <int ACT>
+__device__ __forceinline__ v4f mfma16(const uint4& a, const uint4& b, const v4f& c) {
+  typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+  typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+  if constexpr (ACT == 1)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0, 0);
+}
+
+}  // namespace moe

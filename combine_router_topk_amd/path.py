@@ -240,3 +240,79 @@ def allocate_split(b: Buffers) -> Split:
 def token_balanced_split(b: Buffers, sp: Split, stream=None) -> None:
     B.moe_token_balanced_split(b.p, b.idx, b.counts, b.pos, b.expert_offsets, b.rep, b.maxrep,
                                sp.gpu_of_pair, sp.active, sp.tokens, stream)
+
+
+@dataclass
+class ExpertWeights:
+    """The experts' weights in 8 bits: w_up [E, 2 I, H] (gate rows first) and
+    w_down [E, H, I] in float8_e4m3fn, with one fp32 scale for each block of
+    128 x 128 (s_up, s_down); or both in the activation format without scales,
+    for the layer of a few tokens."""
+    I: int
+    w_up: torch.Tensor
+    s_up: torch.Tensor | None
+    w_down: torch.Tensor
+    s_down: torch.Tensor | None
+
+
+@dataclass
+class Layer:
+    """Buffers of the layer around the routing: the normed token rows in 8
+    bits, the experts' inner rows in 8 bits, 1 / rms of each token."""
+    I: int
+    xq: torch.Tensor
+    xq_scale: torch.Tensor
+    rstd: torch.Tensor
+    hq: torch.Tensor
+    hq_scale: torch.Tensor
+
+
+def allocate_layer(b: Buffers, I: int) -> Layer:
+    p, dev = b.p, b.idx.device
+    n, f32 = p.T * p.k, dict(dtype=torch.float32, device=dev)
+    return Layer(I=I, xq=torch.empty(p.T, p.H, dtype=B.E4M3, device=dev),
+                 xq_scale=torch.empty(p.T, B.scale_blocks(p.H), **f32),
+                 rstd=torch.empty(p.T, **f32), hq=torch.empty(n, I, dtype=B.E4M3, device=dev),
+                 hq_scale=torch.empty(n, B.scale_blocks(I), **f32))
+
+
+def norm(b: Buffers, l: Layer, x: torch.Tensor, residual: torch.Tensor | None, gamma: torch.Tensor,
+         eps: float = 1e-6, h: torch.Tensor | None = None, stream=None) -> None:
+    """The rows the router scores (b.x) and the experts take (l.xq) from the
+    layer's input x and the residual stream, which becomes h."""
+    B.moe_rms_norm(b.p, x, residual, gamma, eps, h, b.x, l.xq, l.xq_scale, l.rstd, stream)
+
+
+def expert_gate_up(b: Buffers, l: Layer, w: ExpertWeights, stream=None) -> None:
+    """The experts' inner rows, straight from the token rows (no dispatch)."""
+    B.moe_expert_gemm_swiglu(b.p, b.p.H, l.I, l.xq, l.xq_scale, b.src, w.w_up, w.s_up, b.counts,
+                             b.expert_offsets, l.hq, l.hq_scale, stream)
+
+
+def expert_down(b: Buffers, l: Layer, w: ExpertWeights, stream=None) -> None:
+    """The experts' outputs in send order (what standin writes otherwise)."""
+    p = b.p
+    if p.flags & B.MOE_FLAG_OUT_F32:  # y stays in the activation format
+        p = B.make_problem(p.T, p.E, p.k, p.H, p.R, p.act_dtype, p.flags & ~B.MOE_FLAG_OUT_F32)
+    B.moe_expert_gemm(p, l.I, p.H, l.hq, l.hq_scale, None, w.w_down, w.s_down, b.counts,
+                      b.expert_offsets, b.y, stream)
+
+
+def run_layer(b: Buffers, l: Layer, w: ExpertWeights, stream=None) -> None:
+    """Routing, the experts' products and the combine, from b.logits and l's
+    8-bit rows to b.out."""
+    route_assign_layout(b, stream)
+    expert_gate_up(b, l, w, stream)
+    expert_down(b, l, w, stream)
+    combine(b, stream)
+
+
+def layer_few_tokens(b: Buffers, w: ExpertWeights, ws: torch.Tensor, stream=None) -> None:
+    """The same layer for a few tokens in two launches, from b.logits and the
+    16-bit rows b.x to b.out; `ws` has layer_workspace(b, I) bytes."""
+    B.moe_layer_few_tokens(b.p, w.I, b.logits, b.x, w.w_up, w.s_up, w.w_down, w.s_down, b.idx, b.w,
+                           b.out, ws, stream)
+
+
+def layer_workspace(b: Buffers, I: int) -> torch.Tensor:
+    return torch.empty(B.moe_layer_workspace_bytes(b.p, I), dtype=torch.uint8, device=b.idx.device)

@@ -6,7 +6,9 @@
  * and the weighted combine; around them, single-send dispatch (one row per
  * token and destination rank) with its receiver fan-out, the backward of the
  * combine and the dispatch, routing statistics, and token-balanced replica
- * routing as the greedy's baseline.
+ * routing as the greedy's baseline; and the layer around the routing: the
+ * norm that makes its rows with its gradient, the experts' products in
+ * block-scaled 8-bit floating point, and the whole layer for a few tokens.
  *
  * Sources (web pages on MoE dispatch and combine):
  *   [METRO]  "METRO AllGather vs AllToAll for MoE decode".
@@ -77,6 +79,10 @@ enum {
  * work-items. */
 enum { MOE_MAX_E = 1024, MOE_MAX_K = 16, MOE_MAX_R = 1024, MOE_MAX_REP = 16,
        MOE_MAX_ROWS = (1 << 24) - 1 };
+
+/* 8-bit rows: the columns one scale covers, the widest row of the norm, and
+ * the most tokens of moe_layer_few_tokens. */
+enum { MOE_SCALE_BLOCK = 128, MOE_MAX_NORM_H = 16384, MOE_MAX_FEW_TOKENS = 64 };
 
 /* One routing problem.
  *   T  tokens, T >= 0, T*k <= MOE_MAX_ROWS (2^24 - 1)
@@ -416,6 +422,138 @@ moe_status moe_token_balanced_split(const moe_problem* p, const int32_t* idx,
                                     const int32_t* expert_offsets, const int32_t* rep,
                                     int32_t maxrep, int32_t* gpu_of_pair, int32_t* active,
                                     int32_t* tokens, void* stream);
+
+/* ---- the layer around the routing ------------------------------------------
+ *
+ * 8-bit rows hold e4m3 codes (the OCP format: largest value 448, no
+ * infinities) with one fp32 scale for each block of 128 columns (the last
+ * block may be shorter): a value is its code times its block's scale. For a
+ * block of values v with the largest magnitude amax,
+ *   scale = max(amax, 2^-100) / 448,  code = v / scale rounded to nearest even.
+ * A block that holds an infinity or a NaN takes a NaN scale: all its values
+ * are NaN. Rows of C columns have ceil(C / 128) scales.
+ * Weight matrices in 8 bits are [rows, C] codes with one scale for each block
+ * of 128 x 128, [ceil(rows / 128), ceil(C / 128)]; which scales they hold is
+ * the caller's choice (any fp32 number).                                     */
+
+/* Root-mean-square norm of the activation rows, with the residual's addition
+ * and 8-bit output: what makes the rows that the router scores and the
+ * dispatch sends ([METRO] section "METRO AllGather vs AllToAll changes the
+ * routing information" starts from them).
+ *   h[t]    = round16(x[t] + residual[t])           (x[t] without residual)
+ *   rstd[t] = 1 / sqrt(mean over H of h[t]^2 + eps)
+ *   v       = h[t] * rstd[t] * gamma, in fp32
+ *   y[t]    = round16(v),  (q[t], q_scale[t]) = 8-bit row of v
+ * H is at most MOE_MAX_NORM_H (MOE_ERR_UNSUPPORTED); eps finite and >= 0.
+ *   x         16-bit [T, H] (read)
+ *   residual  16-bit [T, H] (read) or NULL
+ *   gamma     16-bit [H] (read)
+ *   h         16-bit [T, H] (write) with a residual, NULL without; may be x
+ *             or residual itself
+ *   y         16-bit [T, H] (write), or NULL to skip; may be x or residual
+ *             itself (and then not h)
+ *   q, q_scale  codes [T, H], 8-byte aligned, and f32 [T, ceil(H/128)]
+ *             (write), or both NULL to skip
+ *   rstd      f32 [T] (write), or NULL to skip
+ * At least one of y and q must be given when T > 0.                          */
+moe_status moe_rms_norm(const moe_problem* p, const void* x, const void* residual,
+                        const void* gamma, float eps, void* h, void* y, void* q, float* q_scale,
+                        float* rstd, void* stream);
+
+/* Bytes of device workspace that moe_rms_norm_backward needs (0 for T = 0).
+ * Host only.                                                                 */
+moe_status moe_rms_norm_workspace_bytes(const moe_problem* p, size_t* bytes);
+
+/* Backward of the norm. With dy the gradient of y (or of the values of q, the
+ * rounding passed through) and dh the one that reaches h along the residual
+ * stream, n = h[t] * rstd[t], u = dy[t] * gamma:
+ *   dx[t]  = round16(rstd[t] * (u - n * mean over H of (u * n)) + dh[t])
+ *   dgamma = sum over t of dy[t] * n, in fp32
+ * dx is the gradient of x and of the residual alike. The sums' order depends
+ * on the sizes alone, so results repeat bit for bit.
+ *   dy, h   16-bit [T, H] (read); h from the forward (x without residual)
+ *   dh      16-bit [T, H] (read) or NULL (no gradient along the residual)
+ *   gamma   16-bit [H] (read)      rstd  f32 [T] (read), from the forward
+ *   dx      16-bit [T, H] (write); may be dy or dh itself
+ *   dgamma  f32 [H] (write; zeros for T = 0)
+ *   ws      workspace of at least moe_rms_norm_workspace_bytes() bytes, 256-byte
+ *           aligned (may be NULL for T = 0)                                  */
+moe_status moe_rms_norm_backward(const moe_problem* p, const void* dy, const void* dh,
+                                 const void* h, const void* gamma, const float* rstd, void* dx,
+                                 float* dgamma, void* ws, size_t ws_bytes, void* stream);
+
+/* Experts' products over the routed rows, in 8 bits:
+ *   y[r, n] = sum over k of a[r', k] * w[e, n, k]
+ * for every row r of expert e's segment [expert_offsets[e], + counts[e]), a
+ * and w being the values that the codes and scales stand for. Each block of
+ * 128 products is summed by the matrix cores, the blocks with their scales in
+ * fp32; y is rounded once to the activation format, or written as fp32 with
+ * MOE_FLAG_OUT_F32.
+ *   src NULL:  r' = r, a has T*k rows in send order
+ *   src given: r' = src[r] / k, a has T rows in token order (the row dispatch
+ *              happens in the product's loads)
+ * Takes the place of moe_expert_standin where weights are at hand ([METRO]
+ * section "Add the expert-weight traffic term": the weights of the activated
+ * experts are what a decode batch reads). The gradient of a is the same
+ * product with the weights and their scales transposed.
+ *   K   columns of a and w, a multiple of 16     N  rows of w, a multiple of 8
+ *   a, a_scale      codes [rows, K], f32 [rows, ceil(K/128)] (read)
+ *   src             i32 [T*k] (read) from moe_layout, or NULL
+ *   w, w_scale      codes [E, N, K], f32 [E, ceil(N/128), ceil(K/128)] (read)
+ *   counts          i32 [E] (read) from moe_route
+ *   expert_offsets  i32 [E] (read) from moe_layout
+ *   y               [T*k, N] in the activation format or fp32 (write)
+ * Codes are 16-byte aligned. Rows in no segment are left untouched; a src
+ * outside [0, T*k) is clamped into it. H of the problem is not used. Sizes
+ * whose offsets would not fit the kernel's 32 bits (an expert's or the rows'
+ * codes of 64 GiB or more) return MOE_ERR_UNSUPPORTED.                       */
+moe_status moe_expert_gemm(const moe_problem* p, int32_t K, int32_t N, const void* a,
+                           const float* a_scale, const int32_t* src, const void* w,
+                           const float* w_scale, const int32_t* counts,
+                           const int32_t* expert_offsets, void* y, void* stream);
+
+/* The gate and up products of the experts with SwiGLU and 8-bit output, in
+ * one pass: with z = the product above for weights of N = 2 I rows (gate
+ * rows 0 .. I-1, up rows I .. 2I-1),
+ *   v[r, i] = z[r, i] / (1 + exp(-z[r, i])) * z[r, I + i], in fp32
+ *   (q[r], q_scale[r]) = 8-bit row of v[r]
+ *   I   a multiple of 16; w [E, 2I, K], w_scale [E, ceil(2I/128), ceil(K/128)]
+ *   q, q_scale  codes [T*k, I], 16-byte aligned, f32 [T*k, ceil(I/128)] (write)
+ * The other arguments are those of moe_expert_gemm; act_dtype and the output
+ * flag are not used.                                                         */
+moe_status moe_expert_gemm_swiglu(const moe_problem* p, int32_t K, int32_t I, const void* a,
+                                  const float* a_scale, const int32_t* src, const void* w,
+                                  const float* w_scale, const int32_t* counts,
+                                  const int32_t* expert_offsets, void* q, float* q_scale,
+                                  void* stream);
+
+/* Bytes of device workspace that moe_layer_few_tokens needs. Host only.      */
+moe_status moe_layer_workspace_bytes(const moe_problem* p, int32_t I, size_t* bytes);
+
+/* A whole mixture-of-experts layer for a few tokens (T <= 64) in two
+ * launches: top-k and gate weights as moe_route gives them, then
+ *   h[t, j] = round16(silu(g) * u),  (g; u) = w_up[e] x[t], e = idx[t, j]
+ *   out[t]  = sum over j of w[t, j] * (w_down[e] h[t, j]), in fp32, rounded
+ *             once to the activation format (fp32 with MOE_FLAG_OUT_F32)
+ * Nothing is dispatched: a decode step reads the chosen experts' weights and
+ * little else ([METRO] section "Add the expert-weight traffic term").
+ * Activations stay in 16 bits.
+ *   H and I are multiples of 16; T > MOE_MAX_FEW_TOKENS returns
+ *   MOE_ERR_UNSUPPORTED. R is not used.
+ *   logits  f32 [T, E] (read)       x  16-bit [T, H] (read)
+ *   w_up    [E, 2I, H] (read), gate rows 0 .. I-1, up rows I .. 2I-1
+ *   w_down  [E, H, I] (read)
+ *   s_up, s_down  f32 [E, ceil(2I/128), ceil(H/128)] and
+ *           [E, ceil(H/128), ceil(I/128)] (read) with e4m3 weights; both NULL
+ *           with weights in the activation format
+ *   idx, w  i32, f32 [T, k] (write)
+ *   out     [T, H] in the activation format or fp32 (write); must not overlap x
+ *   ws      workspace of at least moe_layer_workspace_bytes() bytes, 256-byte
+ *           aligned                                                          */
+moe_status moe_layer_few_tokens(const moe_problem* p, int32_t I, const float* logits, const void* x,
+                                const void* w_up, const float* s_up, const void* w_down,
+                                const float* s_down, int32_t* idx, float* w, void* out, void* ws,
+                                size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

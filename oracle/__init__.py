@@ -31,3 +31,4 @@ from .eplb import (optimal_max_activated, replica_share_index,  # noqa: F401
                    split_tokens_per_gpu, token_balanced_split)
 from .stats import (coselection, dirichlet_alpha, gini, routing_stats,  # noqa: F401
                     send_counts, source_ranks, top_pair_coverage)
+from . import layer  # noqa: F401

@@ -9,7 +9,10 @@
  *                           allocation-free plan against the separate calls,
  *                           the single-send layout, dispatch and fan-out,
  *                           the two backward calls, the routing statistics
- *                           and the token-balanced split.
+ *                           and the token-balanced split;
+ *   moe_c_abi_check_layer() the layer around the routing: the norm and its
+ *                           gradient, the experts' products in 8 bits, the
+ *                           whole layer for a few tokens.
  * Each returns 0 when every check holds and prints the first failure
  * otherwise.
  */
@@ -541,6 +544,156 @@ done:
     free(h[i]);
     free(a[i]);
   }
+  hipFree(ws);
+  return rc;
+}
+
+/* value of an e4m3 code that is not NaN */
+static double e4m3_val(uint8_t c) {
+  const int e = (c >> 3) & 15, m = c & 7;
+  const double v = e == 0 ? ldexp(m, -9) : ldexp(8 + m, e - 10);
+  return c & 128 ? -v : v;
+}
+
+int moe_c_abi_check_layer(void) {
+  enum { T = 5, E = 4, K = 2, H = 64, I = 64, N = T * K };
+  enum { L_X, L_R, L_G, L_H, L_Y, L_Q, L_QS, L_RSTD, L_DX, L_DG, L_SRC, L_W, L_WS, L_CNT, L_OFF,
+         L_OUT, L_LOGITS, L_UP16, L_DOWN16, L_IDX, L_GATE, L_COUNT };
+  const size_t sz[L_COUNT] = {2u * T * H, 2u * T * H, 2u * H, 2u * T * H, 2u * T * H, T * H, 4u * T, 4u * T,
+                              2u * T * H, 4u * H, 4u * N, E * 2 * I * H, 4u * E, 4u * E, 4u * E,
+                              2u * N * H, 4u * T * E, 2u * E * 2 * I * H, 2u * E * H * I, 4u * N, 4u * N};
+  void *d[L_COUNT], *h[L_COUNT], *hq = NULL, *hqs = NULL, *ws = NULL;
+  uint8_t got_q[N * I];
+  float got_s[N];
+  size_t norm_ws = 0, layer_ws = 0;
+  int rc = 0;
+  uint32_t seed = 777u;
+  moe_problem p;
+  p.T = T; p.E = E; p.k = K; p.H = H; p.R = 1; p.act_dtype = MOE_BF16; p.flags = 0;
+  for (int i = 0; i < L_COUNT; ++i) d[i] = NULL, h[i] = calloc(1, sz[i]);
+  for (int i = 0; i < L_COUNT; ++i) HIP_OK(hipMalloc(&d[i], sz[i]));
+  HIP_OK(hipMalloc(&hq, N * I));
+  HIP_OK(hipMalloc(&hqs, 4u * N));
+  for (int i = 0; i < T * H; ++i) {
+    ((uint16_t*)h[L_X])[i] = bf16_bits((int)(lcg(&seed) >> 27) - 16);
+    ((uint16_t*)h[L_R])[i] = bf16_bits((int)(lcg(&seed) >> 27) - 15);
+  }
+  for (int i = 0; i < H; ++i) ((uint16_t*)h[L_G])[i] = bf16_bits(8); /* 1 */
+  for (int r = 0; r < N; ++r) ((int32_t*)h[L_SRC])[r] = (r % T) * K + r / T; /* rows by slot, then token */
+  for (int e = 0; e < E; ++e) {
+    ((float*)h[L_WS])[e] = 1.0f;
+    for (int i = 0; i < I; ++i)
+      for (int part = 0; part < 2; ++part) { /* gate and up are the identity, and so is down */
+        ((uint8_t*)h[L_W])[((size_t)e * 2 * I + part * I + i) * H + i] = 0x38;
+        ((uint16_t*)h[L_UP16])[((size_t)e * 2 * I + part * I + i) * H + i] = bf16_bits(8);
+        ((uint16_t*)h[L_DOWN16])[((size_t)e * H + i) * I + i] = bf16_bits(8);
+      }
+  }
+  /* slot 0 of every token is expert 1, slot 1 expert 3 */
+  ((int32_t*)h[L_CNT])[1] = ((int32_t*)h[L_CNT])[3] = T;
+  ((int32_t*)h[L_OFF])[2] = ((int32_t*)h[L_OFF])[3] = T;
+  for (int t = 0; t < T; ++t) {
+    ((float*)h[L_LOGITS])[t * E + 1] = 2.0f;
+    ((float*)h[L_LOGITS])[t * E + 3] = 1.0f;
+  }
+  for (int i = 0; i < L_COUNT; ++i) HIP_OK(hipMemcpy(d[i], h[i], sz[i], hipMemcpyHostToDevice));
+
+  /* 1. the norm: h exact, y and q from the row's own statistics */
+  MOE_OK_OR_FAIL(moe_rms_norm(&p, d[L_X], d[L_R], d[L_G], 1e-5f, d[L_H], d[L_Y], d[L_Q],
+                              (float*)d[L_QS], (float*)d[L_RSTD], NULL));
+  MOE_OK_OR_FAIL(moe_rms_norm_workspace_bytes(&p, &norm_ws));
+  MOE_OK_OR_FAIL(moe_layer_workspace_bytes(&p, I, &layer_ws));
+  HIP_OK(hipMalloc(&ws, norm_ws > layer_ws ? norm_ws : layer_ws));
+  MOE_OK_OR_FAIL(moe_rms_norm_backward(&p, d[L_X], NULL, d[L_H], d[L_G], (const float*)d[L_RSTD],
+                                       d[L_DX], (float*)d[L_DG], ws, norm_ws, NULL));
+  HIP_OK(hipDeviceSynchronize());
+  for (int i = L_H; i <= L_DG; ++i) HIP_OK(hipMemcpy(h[i], d[i], sz[i], hipMemcpyDeviceToHost));
+  for (int t = 0; t < T; ++t) {
+    double ss = 0.0, dot = 0.0, rstd;
+    for (int c = 0; c < H; ++c) {
+      const int i = t * H + c;
+      const double v = bf16_val(((uint16_t*)h[L_X])[i]) + bf16_val(((uint16_t*)h[L_R])[i]);
+      if (bf16_val(((uint16_t*)h[L_H])[i]) != v) FAIL("h[%d] against %g", i, v);
+      ss += v * v;
+    }
+    rstd = 1.0 / sqrt(ss / H + 1e-5);
+    if (fabs(((float*)h[L_RSTD])[t] - rstd) > 1e-6 * rstd) FAIL("rstd[%d]", t);
+    for (int c = 0; c < H; ++c)
+      dot += bf16_val(((uint16_t*)h[L_X])[t * H + c]) * bf16_val(((uint16_t*)h[L_H])[t * H + c]) * rstd / H;
+    for (int c = 0; c < H; ++c) {
+      const int i = t * H + c;
+      const double n = bf16_val(((uint16_t*)h[L_H])[i]) * rstd, s = ((float*)h[L_QS])[t];
+      const double dx = rstd * (bf16_val(((uint16_t*)h[L_X])[i]) - n * dot);
+      if (fabs(bf16_val(((uint16_t*)h[L_Y])[i]) - n) > fabs(n) / 256 + 1e-5) FAIL("y[%d]", i);
+      /* half a step of 3 mantissa bits, or of the subnormal codes */
+      if (fabs(e4m3_val(((uint8_t*)h[L_Q])[i]) * s - n) > fabs(n) / 16 + s / 1024 + 1e-5) FAIL("q[%d]", i);
+      if (fabs(bf16_val(((uint16_t*)h[L_DX])[i]) - dx) > fabs(dx) / 256 + 1e-5) FAIL("dx[%d]", i);
+    }
+  }
+  for (int c = 0; c < H; ++c) {
+    double want = 0.0;
+    for (int t = 0; t < T; ++t)
+      want += bf16_val(((uint16_t*)h[L_X])[t * H + c]) * bf16_val(((uint16_t*)h[L_H])[t * H + c]) *
+              (double)((float*)h[L_RSTD])[t];
+    if (fabs(((float*)h[L_DG])[c] - want) > 1e-4) FAIL("dgamma[%d]", c);
+  }
+
+  /* 2. products with identity weights: y is the token's 8-bit row, and the
+     SwiGLU's row is z sigmoid(z) z */
+  MOE_OK_OR_FAIL(moe_expert_gemm_swiglu(&p, H, I, d[L_Q], (const float*)d[L_QS], (const int32_t*)d[L_SRC],
+                                        d[L_W], (const float*)d[L_WS], (const int32_t*)d[L_CNT],
+                                        (const int32_t*)d[L_OFF], hq, (float*)hqs, NULL));
+  MOE_OK_OR_FAIL(moe_expert_gemm(&p, H, 2 * I, d[L_Q], (const float*)d[L_QS], (const int32_t*)d[L_SRC], d[L_W],
+                                 (const float*)d[L_WS], (const int32_t*)d[L_CNT], (const int32_t*)d[L_OFF],
+                                 d[L_UP16], NULL)); /* [N, 2 I] fits there */
+  HIP_OK(hipDeviceSynchronize());
+  HIP_OK(hipMemcpy(got_q, hq, sizeof(got_q), hipMemcpyDeviceToHost));
+  HIP_OK(hipMemcpy(got_s, hqs, sizeof(got_s), hipMemcpyDeviceToHost));
+  {
+    uint16_t* y = (uint16_t*)malloc(2u * N * 2 * I);
+    HIP_OK(hipMemcpy(y, d[L_UP16], 2u * N * 2 * I, hipMemcpyDeviceToHost));
+    HIP_OK(hipMemcpy(d[L_UP16], h[L_UP16], sz[L_UP16], hipMemcpyHostToDevice));
+    for (int r = 0; r < N; ++r)
+      for (int c = 0; c < I; ++c) {
+        const int t = r % T;
+        const double z = e4m3_val(((uint8_t*)h[L_Q])[t * H + c]) * (double)((float*)h[L_QS])[t];
+        const double v = z / (1.0 + exp(-z)) * z, s = got_s[r];
+        const double a = bf16_val(y[(size_t)r * 2 * I + c]), b = bf16_val(y[(size_t)r * 2 * I + I + c]);
+        if (a != b || fabs(a - z) > fabs(z) / 256) FAIL("product row %d column %d: %g, %g against %g", r, c, a, b, z);
+        if (fabs(e4m3_val(got_q[r * I + c]) * s - v) > fabs(v) / 16 + s / 1024 + 1e-5)
+          FAIL("SwiGLU row %d column %d: %g against %g", r, c, e4m3_val(got_q[r * I + c]) * s, v);
+      }
+    free(y);
+  }
+
+  /* 3. the layer with identity weights: the gate weights add up to 1, so out
+     is z sigmoid(z) z of the token's row */
+  MOE_OK_OR_FAIL(moe_layer_few_tokens(&p, I, (const float*)d[L_LOGITS], d[L_Y], d[L_UP16], NULL, d[L_DOWN16],
+                                      NULL, (int32_t*)d[L_IDX], (float*)d[L_GATE], d[L_OUT], ws, layer_ws, NULL));
+  HIP_OK(hipDeviceSynchronize());
+  HIP_OK(hipMemcpy(h[L_IDX], d[L_IDX], sz[L_IDX], hipMemcpyDeviceToHost));
+  HIP_OK(hipMemcpy(h[L_GATE], d[L_GATE], sz[L_GATE], hipMemcpyDeviceToHost));
+  HIP_OK(hipMemcpy(h[L_OUT], d[L_OUT], 2u * T * H, hipMemcpyDeviceToHost));
+  for (int t = 0; t < T; ++t) {
+    const int32_t* idx = (const int32_t*)h[L_IDX] + t * K;
+    const float* gate = (const float*)h[L_GATE] + t * K;
+    if (idx[0] != 1 || idx[1] != 3) FAIL("token %d goes to %d and %d", t, idx[0], idx[1]);
+    if (fabs(gate[0] - 1.0 / (1.0 + exp(-1.0))) > 1e-6 || fabs(gate[0] + gate[1] - 1.0) > 1e-6) FAIL("gate weights");
+    for (int c = 0; c < H; ++c) {
+      const double z = bf16_val(((uint16_t*)h[L_Y])[t * H + c]), v = z / (1.0 + exp(-z)) * z;
+      /* two roundings to bf16 */
+      if (fabs(bf16_val(((uint16_t*)h[L_OUT])[t * H + c]) - v) > fabs(v) / 127 + 1e-5) FAIL("out[%d][%d]", t, c);
+    }
+  }
+  printf("c-abi check (layer) ok: T=%d E=%d k=%d H=%d I=%d\n", T, E, K, H, I);
+
+done:
+  for (int i = 0; i < L_COUNT; ++i) {
+    hipFree(d[i]);
+    free(h[i]);
+  }
+  hipFree(hq);
+  hipFree(hqs);
   hipFree(ws);
   return rc;
 }

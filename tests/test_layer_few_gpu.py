@@ -1,0 +1,173 @@
+"""The whole layer for a few tokens on the GPU against the oracle, and its
+routing against moe_route, bit for bit.
+
+Bounds (u = 2^-24): the gate and up sums are off by at most (H + H / 128 + 8)
+2 u of the sum of their terms' magnitudes (a matrix instruction's additions
+may truncate); that moves h = round16(v) by a step where v lies that near to
+a border, and else not at all. The output's sum adds (I + I / 128 + 24) 2 u a
+pair and one rounding."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from combine_router_topk_amd import binding as B
+from layercheck import (ACTS, U, assert_within, bits16, codes8, dev, f64, host, round_bound, scales)
+from oracle import layer as L
+from pathcheck import say
+
+pytestmark = pytest.mark.gpu
+
+
+def weights(rng, E, rows, cols, act, kind):
+    """(device codes or values, device scales or None, fp64 matrices)"""
+    if kind == "e4m3":
+        c = codes8(rng, (E, rows, cols))
+        s = scales(rng, (E, L.blocks(rows), L.blocks(cols)), 1 / (110 * cols ** 0.5))
+        return dev(c), dev(s), np.stack([L.matrix8(c[e], s[e]) for e in range(E)])
+    b = bits16(rng, (E, rows, cols), act, cols ** -0.5)
+    return dev(b, act), None, oracle.decode16(b, act).astype(np.float64)
+
+
+def run_layer(p, I, logits, x, wu, su, wd, sd, act):
+    out_dt = torch.float32 if p.flags & B.MOE_FLAG_OUT_F32 else dev(x, act).dtype
+    idx = torch.full((p.T + 1, p.k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((p.T + 1, p.k), -7.0, device="cuda")
+    out = torch.full((p.T + 1, p.H), -7.0, dtype=out_dt, device="cuda")
+    ws = torch.full((B.moe_layer_workspace_bytes(p, I),), 255, dtype=torch.uint8, device="cuda")
+    B.moe_layer_few_tokens(p, I, dev(logits), dev(x, act), wu, su, wd, sd, idx, w, out, ws)
+    torch.cuda.synchronize()
+    assert (idx[p.T] == -7).all() and (w[p.T] == -7).all() and (out[p.T] == -7).all()
+    return idx[:p.T], w[:p.T], out[:p.T]
+
+
+def route(p, logits):
+    idx = torch.empty(p.T, p.k, dtype=torch.int32, device="cuda")
+    w = torch.empty(p.T, p.k, device="cuda")
+    counts = torch.empty(p.E, dtype=torch.int32, device="cuda")
+    ws = torch.empty(B.moe_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    B.moe_route(p, dev(logits), idx, w, counts, ws)
+    return idx, w
+
+
+def check_layer(T, E, k, H, I, act, kind, flags=0, logits=None, seed=0):
+    say(f"[case] layer T={T} E={E} k={k} H={H} I={I} act={act} {kind} flags={flags}")
+    rng = np.random.default_rng(seed + T + E + H)
+    p = B.make_problem(T, E, k, H, 1, act, flags)
+    if logits is None:
+        logits = rng.standard_normal((T, E)).astype(np.float32)
+    x = bits16(rng, (T, H), act)
+    wu, su, up = weights(rng, E, 2 * I, H, act, kind)
+    wd, sd, down = weights(rng, E, H, I, act, kind)
+    idx, w, out = run_layer(p, I, logits, x, wu, su, wd, sd, act)
+    ridx, rw = route(p, logits)
+    assert torch.equal(idx, ridx) and torch.equal(w.view(torch.int32), rw.view(torch.int32))
+    i, gw = host(idx), host(w).astype(np.float64)
+    h, v, want = L.moe_layer(x, i, gw, up, down, act)
+    xv = np.abs(oracle.decode16(x, act).astype(np.float64))
+    bound = np.zeros_like(want)
+    hv = np.abs(oracle.decode16(h, act).astype(np.float64))
+    for t in range(T):
+        for j in range(k):
+            e = i[t, j]
+            dz = (H + L.blocks(H) + 8) * 2 * U * (np.abs(up[e]) @ xv[t])
+            z = up[e] @ oracle.decode16(x, act)[t].astype(np.float64)
+            dv = 1.1 * dz[:I] * np.abs(z[I:]) + np.abs(L.silu(z[:I])) * dz[I:] + 1.1 * dz[:I] * dz[I:] \
+                + 8 * U * np.abs(v[t, j])
+            lo, hi = (oracle.decode16(oracle.encode16((v[t, j] + d).astype(np.float32), act), act).astype(np.float64)
+                      for d in (-dv, dv))
+            dh = np.maximum(hi - lo, 0)
+            bound[t] += gw[t, j] * (np.abs(down[e]) @ (dh + (I + L.blocks(I) + 24) * 2 * U * (hv[t, j] + dh)))
+    got = f64(out)
+    if flags & B.MOE_FLAG_OUT_F32:
+        assert_within(got, want, bound + 1e-30, "out")
+    else:
+        assert_within(got, want, bound + round_bound(np.abs(want) + bound, act), "out")
+    return out
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "16 bits"])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 1, 1, 16, 16), (1, 8, 2, 128, 128), (2, 4, 4, 144, 48), (7, 64, 3, 272, 80),
+                                       (16, 65, 8, 256, 144), (17, 12, 2, 160, 64), (33, 5, 5, 400, 32),
+                                       (64, 7, 3, 96, 112)])
+def test_layer(T, E, k, H, I, act, kind):
+    check_layer(T, E, k, H, I, act, kind)
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(3, 300, 16, 64, 32), (64, 1024, 16, 32, 16), (5, 256, 8, 1040, 528),
+                                       (1, 160, 6, 2048, 256)])
+def test_layer_many_experts_and_wide_rows(T, E, k, H, I):
+    check_layer(T, E, k, H, I, B.MOE_BF16, "e4m3")
+
+
+def test_layer_fp32_output():
+    check_layer(9, 8, 2, 144, 80, B.MOE_F16, "e4m3", B.MOE_FLAG_OUT_F32)
+    check_layer(40, 8, 2, 144, 80, B.MOE_BF16, "16 bits", B.MOE_FLAG_OUT_F32)
+
+
+def test_every_token_on_one_expert():
+    T, E = 64, 9
+    logits = np.zeros((T, E), np.float32)
+    logits[:, 5] = 3.0
+    check_layer(T, E, 1, 128, 64, B.MOE_BF16, "e4m3", logits=logits)
+
+
+def test_ties_nan_and_infinite_logits_route_as_the_router_does():
+    rng = np.random.default_rng(3)
+    for E, k in ((16, 5), (100, 7), (256, 8), (1000, 16)):
+        T = 24
+        logits = rng.integers(-2, 3, (T, E)).astype(np.float32)
+        logits[1], logits[2] = 0.0, np.nan
+        logits[3, ::2], logits[4, 3], logits[5, 1] = np.nan, np.inf, -np.inf
+        logits[6] = -0.0
+        logits[7] = -np.inf
+        H, I, act = 32, 16, B.MOE_F16
+        p = B.make_problem(T, E, k, H, 1, act)
+        x = bits16(rng, (T, H), act)
+        wu, su, _ = weights(rng, E, 2 * I, H, act, "e4m3")
+        wd, sd, _ = weights(rng, E, H, I, act, "e4m3")
+        idx, w, out = run_layer(p, I, logits, x, wu, su, wd, sd, act)
+        ridx, rw = route(p, logits)
+        assert torch.equal(idx, ridx), (E, k)
+        assert torch.equal(w.view(torch.int32), rw.view(torch.int32)), (E, k)
+        # a token whose weights are NaN has a NaN output, the others have not
+        nan = torch.isnan(w).any(dim=1)
+        assert torch.isnan(out[nan]).all() and not torch.isnan(out[~nan]).any(), (E, k)
+
+
+def test_non_finite_tokens_stay_their_own():
+    T, E, k, H, I, act = 20, 6, 2, 160, 48, B.MOE_BF16
+    rng = np.random.default_rng(4)
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    x = bits16(rng, (T, H), act)
+    wu, su, _ = weights(rng, E, 2 * I, H, act, "e4m3")
+    wd, sd, _ = weights(rng, E, H, I, act, "e4m3")
+    p = B.make_problem(T, E, k, H, 1, act)
+    _, _, want = run_layer(p, I, logits, x, wu, su, wd, sd, act)
+    x2 = x.copy()
+    x2[3, H - 1], x2[17, 0] = 0x7fc0, 0x7f80  # a NaN, an infinity
+    _, _, got = run_layer(p, I, logits, x2, wu, su, wd, sd, act)
+    rest = [t for t in range(T) if t not in (3, 17)]
+    assert torch.equal(got[rest], want[rest]) and torch.isnan(got[3]).all() and not torch.isfinite(got[17]).all()
+
+
+def test_layer_repeats_bit_for_bit_and_takes_a_stream():
+    T, E, k, H, I, act = 40, 32, 4, 512, 256, B.MOE_BF16
+    rng = np.random.default_rng(6)
+    logits, x = rng.standard_normal((T, E)).astype(np.float32), bits16(rng, (T, H), act)
+    wu, su, _ = weights(rng, E, 2 * I, H, act, "e4m3")
+    wd, sd, _ = weights(rng, E, H, I, act, "e4m3")
+    p = B.make_problem(T, E, k, H, 1, act)
+    first = run_layer(p, I, logits, x, wu, su, wd, sd, act)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        second = run_layer(p, I, logits, x, wu, su, wd, sd, act)
+    for a, b in zip(first, second):
+        assert torch.equal(a, b)
+
+
+def test_no_tokens():
+    p = B.make_problem(0, 8, 2, 64, 1, B.MOE_BF16)
+    B.moe_layer_few_tokens(p, 64, *(None,) * 10)
