@@ -389,33 +389,57 @@ def scale_blocks(cols: int) -> int:
     return -(-cols // MOE_SCALE_BLOCK)
 
 
-def _call(name: str, stream, tensors, args) -> None:
-    """The library's call on the device that all tensors share, on that
-    device's current stream unless one is given."""
-    dev = None
-    for t in tensors:
-        if isinstance(t, torch.Tensor):
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"{name}: tensors on {dev} and on {t.device}")
-    f = getattr(_lib, name)
-    if dev is None or dev.index == torch.cuda.current_device():
-        _check(f(*args, _stream(stream)), name)
-    else:
-        with torch.cuda.device(dev):
-            _check(f(*args, _stream(stream)), name)
+class _Args:
+    """Tensor arguments of one call: each checked as _ptr checks it, and that
+    all live on one device."""
+    __slots__ = ("name", "dev")
+
+    def __init__(self, name: str):
+        self.name, self.dev = name, None
+
+    def __call__(self, t, dtype, numel, name):
+        if t is None:
+            return None
+        dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+        if dev < 0 or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype) \
+                or (numel is not None and t.numel() < numel):
+            _ptr(t, dtype, numel, name)  # raises
+        if dev != self.dev:
+            if self.dev is not None:
+                raise ValueError(f"{self.name}: {name} is on device {dev}, others on {self.dev}")
+            self.dev = dev
+        return t.data_ptr()
+
+    def call(self, f, stream, *args) -> None:
+        """The library's function on the tensors' device, on that device's
+        current stream unless one is given."""
+        if self.dev is None or self.dev == torch.cuda.current_device():
+            _check(f(*args, _raw_stream(stream, self.dev)), self.name)
+        else:
+            with torch.cuda.device(self.dev):
+                _check(f(*args, _raw_stream(stream, self.dev)), self.name)
+
+
+# The current stream's handle without a Stream object around it (2.9 us).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, dev) -> int:
+    if stream is None:
+        if _current_raw_stream is not None and dev is not None:
+            return _current_raw_stream(dev)
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def moe_rms_norm(p: Problem, x, residual, gamma, eps: float, h, y, q, q_scale, rstd, stream=None) -> None:
     """residual and h go together, q and q_scale too (None to leave them out);
     y may be None beside q, rstd too. q holds float8_e4m3fn."""
-    act, n = _TORCH_ACT.get(p.act_dtype), p.T * p.H
-    _call("moe_rms_norm", stream, (x, residual, gamma, h, y, q, q_scale, rstd),
-          (ctypes.byref(p), _ptr(x, act, n, "x"), _ptr(residual, act, n, "residual"),
-           _ptr(gamma, act, p.H, "gamma"), eps, _ptr(h, act, n, "h"), _ptr(y, act, n, "y"),
-           _ptr(q, E4M3, n, "q"), _ptr(q_scale, torch.float32, p.T * scale_blocks(p.H), "q_scale"),
-           _ptr(rstd, torch.float32, p.T, "rstd")))
+    act, T, H = _TORCH_ACT.get(p.act_dtype), p.T, p.H
+    n, a = T * H, _Args("moe_rms_norm")
+    a.call(_lib.moe_rms_norm, stream, ctypes.byref(p), a(x, act, n, "x"), a(residual, act, n, "residual"),
+           a(gamma, act, H, "gamma"), eps, a(h, act, n, "h"), a(y, act, n, "y"), a(q, E4M3, n, "q"),
+           a(q_scale, torch.float32, T * scale_blocks(H), "q_scale"), a(rstd, torch.float32, T, "rstd"))
 
 
 def moe_rms_norm_workspace_bytes(p: Problem) -> int:
@@ -427,44 +451,41 @@ def moe_rms_norm_workspace_bytes(p: Problem) -> int:
 
 def moe_rms_norm_backward(p: Problem, dy, dh, h, gamma, rstd, dx, dgamma, ws, stream=None) -> None:
     """dh may be None (no gradient along the residual stream)."""
-    act, n = _TORCH_ACT.get(p.act_dtype), p.T * p.H
-    _call("moe_rms_norm_backward", stream, (dy, dh, h, gamma, rstd, dx, dgamma, ws),
-          (ctypes.byref(p), _ptr(dy, act, n, "dy"), _ptr(dh, act, n, "dh"), _ptr(h, act, n, "h"),
-           _ptr(gamma, act, p.H, "gamma"), _ptr(rstd, torch.float32, p.T, "rstd"),
-           _ptr(dx, act, n, "dx"), _ptr(dgamma, torch.float32, p.H, "dgamma"),
-           _ptr(ws, None, None, "ws"), _nbytes(ws)))
+    act, T, H = _TORCH_ACT.get(p.act_dtype), p.T, p.H
+    n, a = T * H, _Args("moe_rms_norm_backward")
+    a.call(_lib.moe_rms_norm_backward, stream, ctypes.byref(p), a(dy, act, n, "dy"), a(dh, act, n, "dh"),
+           a(h, act, n, "h"), a(gamma, act, H, "gamma"), a(rstd, torch.float32, T, "rstd"), a(dx, act, n, "dx"),
+           a(dgamma, torch.float32, H, "dgamma"), a(ws, None, None, "ws"), _nbytes(ws))
 
 
-def _gemm_args(p: Problem, K: int, rows: int, a, a_scale, src, w, w_scale, counts, expert_offsets):
+def _gemm_args(arg: _Args, p: Problem, K: int, rows: int, a, a_scale, src, w, w_scale, counts, expert_offsets):
     """The arguments that both experts' products share; `rows` of weights."""
-    n = p.T * p.k
+    n, E = p.T * p.k, p.E
     a_rows = n if src is None else p.T
     nb = scale_blocks(K)
-    return (_ptr(a, E4M3, a_rows * K, "a"), _ptr(a_scale, torch.float32, a_rows * nb, "a_scale"),
-            _ptr(src, torch.int32, n, "src"), _ptr(w, E4M3, p.E * rows * K, "w"),
-            _ptr(w_scale, torch.float32, p.E * scale_blocks(rows) * nb, "w_scale"),
-            _ptr(counts, torch.int32, p.E, "counts"),
-            _ptr(expert_offsets, torch.int32, p.E, "expert_offsets"))
+    return (arg(a, E4M3, a_rows * K, "a"), arg(a_scale, torch.float32, a_rows * nb, "a_scale"),
+            arg(src, torch.int32, n, "src"), arg(w, E4M3, E * rows * K, "w"),
+            arg(w_scale, torch.float32, E * scale_blocks(rows) * nb, "w_scale"),
+            arg(counts, torch.int32, E, "counts"), arg(expert_offsets, torch.int32, E, "expert_offsets"))
 
 
 def moe_expert_gemm(p: Problem, K: int, N: int, a, a_scale, src, w, w_scale, counts, expert_offsets,
                     y, stream=None) -> None:
     """src None: a holds the T k rows in send order; given: the T token rows."""
     out_dt = torch.float32 if p.flags & MOE_FLAG_OUT_F32 else _TORCH_ACT.get(p.act_dtype)
-    _call("moe_expert_gemm", stream, (a, a_scale, src, w, w_scale, counts, expert_offsets, y),
-          (ctypes.byref(p), K, N, *_gemm_args(p, K, N, a, a_scale, src, w, w_scale, counts, expert_offsets),
-           _ptr(y, out_dt, p.T * p.k * N, "y")))
+    arg = _Args("moe_expert_gemm")
+    arg.call(_lib.moe_expert_gemm, stream, ctypes.byref(p), K, N,
+             *_gemm_args(arg, p, K, N, a, a_scale, src, w, w_scale, counts, expert_offsets),
+             arg(y, out_dt, p.T * p.k * N, "y"))
 
 
 def moe_expert_gemm_swiglu(p: Problem, K: int, I: int, a, a_scale, src, w, w_scale, counts,
                            expert_offsets, q, q_scale, stream=None) -> None:
     """w holds 2 I rows an expert, the gate's first; src as in moe_expert_gemm."""
-    n = p.T * p.k
-    _call("moe_expert_gemm_swiglu", stream,
-          (a, a_scale, src, w, w_scale, counts, expert_offsets, q, q_scale),
-          (ctypes.byref(p), K, I,
-           *_gemm_args(p, K, 2 * I, a, a_scale, src, w, w_scale, counts, expert_offsets),
-           _ptr(q, E4M3, n * I, "q"), _ptr(q_scale, torch.float32, n * scale_blocks(I), "q_scale")))
+    n, arg = p.T * p.k, _Args("moe_expert_gemm_swiglu")
+    arg.call(_lib.moe_expert_gemm_swiglu, stream, ctypes.byref(p), K, I,
+             *_gemm_args(arg, p, K, 2 * I, a, a_scale, src, w, w_scale, counts, expert_offsets),
+             arg(q, E4M3, n * I, "q"), arg(q_scale, torch.float32, n * scale_blocks(I), "q_scale"))
 
 
 def moe_layer_workspace_bytes(p: Problem, I: int) -> int:
@@ -476,15 +497,13 @@ def moe_layer_workspace_bytes(p: Problem, I: int) -> int:
 def moe_layer_few_tokens(p: Problem, I: int, logits, x, w_up, s_up, w_down, s_down, idx, w, out, ws,
                          stream=None) -> None:
     """s_up and s_down None: weights in the activation format; given: e4m3."""
-    act, n = _TORCH_ACT.get(p.act_dtype), p.T * p.k
+    act, T, E, H, n = _TORCH_ACT.get(p.act_dtype), p.T, p.E, p.H, p.T * p.k
     out_dt = torch.float32 if p.flags & MOE_FLAG_OUT_F32 else act
-    w_dt = act if s_up is None else E4M3
-    nh, ni = scale_blocks(p.H), scale_blocks(I)
-    _call("moe_layer_few_tokens", stream, (logits, x, w_up, s_up, w_down, s_down, idx, w, out, ws),
-          (ctypes.byref(p), I, _ptr(logits, torch.float32, p.T * p.E, "logits"),
-           _ptr(x, act, p.T * p.H, "x"), _ptr(w_up, w_dt, p.E * 2 * I * p.H, "w_up"),
-           _ptr(s_up, torch.float32, p.E * scale_blocks(2 * I) * nh, "s_up"),
-           _ptr(w_down, w_dt, p.E * p.H * I, "w_down"),
-           _ptr(s_down, torch.float32, p.E * nh * ni, "s_down"), _ptr(idx, torch.int32, n, "idx"),
-           _ptr(w, torch.float32, n, "w"), _ptr(out, out_dt, p.T * p.H, "out"),
-           _ptr(ws, None, None, "ws"), _nbytes(ws)))
+    f32, w_dt = torch.float32, act if s_up is None else E4M3
+    nh, ni = scale_blocks(H), scale_blocks(I)
+    a = _Args("moe_layer_few_tokens")
+    a.call(_lib.moe_layer_few_tokens, stream, ctypes.byref(p), I, a(logits, f32, T * E, "logits"),
+           a(x, act, T * H, "x"), a(w_up, w_dt, E * 2 * I * H, "w_up"),
+           a(s_up, f32, E * scale_blocks(2 * I) * nh, "s_up"), a(w_down, w_dt, E * H * I, "w_down"),
+           a(s_down, f32, E * nh * ni, "s_down"), a(idx, torch.int32, n, "idx"), a(w, f32, n, "w"),
+           a(out, out_dt, T * H, "out"), a(ws, None, None, "ws"), _nbytes(ws))

@@ -51,25 +51,22 @@ struct GemmArgs {
   float* q_scale;
 };
 
-// LDS: a ring of stages, one step of K each. A stage of a tile of MF units
-// holds 256 weight rows and 64 MF rows of 128 codes. The ring is as deep as
-// fits. Scales come for four steps at once, into one of two places: a step's
+// LDS: two stages, each a step of K: 256 weight rows and up to 256 rows of 128
+// codes; two places for scales, which come for four steps at once (a step's
 // scales of 64 rows lie in 64 lines of memory, and fetched one by one in each
-// step they were a third of all that the loads moved.
+// step they were a third of all that the loads moved); the source rows of
+// this tile and of the next.
+constexpr int kRows = kMaxUnits * kUnit;
 constexpr int kWBytes = kTileN * kDepth;
-constexpr int kABytes = kUnit * kDepth;  // of one unit
-constexpr int stage_bytes(int mf) { return kWBytes + mf * kABytes; }
+constexpr int kStageBytes = kWBytes + kRows * kDepth;
 constexpr int kGroup = 4;  // steps whose scales are loaded together
-constexpr int ring_depth(int mf) { return mf <= 2 ? 3 : 2; }
-constexpr int scale_place(int mf) { return (mf + 1) * kUnit * kGroup * 4; }  // the units' rows, the weights
-constexpr int ring_bytes(int mf) { return stage_bytes(mf) * ring_depth(mf) + 2 * scale_place(mf); }
-constexpr int kRingBytes = ring_bytes(2);
-static_assert(ring_bytes(1) <= kRingBytes && ring_bytes(3) <= kRingBytes && ring_bytes(4) <= kRingBytes,
-              "every ring fits");
+constexpr int kScalePlace = (kMaxUnits + 1) * kUnit * kGroup;  // floats: the units' rows, the weights
 
 struct Shared {
-  unsigned char ring[kRingBytes];  // stages, then the two places for scales
-  uint32_t amax[2][kMaxUnits * kUnit];
+  unsigned char stage[2][kStageBytes];
+  float scale[2][kScalePlace];
+  uint32_t amax[2][kRows];
+  uint32_t row[2][kRows];
   int count[kMaxE];
   int first_tile[kMaxE];
 };
@@ -80,12 +77,21 @@ static_assert(sizeof(Shared) <= 160 * 1024, "one block's LDS");
 // compiler, which cannot tell the stages of the ring apart, waits for every
 // such load of its own before the next LDS read; here the loop counts them
 // (wait_loads). They have no output register.
+// `base` and `lds` are the same in all lanes.
+__device__ __forceinline__ uint64_t uniform(const void* p) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u >> 32));
+  return lo | static_cast<uint64_t>(hi) << 32;
+}
 __device__ __forceinline__ void load_lds16(const void* base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(
+                   __builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(uniform(base))
                : "memory");
 }
 __device__ __forceinline__ void load_lds4(const void* base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(offset), "s"(base)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(
+                   __builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(uniform(base))
                : "memory");
 }
 
@@ -132,99 +138,150 @@ __device__ __forceinline__ Wide widen(const v8i& c) {
   return o;
 }
 
-// One tile: 64 MF rows from m0 on of the segment that starts at row `seg`
-// (`left` of them valid) against the weights n_tile of expert e.
-template <int MF, bool SWIGLU, int ACT, bool F32>
-__device__ __forceinline__ void tile(const GemmArgs& g, Shared& sh, int e, int seg, int m0, int left,
-                                     int n_tile) {
+// A tile: `left` rows (64 units at most) from row m0 of the segment that starts
+// at row `seg`, against the weights n_tile of expert e.
+struct Tile {
+  int e, seg, m0, left, n_tile, units;
+};
+
+// What a lane loads in each step: chunk `chunk` of the step's 128 bytes of
+// these rows, as byte offsets (the host checked that 32 bits hold them) from
+// the expert's weights and from the first row or token; and its scales. Row r
+// of a stage keeps chunk c at place c ^ (r / 2 % 8), so that the 16 lanes that
+// read one chunk of 16 rows together meet all LDS banks.
+struct Loads {
+  uint32_t w[4], a[kMaxUnits], s;
+  const uint8_t* w0;
+  const uint8_t* a0;
+  const float* s0;
+};
+
+__device__ __forceinline__ uint32_t chunk_of(int tid) { return (tid & 7) ^ ((tid >> 4) & 7); }
+
+// The rows of a tile counted from its first row, or from the first token,
+// those behind the last valid row its copies.
+__device__ __forceinline__ void fill_rows(const GemmArgs& g, const Tile& t, uint32_t* row) {
+  const int tid = threadIdx.x;
+  if (tid < kRows) {
+    const int m = min(tid, t.left - 1);
+    int r = m;
+    if (g.src != nullptr) {
+      const int i = g.src[t.seg + t.m0 + m];
+      r = i < 0 ? 0 : min(i / g.k, g.a_rows - 1);
+    }
+    row[tid] = r;
+  }
+}
+
+template <bool SWIGLU>
+__device__ __forceinline__ Loads loads_of(const GemmArgs& g, const Tile& t, const uint32_t* row) {
   // taken anew for each tile: what follows from it is cheap, and held over the
   // tile loop it would take registers that the accumulators need
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = wave & 1, wm = wave >> 1;
-  const int col = lane & 15, grp = lane >> 4;
   const int nbK = scale_blocks(g.K), nbN = scale_blocks(g.N);
+  const uint32_t c = chunk_of(tid) * 16;
+  Loads l;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    l.w[i] = static_cast<uint32_t>(weight_row<SWIGLU>(g, t.n_tile, i * 64 + (tid >> 3))) * g.K + c;
+    asm volatile("" : "+v"(l.w[i]));  // a plain register: 64-bit multiplications would keep a pair
+  }
+#pragma unroll
+  for (int i = 0; i < kMaxUnits; ++i) {
+    l.a[i] = row[i * 64 + (tid >> 3)] * g.K + c;
+    asm volatile("" : "+v"(l.a[i]));
+  }
+  const int row0 = g.src == nullptr ? t.seg + t.m0 : 0;
+  l.w0 = g.w + static_cast<size_t>(t.e) * g.N * g.K;
+  l.a0 = g.a + static_cast<size_t>(row0) * g.K;
+  // The first waves load their unit's scales, the others the weights' (all the
+  // same 16, so that every wave counts the same loads).
+  if (wave < t.units) {
+    l.s0 = g.a_scale + static_cast<size_t>(row0) * nbK;
+    l.s = row[wave * 64 + lane] * nbK * 4;
+  } else {
+    const int col = lane & 15;
+    l.s0 = g.w_scale + static_cast<size_t>(t.e) * nbN * nbK;
+    l.s = weight_row<SWIGLU>(g, t.n_tile, (col >> 2) * 64 + (col & 3) * 4) / kScaleBlock * nbK * 4;
+  }
+  asm volatile("" : "+v"(l.s));
+  return l;
+}
 
-  // What this lane loads in each step: chunk my_chunk of the step's 128 bytes
-  // of these rows, as byte offsets (the host checked that 32 bits hold them)
-  // from the expert's weights and from the first row or token. Row r of a
-  // stage keeps chunk c at place c ^ (r / 2 % 8), so that the 16 lanes that
-  // read one chunk of 16 rows together meet all LDS banks.
-  const uint32_t my_chunk = (tid & 7) ^ ((tid >> 4) & 7);
-  uint32_t wo[4], ao[MF];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    wo[i] = static_cast<uint32_t>(weight_row<SWIGLU>(g, n_tile, i * 64 + (tid >> 3))) * g.K + my_chunk * 16;
-  const int row0 = g.src == nullptr ? seg + m0 : 0;
-  auto row_of = [&](int m) {  // counted from row0
-    m = min(m, left - 1);
-    if (g.src == nullptr) return m;
-    const int i = g.src[seg + m0 + m];
-    return i < 0 ? 0 : min(i / g.k, g.a_rows - 1);
-  };
-#pragma unroll
-  for (int i = 0; i < MF; ++i) ao[i] = static_cast<uint32_t>(row_of(i * 64 + (tid >> 3))) * g.K + my_chunk * 16;
-  const uint8_t* const w0 = g.w + static_cast<size_t>(e) * g.N * g.K;
-  const uint8_t* const a0 = g.a + static_cast<size_t>(row0) * g.K;
+// The loads of a step come in two parts: the rows' codes and the first half of
+// each wave's weight rows, which the step is done with in its middle, and the
+// second half. Each is loaded again as soon as nobody reads it any more. Of
+// part's loads, all (-1) or one.
+template <int ITEM = -1>
+__device__ __forceinline__ void load_part(const GemmArgs& g, Shared& sh, const Loads& l, int units, int kb,
+                                          bool first) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nbK = scale_blocks(g.K);
+  const uint32_t st = lds_address(sh.stage[0]) + (kb & 1) * kStageBytes + wave * 1024;
+  const uint8_t* wk = l.w0 + kb * kDepth;
+  const uint8_t* ak = l.a0 + kb * kDepth;
   // Chunks past the end of K: their lanes take the row's last one instead, and
   // the weights' are overwritten with zeros in LDS.
-  const int end_chunks = g.K / 16 - (nbK - 1) * 8;  // of the last step
-  const uint32_t past = my_chunk * 16 - min(my_chunk, static_cast<uint32_t>(end_chunks - 1)) * 16;
-  // The first MF waves load their unit's scales, the others the weights' (all
-  // the same 16, so that every wave counts the same loads).
-  const float* s0;
-  uint32_t so;
-  if (wave < MF) {
-    s0 = g.a_scale + static_cast<size_t>(row0) * nbK;
-    so = static_cast<uint32_t>(row_of(wave * 64 + lane)) * nbK * 4;
-  } else {
-    s0 = g.w_scale + static_cast<size_t>(e) * nbN * nbK;
-    so = weight_row<SWIGLU>(g, n_tile, (col >> 2) * 64 + (col & 3) * 4) / kScaleBlock * nbK * 4;
+  uint32_t back = 0;
+  if (kb == nbK - 1) {
+    const uint32_t c = chunk_of(threadIdx.x), end = g.K / 16 - (nbK - 1) * 8;
+    back = (c - min(c, end - 1)) * 16;
   }
-
-  // as plain registers: computed by 64-bit multiplications they would stay pairs
+  auto at_chunk = [&](uint32_t o) { return o - back; };
+  if (first) {
+    if (ITEM <= 0 && kb % kGroup == 0) {
+      // With rows of whole 16-byte groups one load takes the scales of four
+      // steps and lane l's lie at 4 l; else four loads take one step each and
+      // step j's lie at 64 j.
+      const int group = kb / kGroup;
+      const uint32_t at = lds_address(sh.scale[0]) + (min(wave, units) * (kUnit * kGroup) + (group & 1) * kScalePlace) * 4;
+      if (g.scales16) {
+        load_lds16(l.s0 + group * kGroup, l.s, at);
+      } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(wo[i]));
-#pragma unroll
-  for (int i = 0; i < MF; ++i) asm volatile("" : "+v"(ao[i]));
-  asm volatile("" : "+v"(so));
-
-  constexpr int kSteps = ring_depth(MF);
-  constexpr int kFirst = 2 + MF, kSecond = 2;  // loads of each wave and part, without scales
-  constexpr int kScales = stage_bytes(MF) * kSteps;
-  const uint32_t ring = lds_address(sh.ring);
-  // With rows of whole 16-byte groups one load takes the scales of four steps
-  // and lane l's lie at 4 l; else four loads take one step each and step j's
-  // lie at 64 j.
-  auto load_scales = [&](int group) {
-    const uint32_t at = ring + kScales + min(wave, MF) * (kUnit * kGroup * 4) + (group & 1) * scale_place(MF);
-    if (g.scales16) {
-      load_lds16(s0 + group * kGroup, so, at);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j) load_lds4(s0 + min(group * kGroup + j, nbK - 1), so, at + j * 256);
+        for (int j = 0; j < kGroup; ++j) load_lds4(l.s0 + min(group * kGroup + j, nbK - 1), l.s, at + j * 256);
+      }
     }
-  };
-  // The loads come in two parts: the rows' codes and the first half of each
-  // wave's weight rows, which a step is done with in its middle, and the second
-  // half. Each is loaded again as soon as nobody reads it any more.
-  auto load_part = [&](int kb, bool first) {
-    const uint32_t st = ring + (kb % kSteps) * stage_bytes(MF) + wave * 1024;
-    const uint8_t* wk = w0 + kb * kDepth;
-    const uint8_t* ak = a0 + kb * kDepth;
-    const uint32_t back = kb == nbK - 1 ? past : 0;
-    if (first) {
-      if (kb % kGroup == 0) load_scales(kb / kGroup);
+    if constexpr (ITEM < 0) {
+      load_lds16(wk, at_chunk(l.w[0]), st);
+      load_lds16(wk, at_chunk(l.w[2]), st + 2 * 8192);
 #pragma unroll
-      for (int i = 0; i < MF; ++i) load_lds16(ak, ao[i] - back, st + kWBytes + i * 8192);
-      load_lds16(wk, wo[0] - back, st);
-      load_lds16(wk, wo[2] - back, st + 2 * 8192);
+      for (int i = 0; i < kMaxUnits; ++i)
+        if (i < units) load_lds16(ak, at_chunk(l.a[i]), st + kWBytes + i * 8192);
+    } else if constexpr (ITEM < 2) {
+      load_lds16(wk, at_chunk(l.w[2 * ITEM]), st + 2 * ITEM * 8192);
     } else {
-      load_lds16(wk, wo[1] - back, st + 8192);
-      load_lds16(wk, wo[3] - back, st + 3 * 8192);
+      load_lds16(ak, at_chunk(l.a[ITEM - 2]), st + kWBytes + (ITEM - 2) * 8192);
     }
-  };
+  } else {
+    if constexpr (ITEM != 1) load_lds16(wk, at_chunk(l.w[1]), st + 8192);
+    if constexpr (ITEM != 0) load_lds16(wk, at_chunk(l.w[3]), st + 3 * 8192);
+  }
+}
+
+// The loads that run before a tile's first step: all of step 0, the first part
+// of step 1.
+__device__ __forceinline__ void load_ahead(const GemmArgs& g, Shared& sh, const Loads& l, int units) {
+  load_part(g, sh, l, units, 0, true);
+  load_part(g, sh, l, units, 0, false);
+  if (g.K > kDepth) load_part(g, sh, l, units, 1, true);
+}
+
+// The products of one tile whose first loads are under way; `then()` runs
+// between the last step and the tile's output.
+template <int MF, bool SWIGLU, int ACT, bool F32, typename F>
+__device__ __forceinline__ void run_tile(const GemmArgs& g, Shared& sh, const Tile& t, const Loads& l, F&& then) {
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));  // as in loads_of
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave & 1, wm = wave >> 1;
+  const int col = lane & 15, grp = lane >> 4;
+  const int nbK = scale_blocks(g.K);
+  const int end_chunks = g.K / 16 - (nbK - 1) * 8;  // of the last step
+  constexpr int kFirst = 2 + MF;  // loads of each wave in a first part, without scales
+  constexpr int kGap = MF == 1 ? 1 : 2;  // instructions from one load to the next
+  constexpr bool kPrecise = SWIGLU || F32;
   const int s_row = g.scales16 ? kGroup : 1, s_step = g.scales16 ? 1 : kUnit;
 
   v4f acc[8][MF];
@@ -232,72 +289,103 @@ __device__ __forceinline__ void tile(const GemmArgs& g, Shared& sh, int e, int s
   for (int n = 0; n < 8; ++n)
 #pragma unroll
     for (int f = 0; f < MF; ++f) acc[n][f] = v4f{0, 0, 0, 0};
+  using Frag = std::conditional_t<kPrecise, Wide, v8i>;
+  Frag b[MF];
+  v8i w[2];
+  float s[2][MF];
 
-  constexpr bool kPrecise = SWIGLU || F32;
   auto read_frag = [&](const unsigned char* rows, int r) {
     const uint4* p = reinterpret_cast<const uint4*>(rows) + r * 8;
     const uint4 lo = p[(2 * grp) ^ ((r >> 1) & 7)];
     const uint4 hi = p[(2 * grp + 1) ^ ((r >> 1) & 7)];
     return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
   };
-
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    if (i < nbK) load_part(i, true);
-    if (i < kSteps - 1 && i < nbK) load_part(i, false);
-  }
-  // the first part of the step is read: load it anew
-  auto middle = [&](int kb) {
-    wait_reads();
-    if (kb + kSteps < nbK) load_part(kb + kSteps, true);
+  auto read_w = [&](int kb, int n) { return read_frag(sh.stage[kb & 1], wn * 128 + n * 16 + col); };
+  auto read_b = [&](int kb, int f) {
+    const v8i c = read_frag(sh.stage[kb & 1] + kWBytes, (f * 4 + wm) * 16 + col);
+    if constexpr (kPrecise) b[f] = widen(c);
+    else b[f] = c;
   };
-#pragma clang loop unroll(disable)
-  for (int kb = 0; kb < nbK; ++kb) {
-    // Step kb's codes are in LDS, and nobody reads the step before it any
-    // more. Loads issued since then may be in flight; scales among them only
-    // make the wait longer than it has to be.
-    if (kb + kSteps - 1 < nbK) {
-      wait_loads<(kSteps - 1) * kFirst + (kSteps - 2) * kSecond>();
-      load_part(kb + kSteps - 1, false);
-    } else {
-      wait_loads<0>();
-    }
-    unsigned char* st = sh.ring + (kb % kSteps) * stage_bytes(MF);
-    if (kb == nbK - 1 && end_chunks < 8) {  // zeros for the weights past the end of K
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (static_cast<int>(my_chunk) >= end_chunks)
-          reinterpret_cast<uint4*>(st)[i * 512 + tid] = make_uint4(0, 0, 0, 0);
-      wait_reads();
-    }
-    const float* scales = reinterpret_cast<const float*>(sh.ring + kScales + ((kb / kGroup) & 1) * scale_place(MF)) +
-                          (kb % kGroup) * s_step;
-    float s[2][MF];
-    const float sw0 = scales[MF * kUnit * kGroup + (wn * 8 + grp) * s_row];
-    const float sw1 = scales[MF * kUnit * kGroup + (wn * 8 + 4 + grp) * s_row];
+  auto read_scales = [&](int kb) {
+    const float* at = sh.scale[(kb / kGroup) & 1] + (kb % kGroup) * s_step;
+    const float sw0 = at[MF * kUnit * kGroup + (wn * 8 + grp) * s_row];
+    const float sw1 = at[MF * kUnit * kGroup + (wn * 8 + 4 + grp) * s_row];
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
-      const float sa = scales[f * kUnit * kGroup + (wm * 16 + col) * s_row];
+      const float sa = at[f * kUnit * kGroup + (wm * 16 + col) * s_row];
       s[0][f] = sa * sw0;
       s[1][f] = sa * sw1;
     }
-    auto add = [&](const v4f& p, int t) {
-      const int n = t / MF, f = t % MF;
+  };
+  auto add = [&](const v4f& p, int i) {
+    const int n = i / MF, f = i % MF;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][f][i] = fmaf(p[i], s[n >> 2][f], acc[n][f][i]);
-      asm volatile("" : "+v"(acc[n][f]));  // here, not after the branches of the loads
-    };
-    v8i w[2];
-    w[0] = read_frag(st, wn * 128 + col);
+    for (int q = 0; q < 4; ++q) acc[n][f][q] = fmaf(p[q], s[n >> 2][f], acc[n][f][q]);
+    asm volatile("" : "+v"(acc[n][f]));  // here, not after the branches of the loads
+  };
+  // Step kb's codes are in LDS, and nobody reads the step before it any more.
+  // Only a first part of the step after it may be in flight (scales among its
+  // loads make the wait longer than it has to be); at a tile's start also the
+  // stores of the tile before, so all is waited for.
+  auto begin = [&](int kb) {
+    if (kb > 0 && kb + 1 < nbK) wait_loads<kFirst>();
+    else wait_loads<0>();
+    if (kb == nbK - 1 && end_chunks < 8) {  // zeros for the weights past the end of K
+      if (static_cast<int>(chunk_of(tid)) >= end_chunks)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          reinterpret_cast<uint4*>(sh.stage[kb & 1])[i * 512 + tid] = make_uint4(0, 0, 0, 0);
+      wait_reads();
+    }
+  };
+  // The first part of step kb is read: load it anew.
+  // The loads are spread over the matrix instructions: issued at once, the
+  // 48 that all waves issue hold up the waves for as long as they take.
+  auto middle = [&](int) { wait_reads(); };
+  auto first_load = [&](int kb, auto item) {
+    if (kb + 2 < nbK) load_part<decltype(item)::value>(g, sh, l, MF, kb + 2, true);
+  };
+  auto second_load = [&](int kb, auto item) {
+    if (kb + 1 < nbK) load_part<decltype(item)::value>(g, sh, l, MF, kb + 1, false);
+  };
+  using std::integral_constant;
+
+  begin(0);
+  second_load(0, integral_constant<int, -1>{});
+  w[0] = read_w(0, 0);
+#pragma unroll
+  for (int f = 0; f < MF; ++f) read_b(0, f);
+  read_scales(0);
+  // What is loaded after matrix instruction i of a step: the first part from
+  // the middle on, the second part of the next step but one at its end.
+  auto spread = [&](int kb, int i) {
+    const int j = i - 4 * MF;
+    if (j == 0) first_load(kb, integral_constant<int, 0>{});
+    if (j == 1 * kGap) first_load(kb, integral_constant<int, 1>{});
+    if (j == 2 * kGap) first_load(kb, integral_constant<int, 2>{});
+    if constexpr (MF > 1) if (j == 3 * kGap) first_load(kb, integral_constant<int, 3>{});
+    if constexpr (MF > 2) if (j == 4 * kGap) first_load(kb, integral_constant<int, 4>{});
+    if constexpr (MF > 3) if (j == 5 * kGap) first_load(kb, integral_constant<int, 5>{});
+    if (i == 7 * MF) second_load(kb + 1, integral_constant<int, 0>{});
+    if (i == 8 * MF - 1) second_load(kb + 1, integral_constant<int, 1>{});
+  };
+#pragma clang loop unroll(disable)
+  for (int kb = 0; kb < nbK; ++kb) {
+    // A matrix instruction's multiply-adds follow two instructions later. The
+    // next step begins before this one's last weight fragment is used, so its
+    // first reads run under those instructions.
+    const bool more = kb + 1 < nbK;
     if constexpr (kPrecise) {
-      Wide b[MF];
-#pragma unroll
-      for (int f = 0; f < MF; ++f) b[f] = widen(read_frag(st + kWBytes, (f * 4 + wm) * 16 + col));
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
         if (n == 4) middle(kb);
-        if (n < 7) w[(n + 1) & 1] = read_frag(st, wn * 128 + (n + 1) * 16 + col);
         const Wide wide = widen(w[n & 1]);
+        if (n < 7) {
+          w[(n + 1) & 1] = read_w(kb, n + 1);
+        } else if (more) {
+          begin(kb + 1);
+          w[0] = read_w(kb + 1, 0);
+        }
         v4f p[MF];
 #pragma unroll
         for (int f = 0; f < MF; ++f) p[f] = v4f{0, 0, 0, 0};
@@ -306,33 +394,46 @@ __device__ __forceinline__ void tile(const GemmArgs& g, Shared& sh, int e, int s
 #pragma unroll
           for (int f = 0; f < MF; ++f) p[f] = mfma16<1>(wide.v[j], b[f].v[j], p[f]);
 #pragma unroll
-        for (int f = 0; f < MF; ++f) add(p[f], n * MF + f);
+        for (int f = 0; f < MF; ++f) {
+          add(p[f], n * MF + f);
+          spread(kb, n * MF + f);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
-    } else {
-      v8i b[MF];
+      if (more)
 #pragma unroll
-      for (int f = 0; f < MF; ++f) b[f] = read_frag(st + kWBytes, (f * 4 + wm) * 16 + col);
-      // a matrix instruction's multiply-adds follow two instructions later
+        for (int f = 0; f < MF; ++f) read_b(kb + 1, f);
+    } else {
       v4f p[3];
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
         if (n == 4) middle(kb);
-        if (n < 7) w[(n + 1) & 1] = read_frag(st, wn * 128 + (n + 1) * 16 + col);
+        if (n < 7) {
+          w[(n + 1) & 1] = read_w(kb, n + 1);
+        } else if (more) {
+          begin(kb + 1);
+          w[0] = read_w(kb + 1, 0);
+        }
 #pragma unroll
         for (int f = 0; f < MF; ++f) {
-          const int t = n * MF + f;
+          const int i = n * MF + f;
           const v4f z = {0, 0, 0, 0};
-          p[t % 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[n & 1], b[f], z, 0, 0, 0, 0, 0, 0);
-          if (t >= 2) add(p[(t - 2) % 3], t - 2);
+          p[i % 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[n & 1], b[f], z, 0, 0, 0, 0, 0, 0);
+          if (i >= 2) add(p[(i - 2) % 3], i - 2);
+          if (n == 7 && more) read_b(kb + 1, f);
+          spread(kb, i);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
       add(p[(8 * MF - 2) % 3], 8 * MF - 2);
       add(p[(8 * MF - 1) % 3], 8 * MF - 1);
     }
+    if (more) read_scales(kb + 1);
   }
+  wait_reads();  // nobody reads the stages any more
+  then();
 
+  const int seg = t.seg, m0 = t.m0, left = t.left, n_tile = t.n_tile;
   if constexpr (SWIGLU) {
     const int c0 = n_tile * 128 + wn * 64 + grp * 16;
 #pragma unroll
@@ -352,7 +453,7 @@ __device__ __forceinline__ void tile(const GemmArgs& g, Shared& sh, int e, int s
       top = umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, kWave)));
       if (grp == 0) sh.amax[wn][(f * 4 + wm) * 16 + col] = top;
     }
-    __syncthreads();
+    wait_reads();
     const int nbH = scale_blocks(g.half);
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
@@ -361,10 +462,11 @@ __device__ __forceinline__ void tile(const GemmArgs& g, Shared& sh, int e, int s
       if (m >= left) continue;
       const size_t r = static_cast<size_t>(seg) + m0 + m;
       if (c0 < g.half) {
+        const float inv = 1.0f / s;
         uint32_t o[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n)
-          o[n] = quant4(acc[n][f][0], acc[n][f][1], acc[n][f][2], acc[n][f][3], s);
+          o[n] = quant4(acc[n][f][0], acc[n][f][1], acc[n][f][2], acc[n][f][3], inv);
         *reinterpret_cast<uint4*>(g.q + r * g.half + c0) = make_uint4(o[0], o[1], o[2], o[3]);
       }
       if (wn == 0 && grp == 0) g.q_scale[r * nbH + n_tile] = s;
@@ -392,7 +494,6 @@ __device__ __forceinline__ void tile(const GemmArgs& g, Shared& sh, int e, int s
       }
     }
   }
-  __syncthreads();  // the next tile's loads overwrite the stages
 }
 
 // A segment of R rows is cut into ceil(R / 256) tiles of whole 64-row units,
@@ -433,35 +534,67 @@ __global__ __launch_bounds__(kGemmThreads, 2) void expert_gemm_kernel(GemmArgs g
 
   // Each XCD takes one run of tiles, and its blocks neighbouring ones: an
   // expert's weights and rows then pass through one L2.
-  const int total = __builtin_amdgcn_readfirstlane(sh.first_tile[g.E - 1] + tiles_of<kUnits>(sh.count[g.E - 1])) * g.n_tiles;  // the host checked that it fits
+  const int total = __builtin_amdgcn_readfirstlane(sh.first_tile[g.E - 1] + tiles_of<kUnits>(sh.count[g.E - 1])) *
+                    g.n_tiles;  // the host checked that it fits
   const int per_xcd = (total + kXcds - 1) / kXcds;
   const int first = static_cast<int>(blockIdx.x % kXcds) * per_xcd;
   const int last = min(total, first + per_xcd);
-  for (int t = first + static_cast<int>(blockIdx.x / kXcds); t < last; t += kGemmBlocks / kXcds) {
+  auto find = [&](int t) {
     const int mt = t / g.n_tiles;
     int lo = 0, hi = g.E;  // the last expert whose first tile is at most mt
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (sh.first_tile[mid] <= mt) lo = mid;
+      if (__builtin_amdgcn_readfirstlane(sh.first_tile[mid]) <= mt) lo = mid;
       else hi = mid;
     }
-    const int e = __builtin_amdgcn_readfirstlane(lo);
-    const int rows = __builtin_amdgcn_readfirstlane(sh.count[e]), tiles = tiles_of<kUnits>(rows);
-    const int in = t - __builtin_amdgcn_readfirstlane(sh.first_tile[e]) * g.n_tiles;
-    const int m_tile = in % tiles, n_tile = in / tiles;
+    Tile x;
+    x.e = lo;
+    const int rows = __builtin_amdgcn_readfirstlane(sh.count[x.e]), tiles = tiles_of<kUnits>(rows);
+    const int in = t - __builtin_amdgcn_readfirstlane(sh.first_tile[x.e]) * g.n_tiles;
+    const int m_tile = in % tiles;
+    x.n_tile = in / tiles;
     const int units = (rows + kUnit - 1) / kUnit, base = units / tiles, more = units % tiles;
     const int u0 = m_tile * base + min(m_tile, more);
-    const int u1 = u0 + base + (m_tile < more ? 1 : 0);
-    const int m0 = u0 * kUnit;
+    x.units = base + (m_tile < more ? 1 : 0);
+    x.m0 = u0 * kUnit;
     // a segment that would end past the rows is moved back inside
-    const int seg = __builtin_amdgcn_readfirstlane(max(0, min(g.offsets[e], g.rows - rows)));
-    const int left = min(rows, u1 * kUnit) - m0;
-    switch (u1 - u0) {
-      case 1: tile<1, SWIGLU, ACT, F32>(g, sh, e, seg, m0, left, n_tile); break;
-      case 2: tile<2, SWIGLU, ACT, F32>(g, sh, e, seg, m0, left, n_tile); break;
-      case 3: tile<3, SWIGLU, ACT, F32>(g, sh, e, seg, m0, left, n_tile); break;
-      default: tile<kUnits, SWIGLU, ACT, F32>(g, sh, e, seg, m0, left, n_tile); break;
+    x.seg = __builtin_amdgcn_readfirstlane(max(0, min(g.offsets[x.e], g.rows - rows)));
+    x.left = min(rows, (u0 + x.units) * kUnit) - x.m0;
+    return x;
+  };
+  int t = first + static_cast<int>(blockIdx.x / kXcds);
+  if (t >= last) return;
+  Tile cur = find(t);
+  fill_rows(g, cur, sh.row[0]);
+  __syncthreads();
+  Loads l = loads_of<SWIGLU>(g, cur, sh.row[0]);
+  load_ahead(g, sh, l, cur.units);
+  for (int turn = 1;; turn ^= 1) {
+    // the next tile's rows are looked up while this one runs, and its first
+    // loads run under this one's output
+    t += kGemmBlocks / kXcds;
+    const bool more = t < last;
+    Tile next = cur;
+    if (more) {
+      next = find(t);
+      fill_rows(g, next, sh.row[turn]);
     }
+    Loads nl = l;
+    auto then = [&] {
+      if (more) {
+        nl = loads_of<SWIGLU>(g, next, sh.row[turn]);
+        load_ahead(g, sh, nl, next.units);
+      }
+    };
+    switch (cur.units) {
+      case 1: run_tile<1, SWIGLU, ACT, F32>(g, sh, cur, l, then); break;
+      case 2: run_tile<2, SWIGLU, ACT, F32>(g, sh, cur, l, then); break;
+      case 3: run_tile<3, SWIGLU, ACT, F32>(g, sh, cur, l, then); break;
+      default: run_tile<kUnits, SWIGLU, ACT, F32>(g, sh, cur, l, then); break;
+    }
+    if (!more) break;
+    cur = next;
+    l = nl;
   }
 }
 
