@@ -13,8 +13,6 @@
 // in registers by one block, each lane owning 16-byte chunks (8 elements), so
 // every input is read once; a scale block of 128 elements is 16 lanes, one
 // DPP row, and its maximum never leaves the registers.
-#include <algorithm>
-
 #include "device.hpp"
 #include "launch.hpp"
 #include "quant.hpp"
@@ -23,9 +21,15 @@ namespace moe {
 
 namespace {
 
-// Rows of one forward launch at most: with 1024 threads a row a launch stays
-// below 2^32 work-items.
-constexpr int kNormRows = 1 << 21;
+// Blocks of a forward launch: what the chip holds of NT threads at this
+// kernel's registers (24 waves a CU), fewer if that evens out the rows a block
+// takes: with a few rows left for another round, that round costs as much as a
+// full one.
+constexpr int norm_blocks(int T, int NT) {
+  const int most = 256 * (24 * kWave / NT);
+  const int rounds = (T + most - 1) / most;
+  return (T + rounds - 1) / rounds;
+}
 
 // Sum over the block in a fixed order: a butterfly in the wave, then the
 // waves' sums in order. Uses one slot of `part` per wave; the caller puts a
@@ -46,88 +50,98 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
 // The larger of two magnitudes; NaN if either is.
 __device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, fabsf(b)); }
 
-// One row per block; lane i of the block owns chunks i, i + NT, ... (U of
-// them at most). h_out and y may be x or res themselves: a lane reads its
-// chunks before it writes them, and nobody else does either.
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ...; lane i of the block owns chunks
+// i, i + NT, ... (U of them at most) of each. The next row is loaded before
+// this one's sum goes round the block: with a block for each row a CU holds
+// 64 KiB in flight and then waits (16384 rows of 4096, y alone: 63.7 us). h_out
+// and y may be x or res themselves: a lane reads its chunks of a row before it
+// writes them, and nobody else does either.
 template <int ACT, int NT, int U>
 __global__ __launch_bounds__(NT) void rms_norm_kernel(
-    const uint4* x, const uint4* res, const uint4* __restrict__ gamma,
-    float eps, int first, int H, uint4* h_out, uint4* y, uint2* __restrict__ q,
-    float* __restrict__ q_scale, float* __restrict__ rstd_out) {
-  __shared__ float part[2][NT / kWave];
-  const int cpr = H / 8;
-  const size_t row = static_cast<size_t>(first) + blockIdx.x;
+    const uint4* x, const uint4* res, const uint4* __restrict__ gamma, float eps, int T, int H,
+    uint4* h_out, uint4* y, uint2* __restrict__ q, float* __restrict__ q_scale,
+    float* __restrict__ rstd_out) {
+  __shared__ float part[3][NT / kWave];
+  const int cpr = H / 8, nb = scale_blocks(H);
   const uint4 zero = make_uint4(0, 0, 0, 0);
   uint4 xv[U], rv[U], gv[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int c = static_cast<int>(threadIdx.x) + u * NT;
-    xv[u] = c < cpr ? x[row * cpr + c] : zero;
-  }
-  if (res != nullptr) {
+  auto load = [&](int r) {
+    const size_t base = static_cast<size_t>(r) * cpr;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = static_cast<int>(threadIdx.x) + u * NT;
-      rv[u] = c < cpr ? res[row * cpr + c] : zero;
+      xv[u] = c < cpr ? x[base + c] : zero;
     }
-  }
+    if (res != nullptr) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = static_cast<int>(threadIdx.x) + u * NT;
+        rv[u] = c < cpr ? res[base + c] : zero;
+      }
+    }
+  };
+  load(blockIdx.x);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int c = static_cast<int>(threadIdx.x) + u * NT;
     gv[u] = c < cpr ? gamma[c] : zero;
   }
-  float f[U][8];
-  float ss = 0.0f;
+  int turn = 0;
+  for (int r = blockIdx.x; r < T; r += gridDim.x, turn ^= 1) {
+    const size_t row = r;
+    float f[U][8];
+    float ss = 0.0f;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int c = static_cast<int>(threadIdx.x) + u * NT;
-    unpack8<ACT>(xv[u], f[u]);
-    if (res != nullptr) {
-      float r[8];
-      unpack8<ACT>(rv[u], r);
+    for (int u = 0; u < U; ++u) {
+      const int c = static_cast<int>(threadIdx.x) + u * NT;
+      unpack8<ACT>(xv[u], f[u]);
+      if (res != nullptr) {
+        float a[8];
+        unpack8<ACT>(rv[u], a);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[u][i] = keep_f32(f[u][i] + r[i]);
-      const uint4 hv = round8<ACT>(f[u]);
-      if (c < cpr) h_out[row * cpr + c] = hv;
-      unpack8<ACT>(hv, f[u]);
+        for (int i = 0; i < 8; ++i) f[u][i] = keep_f32(f[u][i] + a[i]);
+        const uint4 hv = round8<ACT>(f[u]);
+        if (c < cpr) h_out[row * cpr + c] = hv;
+        unpack8<ACT>(hv, f[u]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(f[u][i], f[u][i], ss);
     }
+    if (r + static_cast<int>(gridDim.x) < T) load(r + gridDim.x);
+    ss = block_sum<NT>(ss, part[turn]);
+    float rstd = 1.0f / sqrtf(ss / static_cast<float>(H) + eps);
+    if (!(ss < 0x1p126f) || (ss < 0x1p-90f && eps < 0x1p-90f)) {
+      // Squares that fp32 does not hold, as bf16 values may have: once more, of
+      // the values brought near 1. Rare, and the same for the whole block.
+      const float scale = ss < 1.0f ? 0x1p60f : 0x1p-80f;
+      float again = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(f[u][i], f[u][i], ss);
-  }
-  ss = block_sum<NT>(ss, part[0]);
-  float rstd = 1.0f / sqrtf(ss / static_cast<float>(H) + eps);
-  if (!(ss < 0x1p126f) || (ss < 0x1p-90f && eps < 0x1p-90f)) {
-    // Squares that fp32 does not hold, as bf16 values may have: once more, of
-    // the values brought near 1. Rare, and the same for the whole block.
-    const float scale = ss < 1.0f ? 0x1p60f : 0x1p-80f;
-    float again = 0.0f;
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) again = fmaf(f[u][i] * scale, f[u][i] * scale, again);
-    again = block_sum<NT>(again, part[1]);
-    rstd = scale / sqrtf(again / static_cast<float>(H) + eps * scale * scale);
-  }
-  if (rstd_out != nullptr && threadIdx.x == 0) rstd_out[row] = rstd;
-  const int nb = scale_blocks(H);
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int c = static_cast<int>(threadIdx.x) + u * NT;
-    float g[8];
-    unpack8<ACT>(gv[u], g);
-    float most = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      f[u][i] = keep_f32(f[u][i] * rstd * g[i]);
-      most = larger(most, f[u][i]);
+        for (int i = 0; i < 8; ++i) again = fmaf(f[u][i] * scale, f[u][i] * scale, again);
+      again = block_sum<NT>(again, part[2]);
+      rstd = scale / sqrtf(again / static_cast<float>(H) + eps * scale * scale);
     }
-    if (y != nullptr && c < cpr) y[row * cpr + c] = round8<ACT>(f[u]);
-    if (q != nullptr) {
-      // lanes past the row hold zeros; among bits NaN is the largest magnitude
-      const float s = block_scale(group_max<16>(__float_as_uint(most) & 0x7fffffffu));
-      if (c < cpr) {
-        q[row * cpr + c] = quant8(f[u], 1.0f / s);
-        if ((c & 15) == 0) q_scale[row * nb + c / 16] = s;
+    if (rstd_out != nullptr && threadIdx.x == 0) rstd_out[row] = rstd;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = static_cast<int>(threadIdx.x) + u * NT;
+      float g[8];
+      unpack8<ACT>(gv[u], g);
+      float most = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f[u][i] = keep_f32(f[u][i] * rstd * g[i]);
+        most = larger(most, f[u][i]);
+      }
+      if (y != nullptr && c < cpr) y[row * cpr + c] = round8<ACT>(f[u]);
+      if (q != nullptr) {
+        // lanes past the row hold zeros; among bits NaN is the largest magnitude
+        const float s = block_scale(group_max<16>(__float_as_uint(most) & 0x7fffffffu));
+        if (c < cpr) {
+          q[row * cpr + c] = quant8(f[u], 1.0f / s);
+          if ((c & 15) == 0) q_scale[row * nb + c / 16] = s;
+        }
       }
     }
   }
@@ -254,11 +268,10 @@ hipError_t launch_rms_norm(const void* x, const void* residual, const void* gamm
                            hipStream_t s) {
   by_act(act, [&](auto A) {
     by_row(H / 8, [&](auto NT, auto U) {
-      for (int first = 0; first < T; first += kNormRows)
-        rms_norm_kernel<A, NT, U><<<std::min(T - first, kNormRows), int(NT), 0, s>>>(
-            static_cast<const uint4*>(x), static_cast<const uint4*>(residual),
-            static_cast<const uint4*>(gamma), eps, first, H, static_cast<uint4*>(h),
-            static_cast<uint4*>(y), static_cast<uint2*>(q), q_scale, rstd);
+      rms_norm_kernel<A, NT, U><<<norm_blocks(T, NT), int(NT), 0, s>>>(
+          static_cast<const uint4*>(x), static_cast<const uint4*>(residual),
+          static_cast<const uint4*>(gamma), eps, T, H, static_cast<uint4*>(h), static_cast<uint4*>(y),
+          static_cast<uint2*>(q), q_scale, rstd);
     });
   });
   return hipGetLastError();
