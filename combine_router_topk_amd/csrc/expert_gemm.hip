@@ -51,26 +51,24 @@ struct GemmArgs {
   float* q_scale;
 };
 
-// LDS: two stages, each a step of K: 256 weight rows and up to 256 rows of 128
-// codes; two places for scales, which come for four steps at once (a step's
-// scales of 64 rows lie in 64 lines of memory, and fetched one by one in each
-// step they were a third of all that the loads moved); the source rows of
-// this tile and of the next.
-constexpr int kRows = kMaxUnits * kUnit;
+// LDS: two stages, each a step of K (256 weight rows and the rows' codes); two
+// places for scales, which come for four steps at once (a step's scales of 64
+// rows lie in 64 lines of memory, and fetched one by one in each step they were
+// a third of all that the loads moved); the source rows of the next tile.
 constexpr int kWBytes = kTileN * kDepth;
-constexpr int kStageBytes = kWBytes + kRows * kDepth;
 constexpr int kGroup = 4;  // steps whose scales are loaded together
-constexpr int kScalePlace = (kMaxUnits + 1) * kUnit * kGroup;  // floats: the units' rows, the weights
 
+template <int UNITS>
 struct Shared {
-  unsigned char stage[2][kStageBytes];
+  static constexpr int kRows = UNITS * kUnit;
+  static constexpr int kStage = kWBytes + kRows * kDepth;
+  static constexpr int kScalePlace = (UNITS + 1) * kUnit * kGroup;  // floats: the units' rows, the weights
+  unsigned char stage[2][kStage];
   float scale[2][kScalePlace];
   uint32_t amax[2][kRows];
-  uint32_t row[2][kRows];
-  int count[kMaxE];
+  uint32_t row[kRows];
   int first_tile[kMaxE];
 };
-static_assert(sizeof(Shared) <= 160 * 1024, "one block's LDS");
 
 // Each lane's 16 (or 4) bytes from base + offset go to LDS at byte lds + 16
 // (or 4) * lane without passing through registers. Written as assembly because the
@@ -84,10 +82,11 @@ __device__ __forceinline__ uint64_t uniform(const void* p) {
   const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u >> 32));
   return lo | static_cast<uint64_t>(hi) << 32;
 }
+template <int PLUS = 0>  // added to lds
 __device__ __forceinline__ void load_lds16(const void* base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(
-                   __builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(uniform(base))
-               : "memory");
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(
+                   __builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(uniform(base)), "n"(PLUS)
+               : "memory", "scc");
 }
 __device__ __forceinline__ void load_lds4(const void* base, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(
@@ -146,9 +145,7 @@ struct Tile {
 
 // What a lane loads in each step: chunk `chunk` of the step's 128 bytes of
 // these rows, as byte offsets (the host checked that 32 bits hold them) from
-// the expert's weights and from the first row or token; and its scales. Row r
-// of a stage keeps chunk c at place c ^ (r / 2 % 8), so that the 16 lanes that
-// read one chunk of 16 rows together meet all LDS banks.
+// the expert's weights and from the first row or token; and its scales.
 struct Loads {
   uint32_t w[4], a[kMaxUnits], s;
   const uint8_t* w0;
@@ -156,13 +153,30 @@ struct Loads {
   const float* s0;
 };
 
-__device__ __forceinline__ uint32_t chunk_of(int tid) { return (tid & 7) ^ ((tid >> 4) & 7); }
+// Row r of a stage keeps 16-byte chunk c at place c ^ swizzle(r): a 128-bit LDS
+// read takes 16 lanes at a time, four by four from two neighbouring groups of
+// 16 lanes (which read chunks c and c ^ 2 here), and with this the 16 meet all
+// 64 banks.
+__device__ __forceinline__ int swizzle(int r) {
+  const int i = r >> 1;
+  return ((i & 1) << 1) | ((i >> 2) & 1) | ((((i >> 1) ^ (i >> 2)) & 1) << 2);
+}
+__device__ __forceinline__ uint32_t chunk_of(int tid) { return (tid & 7) ^ swizzle(tid >> 3); }
+
+// The thread's number, from its wave's in a scalar register. Computed anew
+// wherever it is asked for: held over the tile loop, it and what follows from it
+// would take registers that the accumulators need.
+__device__ __forceinline__ int thread_of(int wave) {
+  uint32_t zero = 0;
+  asm volatile("" : "+s"(zero));
+  return wave * kWave + static_cast<int>(__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero)));
+}
 
 // The rows of a tile counted from its first row, or from the first token,
 // those behind the last valid row its copies.
-__device__ __forceinline__ void fill_rows(const GemmArgs& g, const Tile& t, uint32_t* row) {
-  const int tid = threadIdx.x;
-  if (tid < kRows) {
+__device__ __forceinline__ void fill_rows(const GemmArgs& g, int wave, const Tile& t, uint32_t* row, int rows) {
+  const int tid = thread_of(wave);
+  if (tid < rows) {
     const int m = min(tid, t.left - 1);
     int r = m;
     if (g.src != nullptr) {
@@ -173,13 +187,9 @@ __device__ __forceinline__ void fill_rows(const GemmArgs& g, const Tile& t, uint
   }
 }
 
-template <bool SWIGLU>
-__device__ __forceinline__ Loads loads_of(const GemmArgs& g, const Tile& t, const uint32_t* row) {
-  // taken anew for each tile: what follows from it is cheap, and held over the
-  // tile loop it would take registers that the accumulators need
-  int tid = threadIdx.x;
-  asm volatile("" : "+v"(tid));
-  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+template <int UNITS, bool SWIGLU>
+__device__ __forceinline__ Loads loads_of(const GemmArgs& g, int wave, const Tile& t, const uint32_t* row) {
+  const int tid = thread_of(wave), lane = tid & 63;
   const int nbK = scale_blocks(g.K), nbN = scale_blocks(g.N);
   const uint32_t c = chunk_of(tid) * 16;
   Loads l;
@@ -189,7 +199,7 @@ __device__ __forceinline__ Loads loads_of(const GemmArgs& g, const Tile& t, cons
     asm volatile("" : "+v"(l.w[i]));  // a plain register: 64-bit multiplications would keep a pair
   }
 #pragma unroll
-  for (int i = 0; i < kMaxUnits; ++i) {
+  for (int i = 0; i < UNITS; ++i) {
     l.a[i] = row[i * 64 + (tid >> 3)] * g.K + c;
     asm volatile("" : "+v"(l.a[i]));
   }
@@ -210,79 +220,72 @@ __device__ __forceinline__ Loads loads_of(const GemmArgs& g, const Tile& t, cons
   return l;
 }
 
-// The loads of a step come in two parts: the rows' codes and the first half of
-// each wave's weight rows, which the step is done with in its middle, and the
-// second half. Each is loaded again as soon as nobody reads it any more. Of
-// part's loads, all (-1) or one.
-template <int ITEM = -1>
-__device__ __forceinline__ void load_part(const GemmArgs& g, Shared& sh, const Loads& l, int units, int kb,
-                                          bool first) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nbK = scale_blocks(g.K);
-  const uint32_t st = lds_address(sh.stage[0]) + (kb & 1) * kStageBytes + wave * 1024;
-  const uint8_t* wk = l.w0 + kb * kDepth;
-  const uint8_t* ak = l.a0 + kb * kDepth;
-  // Chunks past the end of K: their lanes take the row's last one instead, and
-  // the weights' are overwritten with zeros in LDS.
-  uint32_t back = 0;
-  if (kb == nbK - 1) {
-    const uint32_t c = chunk_of(threadIdx.x), end = g.K / 16 - (nbK - 1) * 8;
-    back = (c - min(c, end - 1)) * 16;
-  }
-  auto at_chunk = [&](uint32_t o) { return o - back; };
-  if (first) {
-    if (ITEM <= 0 && kb % kGroup == 0) {
-      // With rows of whole 16-byte groups one load takes the scales of four
-      // steps and lane l's lie at 4 l; else four loads take one step each and
-      // step j's lie at 64 j.
-      const int group = kb / kGroup;
-      const uint32_t at = lds_address(sh.scale[0]) + (min(wave, units) * (kUnit * kGroup) + (group & 1) * kScalePlace) * 4;
-      if (g.scales16) {
-        load_lds16(l.s0 + group * kGroup, l.s, at);
-      } else {
+// Chunks past the end of K: in the last step their lanes take the row's last
+// one instead, and the weights' are overwritten with zeros in LDS. How far back
+// that is:
+__device__ __forceinline__ uint32_t past_end(const GemmArgs& g, int wave) {
+  const uint32_t c = chunk_of(thread_of(wave)), end = g.K / 16 - (scale_blocks(g.K) - 1) * 8;
+  return (c - min(c, end - 1)) * 16;
+}
+
+template <int UNITS>
+__device__ __forceinline__ void step_back(Loads& l, uint32_t by) {
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) load_lds4(l.s0 + min(group * kGroup + j, nbK - 1), l.s, at + j * 256);
-      }
-    }
-    if constexpr (ITEM < 0) {
-      load_lds16(wk, at_chunk(l.w[0]), st);
-      load_lds16(wk, at_chunk(l.w[2]), st + 2 * 8192);
+  for (int i = 0; i < 4; ++i) l.w[i] -= by;
 #pragma unroll
-      for (int i = 0; i < kMaxUnits; ++i)
-        if (i < units) load_lds16(ak, at_chunk(l.a[i]), st + kWBytes + i * 8192);
-    } else if constexpr (ITEM < 2) {
-      load_lds16(wk, at_chunk(l.w[2 * ITEM]), st + 2 * ITEM * 8192);
-    } else {
-      load_lds16(ak, at_chunk(l.a[ITEM - 2]), st + kWBytes + (ITEM - 2) * 8192);
-    }
+  for (int i = 0; i < UNITS; ++i) l.a[i] -= by;
+}
+
+// The scales of steps 4 group .. 4 group + 3. With rows of whole 16-byte groups
+// one load takes them and lane l's lie at 4 l; else four loads take one step
+// each and step j's lie at 64 j.
+template <int UNITS>
+__device__ __forceinline__ void load_scales(const GemmArgs& g, int wave, Shared<UNITS>& sh, const Loads& l, int units,
+                                            int group) {
+  const uint32_t at = lds_address(sh.scale[0]) +
+                      (min(wave, units) * (kUnit * kGroup) + (group & 1) * Shared<UNITS>::kScalePlace) * 4;
+  if (g.scales16) {
+    load_lds16(l.s0 + group * kGroup, l.s, at);
   } else {
-    if constexpr (ITEM != 1) load_lds16(wk, at_chunk(l.w[1]), st + 8192);
-    if constexpr (ITEM != 0) load_lds16(wk, at_chunk(l.w[3]), st + 3 * 8192);
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j)
+      load_lds4(l.s0 + min(group * kGroup + j, scale_blocks(g.K) - 1), l.s, at + j * 256);
   }
 }
 
-// The loads that run before a tile's first step: all of step 0, the first part
-// of step 1.
-__device__ __forceinline__ void load_ahead(const GemmArgs& g, Shared& sh, const Loads& l, int units) {
-  load_part(g, sh, l, units, 0, true);
-  load_part(g, sh, l, units, 0, false);
-  if (g.K > kDepth) load_part(g, sh, l, units, 1, true);
+// The loads that run before a tile's first step: all of steps 0 and 1.
+template <int UNITS>
+__device__ __forceinline__ void load_ahead(const GemmArgs& g, int wave, Shared<UNITS>& sh, Loads& l, int units) {
+  const int nbK = scale_blocks(g.K);
+  load_scales(g, wave, sh, l, units, 0);
+  for (int kb = 0; kb < min(nbK, 2); ++kb) {
+    const uint32_t st = lds_address(sh.stage[0]) + kb * Shared<UNITS>::kStage + wave * 1024;
+    if (kb == nbK - 1) step_back<UNITS>(l, past_end(g, wave));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_lds16(l.w0 + kb * kDepth, l.w[i], st + i * 8192);
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i)
+      if (i < units) load_lds16(l.a0 + kb * kDepth, l.a[i], st + kWBytes + i * 8192);
+  }
 }
 
 // The products of one tile whose first loads are under way; `then()` runs
 // between the last step and the tile's output.
-template <int MF, bool SWIGLU, int ACT, bool F32, typename F>
-__device__ __forceinline__ void run_tile(const GemmArgs& g, Shared& sh, const Tile& t, const Loads& l, F&& then) {
-  int tid = threadIdx.x;
-  asm volatile("" : "+v"(tid));  // as in loads_of
-  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+//
+// In a step the rows' codes and the first half of each wave's weight rows are
+// read by its middle, the second half by its end; each is then loaded anew for
+// the next step but one.
+template <int MF, int UNITS, bool SWIGLU, int ACT, bool F32, typename F>
+__device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, Shared<UNITS>& sh, const Tile& t, Loads& l,
+                                         F&& then) {
+  const int tid = thread_of(wave), lane = tid & 63;
   const int wn = wave & 1, wm = wave >> 1;
   const int col = lane & 15, grp = lane >> 4;
   const int nbK = scale_blocks(g.K);
   const int end_chunks = g.K / 16 - (nbK - 1) * 8;  // of the last step
   constexpr int kFirst = 2 + MF;  // loads of each wave in a first part, without scales
-  constexpr int kGap = MF == 1 ? 1 : 2;  // instructions from one load to the next
   constexpr bool kPrecise = SWIGLU || F32;
-  const int s_row = g.scales16 ? kGroup : 1, s_step = g.scales16 ? 1 : kUnit;
+  constexpr int kStage = Shared<UNITS>::kStage;
 
   v4f acc[8][MF];
 #pragma unroll
@@ -291,73 +294,72 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, Shared& sh, const Ti
     for (int f = 0; f < MF; ++f) acc[n][f] = v4f{0, 0, 0, 0};
   using Frag = std::conditional_t<kPrecise, Wide, v8i>;
   Frag b[MF];
-  v8i w[2];
   float s[2][MF];
 
-  auto read_frag = [&](const unsigned char* rows, int r) {
-    const uint4* p = reinterpret_cast<const uint4*>(rows) + r * 8;
-    const uint4 lo = p[(2 * grp) ^ ((r >> 1) & 7)];
-    const uint4 hi = p[(2 * grp + 1) ^ ((r >> 1) & 7)];
-    return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+  // this lane's two chunks in the stage of the current step, of weight and of
+  // row fragments
+  const unsigned char* const stage0 = sh.stage[0];
+  int wl = (wn * 128 + col) * 128 + ((2 * grp) ^ swizzle(col)) * 16;
+  int wh = (wn * 128 + col) * 128 + ((2 * grp + 1) ^ swizzle(col)) * 16;
+  int al = wl + kWBytes + (wm * 16 - wn * 128) * 128, ah = wh + kWBytes + (wm * 16 - wn * 128) * 128;
+  auto read2 = [&](int lo, int hi) {
+    const uint4 x = *reinterpret_cast<const uint4*>(stage0 + lo), y = *reinterpret_cast<const uint4*>(stage0 + hi);
+    return v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
   };
-  auto read_w = [&](int kb, int n) { return read_frag(sh.stage[kb & 1], wn * 128 + n * 16 + col); };
-  auto read_b = [&](int kb, int f) {
-    const v8i c = read_frag(sh.stage[kb & 1] + kWBytes, (f * 4 + wm) * 16 + col);
-    if constexpr (kPrecise) b[f] = widen(c);
-    else b[f] = c;
+  auto read_w = [&](int n) { return read2(wl + n * 2048, wh + n * 2048); };
+  auto read_b = [&](int f) { return read2(al + f * 8192, ah + f * 8192); };
+  auto other_stage = [&] {
+    wl = kStage + 2 * ((wn * 128 + col) * 128 + ((2 * grp) ^ swizzle(col)) * 16) - wl;
+    wh = kStage + 2 * ((wn * 128 + col) * 128 + ((2 * grp + 1) ^ swizzle(col)) * 16) - wh;
+    al = wl + kWBytes + (wm * 16 - wn * 128) * 128;
+    ah = wh + kWBytes + (wm * 16 - wn * 128) * 128;
   };
+  const int s_row = g.scales16 ? kGroup : 1, s_step = g.scales16 ? 1 : kUnit;
+  const int sa_at = (wm * 16 + col) * s_row, sw_at = MF * kUnit * kGroup + (wn * 8 + grp) * s_row;
   auto read_scales = [&](int kb) {
-    const float* at = sh.scale[(kb / kGroup) & 1] + (kb % kGroup) * s_step;
-    const float sw0 = at[MF * kUnit * kGroup + (wn * 8 + grp) * s_row];
-    const float sw1 = at[MF * kUnit * kGroup + (wn * 8 + 4 + grp) * s_row];
+    const float* at = sh.scale[0] + ((kb / kGroup) & 1) * Shared<UNITS>::kScalePlace + (kb % kGroup) * s_step;
+    const float sw0 = at[sw_at], sw1 = at[sw_at + 4 * s_row];
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
-      const float sa = at[f * kUnit * kGroup + (wm * 16 + col) * s_row];
+      const float sa = at[f * kUnit * kGroup + sa_at];
       s[0][f] = sa * sw0;
       s[1][f] = sa * sw1;
     }
   };
-  auto add = [&](const v4f& p, int i) {
+  auto add1 = [&](const v4f& p, int i, int q) {
     const int n = i / MF, f = i % MF;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) acc[n][f][q] = fmaf(p[q], s[n >> 2][f], acc[n][f][q]);
-    asm volatile("" : "+v"(acc[n][f]));  // here, not after the branches of the loads
+    acc[n][f][q] = fmaf(p[q], s[n >> 2][f], acc[n][f][q]);
   };
-  // Step kb's codes are in LDS, and nobody reads the step before it any more.
-  // Only a first part of the step after it may be in flight (scales among its
-  // loads make the wait longer than it has to be); at a tile's start also the
-  // stores of the tile before, so all is waited for.
-  auto begin = [&](int kb) {
-    if (kb > 0 && kb + 1 < nbK) wait_loads<kFirst>();
-    else wait_loads<0>();
-    if (kb == nbK - 1 && end_chunks < 8) {  // zeros for the weights past the end of K
-      if (static_cast<int>(chunk_of(tid)) >= end_chunks)
+  auto add = [&](const v4f& p, int i) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          reinterpret_cast<uint4*>(sh.stage[kb & 1])[i * 512 + tid] = make_uint4(0, 0, 0, 0);
-      wait_reads();
-    }
+    for (int q = 0; q < 4; ++q) add1(p, i, q);
+    asm volatile("" : "+v"(acc[i / MF][i % MF]));  // here, not after the branches of the loads
   };
-  // The first part of step kb is read: load it anew.
-  // The loads are spread over the matrix instructions: issued at once, the
-  // 48 that all waves issue hold up the waves for as long as they take.
-  auto middle = [&](int) { wait_reads(); };
+
+  // where the loads of step kb + 2 come from, and the stage they go to, that of
+  // step kb
+  const uint8_t* wk = l.w0 + 2 * kDepth;
+  const uint8_t* ak = l.a0 + 2 * kDepth;
+  uint32_t st = lds_address(sh.stage[0]) + wave * 1024;
+  const uint32_t st_sum = 2 * st + kStage;
   auto first_load = [&](int kb, auto item) {
-    if (kb + 2 < nbK) load_part<decltype(item)::value>(g, sh, l, MF, kb + 2, true);
+    constexpr int I = decltype(item)::value;
+    if constexpr (I == 0) {
+      if (kb + 3 == nbK) step_back<UNITS>(l, past_end(g, wave));
+      if ((kb + 2) % kGroup == 0) load_scales(g, wave, sh, l, MF, (kb + 2) / kGroup);
+    }
+    if constexpr (I < 2) load_lds16<I * 2 * 8192>(wk, l.w[2 * I], st);
+    else load_lds16<kWBytes + (I - 2) * 8192>(ak, l.a[I - 2], st);
   };
-  auto second_load = [&](int kb, auto item) {
-    if (kb + 1 < nbK) load_part<decltype(item)::value>(g, sh, l, MF, kb + 1, false);
+  auto second_load = [&](auto item) {
+    constexpr int I = decltype(item)::value;
+    load_lds16<(1 + 2 * I) * 8192>(wk, l.w[1 + 2 * I], st);
   };
   using std::integral_constant;
-
-  begin(0);
-  second_load(0, integral_constant<int, -1>{});
-  w[0] = read_w(0, 0);
-#pragma unroll
-  for (int f = 0; f < MF; ++f) read_b(0, f);
-  read_scales(0);
-  // What is loaded after matrix instruction i of a step: the first part from
-  // the middle on, the second part of the next step but one at its end.
+  // The loads are spread over a step's matrix instructions, from number 4 MF on
+  // (the first part) and from 7 MF on, once the next step has begun: issued at
+  // once they would hold up every wave.
+  constexpr int kGap = MF == 1 ? 1 : 2;
   auto spread = [&](int kb, int i) {
     const int j = i - 4 * MF;
     if (j == 0) first_load(kb, integral_constant<int, 0>{});
@@ -366,75 +368,138 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, Shared& sh, const Ti
     if constexpr (MF > 1) if (j == 3 * kGap) first_load(kb, integral_constant<int, 3>{});
     if constexpr (MF > 2) if (j == 4 * kGap) first_load(kb, integral_constant<int, 4>{});
     if constexpr (MF > 3) if (j == 5 * kGap) first_load(kb, integral_constant<int, 5>{});
-    if (i == 7 * MF) second_load(kb + 1, integral_constant<int, 0>{});
-    if (i == 8 * MF - 1) second_load(kb + 1, integral_constant<int, 1>{});
+    if (i == 7 * MF) second_load(integral_constant<int, 0>{});
+    if (i == 8 * MF - 1) {
+      second_load(integral_constant<int, 1>{});
+      wk += kDepth;
+      ak += kDepth;
+      st = st_sum - st;
+    }
   };
-#pragma clang loop unroll(disable)
-  for (int kb = 0; kb < nbK; ++kb) {
-    // A matrix instruction's multiply-adds follow two instructions later. The
-    // next step begins before this one's last weight fragment is used, so its
-    // first reads run under those instructions.
-    const bool more = kb + 1 < nbK;
+  auto zero_tail = [&](int kb) {  // zeros for the weights past the end of K
+    if (kb == nbK - 1 && end_chunks < 8) {
+      const int me = thread_of(wave);
+      if (static_cast<int>(chunk_of(me)) >= end_chunks) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          reinterpret_cast<uint4*>(sh.stage[kb & 1])[i * 512 + me] = make_uint4(0, 0, 0, 0);
+      }
+      wait_reads();
+    }
+  };
+
+  // One step. LOAD: there is a step kb + 2 to load; MORE: there is a step kb + 1.
+  // That one begins before this one's last weight fragment is used, so its first
+  // reads run under those instructions: its codes are in LDS and nobody reads
+  // this step any more; only the first part of the step after it may be in
+  // flight (scales among its loads make the wait longer than it has to be).
+  v8i w[2];
+  Wide wide[2];
+  auto step = [&](int kb, auto load, auto has_next) {
+    constexpr bool LOAD = decltype(load)::value, MORE = decltype(has_next)::value;
+    auto next = [&] {
+      if constexpr (MORE) {
+        wait_loads<LOAD ? kFirst : 0>();
+        if constexpr (!LOAD) zero_tail(kb + 1);
+        other_stage();
+      }
+    };
     if constexpr (kPrecise) {
+      // Under the matrix instructions of fragment n run the multiply-adds of
+      // n - 1 and the widening of n + 1, whose codes were read under n - 1.
+      v4f p[2][MF];
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
-        if (n == 4) middle(kb);
-        const Wide wide = widen(w[n & 1]);
-        if (n < 7) {
-          w[(n + 1) & 1] = read_w(kb, n + 1);
-        } else if (more) {
-          begin(kb + 1);
-          w[0] = read_w(kb + 1, 0);
-        }
-        v4f p[MF];
-#pragma unroll
-        for (int f = 0; f < MF; ++f) p[f] = v4f{0, 0, 0, 0};
+        if (n == 3) wait_reads();  // the step's first part is read
+        if (n == 6) next();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int f = 0; f < MF; ++f) p[f] = mfma16<1>(wide.v[j], b[f].v[j], p[f]);
-#pragma unroll
-        for (int f = 0; f < MF; ++f) {
-          add(p[f], n * MF + f);
-          spread(kb, n * MF + f);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+          for (int f = 0; f < MF; ++f) {
+            const int q = j * MF + f;
+            const v4f z = {0, 0, 0, 0};
+            p[n & 1][f] = mfma16<1>(wide[n & 1].v[j], b[f].v[j], j == 0 ? z : p[n & 1][f]);
+            if (n > 0) {
+              add1(p[(n - 1) & 1][q / 4], (n - 1) * MF + q / 4, q % 4);
+              if (q % 4 == 3) asm volatile("" : "+v"(acc[n - 1][q / 4]));
+            }
+            if (f == 0 && (n < 7 || MORE)) {
+              const v8i& c = w[(n + 1) & 1];
+              const uint2 lo = widen4<1>(static_cast<uint32_t>(c[2 * j]));
+              const uint2 hi = widen4<1>(static_cast<uint32_t>(c[2 * j + 1]));
+              wide[(n + 1) & 1].v[j] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
+            if (j == 0 && f == 0) {
+              if (n < 6) w[n & 1] = read_w(n + 2);
+              else if constexpr (MORE) w[n & 1] = read_w(n - 6);
+            }
+            if constexpr (LOAD) {
+              const int i = n * MF + f;
+              if (j == 3) spread(kb, i);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
       }
-      if (more)
+      if constexpr (MORE)
 #pragma unroll
-        for (int f = 0; f < MF; ++f) read_b(kb + 1, f);
+        for (int f = 0; f < MF; ++f) b[f] = widen(read_b(f));
+#pragma unroll
+      for (int f = 0; f < MF; ++f) add(p[1][f], 7 * MF + f);
     } else {
+      // a matrix instruction's multiply-adds follow two instructions later
       v4f p[3];
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
-        if (n == 4) middle(kb);
-        if (n < 7) {
-          w[(n + 1) & 1] = read_w(kb, n + 1);
-        } else if (more) {
-          begin(kb + 1);
-          w[0] = read_w(kb + 1, 0);
-        }
+        if (n == 4) wait_reads();  // the step's first part is read
+        if (n == 7) next();
+        if (n < 7) w[(n + 1) & 1] = read_w(n + 1);
+        else if constexpr (MORE) w[0] = read_w(0);
 #pragma unroll
         for (int f = 0; f < MF; ++f) {
           const int i = n * MF + f;
           const v4f z = {0, 0, 0, 0};
           p[i % 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[n & 1], b[f], z, 0, 0, 0, 0, 0, 0);
           if (i >= 2) add(p[(i - 2) % 3], i - 2);
-          if (n == 7 && more) read_b(kb + 1, f);
-          spread(kb, i);
+          if constexpr (MORE) if (n == 7) b[f] = read_b(f);
+          if constexpr (LOAD) spread(kb, i);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
       add(p[(8 * MF - 2) % 3], 8 * MF - 2);
       add(p[(8 * MF - 1) % 3], 8 * MF - 1);
     }
-    if (more) read_scales(kb + 1);
+    if constexpr (MORE) read_scales(kb + 1);
+  };
+
+  // all of the tile's first loads, and the stores of the tile before
+  wait_loads<0>();
+  zero_tail(0);
+#pragma unroll
+  for (int f = 0; f < MF; ++f) {
+    if constexpr (kPrecise) b[f] = widen(read_b(f));
+    else b[f] = read_b(f);
   }
+  w[0] = read_w(0);
+  if constexpr (kPrecise) {
+    wide[0] = widen(w[0]);
+    w[1] = read_w(1);
+  }
+  read_scales(0);
+  using std::bool_constant;
+  int kb = 0;
+#pragma clang loop unroll(disable)
+  for (; kb + 2 < nbK; ++kb) step(kb, bool_constant<true>{}, bool_constant<true>{});
+  if (kb + 1 < nbK) {
+    step(kb, bool_constant<false>{}, bool_constant<true>{});
+    ++kb;
+  }
+  step(kb, bool_constant<false>{}, bool_constant<false>{});
   wait_reads();  // nobody reads the stages any more
   then();
 
   const int seg = t.seg, m0 = t.m0, left = t.left, n_tile = t.n_tile;
   if constexpr (SWIGLU) {
+    uint32_t* amax = sh.amax[0];
     const int c0 = n_tile * 128 + wn * 64 + grp * 16;
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
@@ -451,14 +516,14 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, Shared& sh, const Ti
       if (c0 >= g.half) top = 0;
       top = umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16, kWave)));
       top = umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, kWave)));
-      if (grp == 0) sh.amax[wn][(f * 4 + wm) * 16 + col] = top;
+      if (grp == 0) amax[wn * Shared<UNITS>::kRows + (f * 4 + wm) * 16 + col] = top;
     }
     wait_reads();
     const int nbH = scale_blocks(g.half);
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
       const int m = (f * 4 + wm) * 16 + col;
-      const float s = block_scale(umax(sh.amax[0][m], sh.amax[1][m]));
+      const float s = block_scale(umax(amax[m], amax[Shared<UNITS>::kRows + m]));
       if (m >= left) continue;
       const size_t r = static_cast<size_t>(seg) + m0 + m;
       if (c0 < g.half) {
@@ -496,52 +561,71 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, Shared& sh, const Ti
   }
 }
 
-// A segment of R rows is cut into ceil(R / 256) tiles of whole 64-row units,
-// as even as they go, so a segment just past a multiple of 256 rows costs one
-// unit more and not one tile more.
-template <int UNITS>
-__device__ __forceinline__ int tiles_of(int rows) { return (rows + UNITS * kUnit - 1) / (UNITS * kUnit); }
+// A segment of R rows is cut into tiles of whole 64-row units, `cap` at most
+// and as even as they go, so a segment just past a whole number of tiles costs
+// one unit more and not one tile more.
+__device__ __forceinline__ int tiles_of(int rows, int cap) {
+  return ((rows + kUnit - 1) / kUnit + cap - 1) / cap;
+}
 
 template <bool SWIGLU, int ACT, bool F32>
 __global__ __launch_bounds__(kGemmThreads, 2) void expert_gemm_kernel(GemmArgs g) {
-  constexpr int kUnits = SWIGLU || F32 ? 3 : 4;
+  constexpr int kUnits = SWIGLU || F32 ? 3 : kMaxUnits;
   extern __shared__ __align__(16) char smem[];
-  Shared& sh = *reinterpret_cast<Shared*>(smem);
-  const int tid = threadIdx.x, lane = tid & 63;
+  Shared<kUnits>& sh = *reinterpret_cast<Shared<kUnits>*>(smem);
+  static_assert(sizeof(Shared<kUnits>) <= 160 * 1024, "one block's LDS");
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  // every expert's rows and first tile. Counts are cut so that they never add
-  // up to more than the rows there are, whatever the table holds.
+  // Every expert's first tile. Counts are cut so that they never add up to more
+  // than the rows there are, whatever the table holds.
   if (tid < kWave) {
-    const int per = (g.E + kWave - 1) / kWave, e0 = lane * per;
+    const int per = (g.E + kWave - 1) / kWave, e0 = lane * per, e1 = min(g.E, e0 + per);
     int sum = 0;
-    for (int e = e0; e < min(g.E, e0 + per); ++e) sum += min(max(0, g.counts[e]), g.rows - sum);
+    for (int e = e0; e < e1; ++e) sum += min(max(0, g.counts[e]), g.rows - sum);
     // partial sums stay below 2^30: 64 lanes of at most 2^24 rows
-    int before = wave_incl_scan(sum, lane) - sum;
-    int tiles = 0;
-    for (int e = e0; e < min(g.E, e0 + per); ++e) {
-      const int c = max(0, min(max(0, g.counts[e]), g.rows - before));
-      before += c;
-      sh.count[e] = c;
-      tiles += tiles_of<kUnits>(c);
+    const int before = wave_incl_scan(sum, lane) - sum;
+    // Units a tile: as many as give the shortest run of rounds. A round of
+    // tiles of u units takes about 2 u + 3 (a step of 4, 2 and 1 units takes
+    // 1.5, 0.85 and 0.6 us), and there are 256 tiles in it.
+    int cap = 1, best = 0x7fffffff;
+    for (int u = kUnits; u >= 1; --u) {
+      int tiles = 0, left = g.rows - before;
+      for (int e = e0; e < e1; ++e) {
+        const int c = max(0, min(max(0, g.counts[e]), left));
+        left -= c;
+        tiles += tiles_of(c, u);
+      }
+      tiles = wave_sum(tiles);
+      const long long rounds = (static_cast<long long>(tiles) * g.n_tiles + kGemmBlocks - 1) / kGemmBlocks;
+      const int cost = static_cast<int>(min(rounds * (2 * u + 3), 0x7ffffffell));
+      if (cost < best) best = cost, cap = u;
     }
-    int first = wave_incl_scan(tiles, lane) - tiles;
-    for (int e = e0; e < min(g.E, e0 + per); ++e) {
-      sh.first_tile[e] = first;
-      first += tiles_of<kUnits>(sh.count[e]);
+    int tiles = 0, left = g.rows - before;
+    for (int e = e0; e < e1; ++e) {
+      const int c = max(0, min(max(0, g.counts[e]), left));
+      left -= c;
+      sh.first_tile[e] = tiles;
+      tiles += tiles_of(c, cap);
+    }
+    const int first = wave_incl_scan(tiles, lane) - tiles;
+    for (int e = e0; e < e1; ++e) sh.first_tile[e] += first;
+    if (lane == kWave - 1) {
+      sh.row[0] = first + tiles;
+      sh.row[1] = cap;
     }
   }
   __syncthreads();
 
   // Each XCD takes one run of tiles, and its blocks neighbouring ones: an
   // expert's weights and rows then pass through one L2.
-  const int total = __builtin_amdgcn_readfirstlane(sh.first_tile[g.E - 1] + tiles_of<kUnits>(sh.count[g.E - 1])) *
-                    g.n_tiles;  // the host checked that it fits
+  const int total = __builtin_amdgcn_readfirstlane(sh.row[0]) * g.n_tiles;  // the host checked that it fits
+  const int cap = __builtin_amdgcn_readfirstlane(sh.row[1]);
   const int per_xcd = (total + kXcds - 1) / kXcds;
   const int first = static_cast<int>(blockIdx.x % kXcds) * per_xcd;
   const int last = min(total, first + per_xcd);
   auto find = [&](int t) {
     const int mt = t / g.n_tiles;
-    int lo = 0, hi = g.E;  // the last expert whose first tile is at most mt
+    int lo = 0, hi = g.E;  // the last expert whose first tile is at most mt: one with rows
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (__builtin_amdgcn_readfirstlane(sh.first_tile[mid]) <= mt) lo = mid;
@@ -549,10 +633,11 @@ __global__ __launch_bounds__(kGemmThreads, 2) void expert_gemm_kernel(GemmArgs g
     }
     Tile x;
     x.e = lo;
-    const int rows = __builtin_amdgcn_readfirstlane(sh.count[x.e]), tiles = tiles_of<kUnits>(rows);
+    const int rows = __builtin_amdgcn_readfirstlane(min(max(1, g.counts[x.e]), g.rows));
+    const int tiles = tiles_of(rows, cap);
     const int in = t - __builtin_amdgcn_readfirstlane(sh.first_tile[x.e]) * g.n_tiles;
     const int m_tile = in % tiles;
-    x.n_tile = in / tiles;
+    x.n_tile = min(in / tiles, g.n_tiles - 1);
     const int units = (rows + kUnit - 1) / kUnit, base = units / tiles, more = units % tiles;
     const int u0 = m_tile * base + min(m_tile, more);
     x.units = base + (m_tile < more ? 1 : 0);
@@ -565,11 +650,12 @@ __global__ __launch_bounds__(kGemmThreads, 2) void expert_gemm_kernel(GemmArgs g
   int t = first + static_cast<int>(blockIdx.x / kXcds);
   if (t >= last) return;
   Tile cur = find(t);
-  fill_rows(g, cur, sh.row[0]);
+  __syncthreads();  // everyone has read the table's totals
+  fill_rows(g, wave, cur, sh.row, Shared<kUnits>::kRows);
   __syncthreads();
-  Loads l = loads_of<SWIGLU>(g, cur, sh.row[0]);
-  load_ahead(g, sh, l, cur.units);
-  for (int turn = 1;; turn ^= 1) {
+  Loads l = loads_of<kUnits, SWIGLU>(g, wave, cur, sh.row);
+  load_ahead(g, wave, sh, l, cur.units);
+  for (;;) {
     // the next tile's rows are looked up while this one runs, and its first
     // loads run under this one's output
     t += kGemmBlocks / kXcds;
@@ -577,20 +663,21 @@ __global__ __launch_bounds__(kGemmThreads, 2) void expert_gemm_kernel(GemmArgs g
     Tile next = cur;
     if (more) {
       next = find(t);
-      fill_rows(g, next, sh.row[turn]);
+      wait_reads();  // everyone has read this tile's rows
+      fill_rows(g, wave, next, sh.row, Shared<kUnits>::kRows);
     }
     Loads nl = l;
     auto then = [&] {
       if (more) {
-        nl = loads_of<SWIGLU>(g, next, sh.row[turn]);
-        load_ahead(g, sh, nl, next.units);
+        nl = loads_of<kUnits, SWIGLU>(g, wave, next, sh.row);
+        load_ahead(g, wave, sh, nl, next.units);
       }
     };
     switch (cur.units) {
-      case 1: run_tile<1, SWIGLU, ACT, F32>(g, sh, cur, l, then); break;
-      case 2: run_tile<2, SWIGLU, ACT, F32>(g, sh, cur, l, then); break;
-      case 3: run_tile<3, SWIGLU, ACT, F32>(g, sh, cur, l, then); break;
-      default: run_tile<kUnits, SWIGLU, ACT, F32>(g, sh, cur, l, then); break;
+      case 1: run_tile<1, kUnits, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
+      case 2: run_tile<2, kUnits, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
+      case 3: run_tile<3, kUnits, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
+      default: run_tile<kUnits, kUnits, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
     }
     if (!more) break;
     cur = next;
@@ -602,7 +689,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void expert_gemm_kernel(GemmArgs g
 
 bool expert_gemm_fits(int T, int E, int k, int K, int n, bool gather) {
   const long long rows = static_cast<long long>(T) * k, most = 1ll << 32;
-  const long long tiles = rows / (3 * kUnit) + 1 + (rows < E ? rows : E);
+  const long long tiles = rows / kUnit + 1 + (rows < E ? rows : E);
   // with SwiGLU a tile holds 128 columns of each half: one more at most
   const long long across = (static_cast<long long>(n) + kTileN - 1) / kTileN + 1;
   return (gather ? static_cast<long long>(T) : 256) * K < most && static_cast<long long>(n) * K < most &&
@@ -635,9 +722,10 @@ hipError_t launch_expert_gemm(const void* a, const float* a_scale, const int32_t
   g.scales16 = whole_groups(a_scale, w_scale, K);
   g.n_tiles = (N + kTileN - 1) / kTileN;
   g.y = y;
-  if (out_f32) expert_gemm_kernel<false, 1, true><<<kGemmBlocks, kGemmThreads, sizeof(Shared), s>>>(g);
-  else if (act == 1) expert_gemm_kernel<false, 1, false><<<kGemmBlocks, kGemmThreads, sizeof(Shared), s>>>(g);
-  else expert_gemm_kernel<false, 2, false><<<kGemmBlocks, kGemmThreads, sizeof(Shared), s>>>(g);
+  constexpr size_t kLds = sizeof(Shared<kMaxUnits>), kLds3 = sizeof(Shared<3>);
+  if (out_f32) expert_gemm_kernel<false, 1, true><<<kGemmBlocks, kGemmThreads, kLds3, s>>>(g);
+  else if (act == 1) expert_gemm_kernel<false, 1, false><<<kGemmBlocks, kGemmThreads, kLds, s>>>(g);
+  else expert_gemm_kernel<false, 2, false><<<kGemmBlocks, kGemmThreads, kLds, s>>>(g);
   return hipGetLastError();
 }
 
@@ -664,7 +752,7 @@ hipError_t launch_expert_gemm_swiglu(const void* a, const float* a_scale, const 
   g.n_tiles = (I + 127) / 128;
   g.q = static_cast<uint8_t*>(q);
   g.q_scale = q_scale;
-  expert_gemm_kernel<true, 1, false><<<kGemmBlocks, kGemmThreads, sizeof(Shared), s>>>(g);
+  expert_gemm_kernel<true, 1, false><<<kGemmBlocks, kGemmThreads, sizeof(Shared<3>), s>>>(g);
   return hipGetLastError();
 }
 
