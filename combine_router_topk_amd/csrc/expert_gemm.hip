@@ -51,21 +51,25 @@ struct GemmArgs {
   float* q_scale;
 };
 
-// LDS: two stages, each a step of K (256 weight rows and the rows' codes); two
-// places for scales, which come for four steps at once (a step's scales of 64
-// rows lie in 64 lines of memory, and fetched one by one in each step they were
-// a third of all that the loads moved); the source rows of the next tile.
+// LDS: stages, each a step of K (256 weight rows and the rows' codes), two of a
+// tile of 3 or 4 units and three of a smaller one; two places for scales, which
+// come for four steps at once (a step's scales of 64 rows lie in 64 lines of
+// memory, and fetched one by one in each step they were a third of all that the
+// loads moved); the source rows of the next tile.
 constexpr int kWBytes = kTileN * kDepth;
-constexpr int kGroup = 4;  // steps whose scales are loaded together
+constexpr int kABytes = kUnit * kDepth;  // of one unit
+constexpr int kGroup = 4;                // steps whose scales are loaded together
+__host__ __device__ constexpr int stage_bytes(int units) { return kWBytes + units * kABytes; }
 
-template <int UNITS>
+template <int UNITS, bool AMAX>
 struct Shared {
+  static constexpr int kUnits = UNITS;
   static constexpr int kRows = UNITS * kUnit;
-  static constexpr int kStage = kWBytes + kRows * kDepth;
+  static constexpr int kStages = 2 * stage_bytes(UNITS) > 3 * stage_bytes(2) ? 2 * stage_bytes(UNITS) : 3 * stage_bytes(2);
   static constexpr int kScalePlace = (UNITS + 1) * kUnit * kGroup;  // floats: the units' rows, the weights
-  unsigned char stage[2][kStage];
+  unsigned char stages[kStages];
   float scale[2][kScalePlace];
-  uint32_t amax[2][kRows];
+  uint32_t amax[AMAX ? 2 * kRows : 1];
   uint32_t row[kRows];
   int first_tile[kMaxE];
 };
@@ -239,11 +243,11 @@ __device__ __forceinline__ void step_back(Loads& l, uint32_t by) {
 // The scales of steps 4 group .. 4 group + 3. With rows of whole 16-byte groups
 // one load takes them and lane l's lie at 4 l; else four loads take one step
 // each and step j's lie at 64 j.
-template <int UNITS>
-__device__ __forceinline__ void load_scales(const GemmArgs& g, int wave, Shared<UNITS>& sh, const Loads& l, int units,
+template <typename S>
+__device__ __forceinline__ void load_scales(const GemmArgs& g, int wave, S& sh, const Loads& l, int units,
                                             int group) {
   const uint32_t at = lds_address(sh.scale[0]) +
-                      (min(wave, units) * (kUnit * kGroup) + (group & 1) * Shared<UNITS>::kScalePlace) * 4;
+                      (min(wave, units) * (kUnit * kGroup) + (group & 1) * S::kScalePlace) * 4;
   if (g.scales16) {
     load_lds16(l.s0 + group * kGroup, l.s, at);
   } else {
@@ -254,17 +258,17 @@ __device__ __forceinline__ void load_scales(const GemmArgs& g, int wave, Shared<
 }
 
 // The loads that run before a tile's first step: all of steps 0 and 1.
-template <int UNITS>
-__device__ __forceinline__ void load_ahead(const GemmArgs& g, int wave, Shared<UNITS>& sh, Loads& l, int units) {
+template <typename S>
+__device__ __forceinline__ void load_ahead(const GemmArgs& g, int wave, S& sh, Loads& l, int units) {
   const int nbK = scale_blocks(g.K);
   load_scales(g, wave, sh, l, units, 0);
   for (int kb = 0; kb < min(nbK, 2); ++kb) {
-    const uint32_t st = lds_address(sh.stage[0]) + kb * Shared<UNITS>::kStage + wave * 1024;
-    if (kb == nbK - 1) step_back<UNITS>(l, past_end(g, wave));
+    const uint32_t st = lds_address(sh.stages) + kb * stage_bytes(units) + wave * 1024;
+    if (kb == nbK - 1) step_back<S::kUnits>(l, past_end(g, wave));
 #pragma unroll
     for (int i = 0; i < 4; ++i) load_lds16(l.w0 + kb * kDepth, l.w[i], st + i * 8192);
 #pragma unroll
-    for (int i = 0; i < UNITS; ++i)
+    for (int i = 0; i < S::kUnits; ++i)
       if (i < units) load_lds16(l.a0 + kb * kDepth, l.a[i], st + kWBytes + i * 8192);
   }
 }
@@ -272,20 +276,25 @@ __device__ __forceinline__ void load_ahead(const GemmArgs& g, int wave, Shared<U
 // The products of one tile whose first loads are under way; `then()` runs
 // between the last step and the tile's output.
 //
-// In a step the rows' codes and the first half of each wave's weight rows are
-// read by its middle, the second half by its end; each is then loaded anew for
-// the next step but one.
-template <int MF, int UNITS, bool SWIGLU, int ACT, bool F32, typename F>
-__device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, Shared<UNITS>& sh, const Tile& t, Loads& l,
+// With two stages, the rows' codes and the first half of each wave's weight rows
+// are read by a step's middle, the second half by its end; each is then loaded
+// anew for the next step but one. With three, the step before's stage is loaded
+// for the step after next, and there is no barrier in the middle: such tiles
+// have little to do in a step and wait for memory (2042 rows in 8 segments at
+// K = 1424: 1.2 us a step of two units with two stages).
+template <int MF, bool SWIGLU, int ACT, bool F32, typename S, typename F>
+__device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, const Tile& t, Loads& l,
                                          F&& then) {
   const int tid = thread_of(wave), lane = tid & 63;
   const int wn = wave & 1, wm = wave >> 1;
   const int col = lane & 15, grp = lane >> 4;
   const int nbK = scale_blocks(g.K);
   const int end_chunks = g.K / 16 - (nbK - 1) * 8;  // of the last step
-  constexpr int kFirst = 2 + MF;  // loads of each wave in a first part, without scales
+  constexpr bool kThree = MF <= 2;  // stages
+  // loads of each wave that may be in flight when a step begins, without scales
+  constexpr int kInFlight = kThree ? 4 + MF : 2 + MF;
   constexpr bool kPrecise = SWIGLU || F32;
-  constexpr int kStage = Shared<UNITS>::kStage;
+  constexpr int kStage = stage_bytes(MF), UNITS = S::kUnits;
 
   v4f acc[8][MF];
 #pragma unroll
@@ -298,26 +307,30 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, Shared<UNI
 
   // this lane's two chunks in the stage of the current step, of weight and of
   // row fragments
-  const unsigned char* const stage0 = sh.stage[0];
-  int wl = (wn * 128 + col) * 128 + ((2 * grp) ^ swizzle(col)) * 16;
-  int wh = (wn * 128 + col) * 128 + ((2 * grp + 1) ^ swizzle(col)) * 16;
-  int al = wl + kWBytes + (wm * 16 - wn * 128) * 128, ah = wh + kWBytes + (wm * 16 - wn * 128) * 128;
+  const unsigned char* const stage0 = sh.stages;
+  const int w_lo = (wn * 128 + col) * 128 + ((2 * grp) ^ swizzle(col)) * 16;
+  const int w_hi = (wn * 128 + col) * 128 + ((2 * grp + 1) ^ swizzle(col)) * 16;
+  const int w_to_a = kWBytes + (wm * 16 - wn * 128) * 128;
+  int now = 0;  // the current step's stage, in bytes
+  int wl = w_lo, wh = w_hi, al = wl + w_to_a, ah = wh + w_to_a;
   auto read2 = [&](int lo, int hi) {
     const uint4 x = *reinterpret_cast<const uint4*>(stage0 + lo), y = *reinterpret_cast<const uint4*>(stage0 + hi);
     return v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
   };
   auto read_w = [&](int n) { return read2(wl + n * 2048, wh + n * 2048); };
   auto read_b = [&](int f) { return read2(al + f * 8192, ah + f * 8192); };
-  auto other_stage = [&] {
-    wl = kStage + 2 * ((wn * 128 + col) * 128 + ((2 * grp) ^ swizzle(col)) * 16) - wl;
-    wh = kStage + 2 * ((wn * 128 + col) * 128 + ((2 * grp + 1) ^ swizzle(col)) * 16) - wh;
-    al = wl + kWBytes + (wm * 16 - wn * 128) * 128;
-    ah = wh + kWBytes + (wm * 16 - wn * 128) * 128;
+  constexpr int kLast = (kThree ? 2 : 1) * kStage;
+  auto next_stage = [&] {
+    now = now == kLast ? 0 : now + kStage;
+    wl = w_lo + now;
+    wh = w_hi + now;
+    al = wl + w_to_a;
+    ah = wh + w_to_a;
   };
   const int s_row = g.scales16 ? kGroup : 1, s_step = g.scales16 ? 1 : kUnit;
   const int sa_at = (wm * 16 + col) * s_row, sw_at = MF * kUnit * kGroup + (wn * 8 + grp) * s_row;
   auto read_scales = [&](int kb) {
-    const float* at = sh.scale[0] + ((kb / kGroup) & 1) * Shared<UNITS>::kScalePlace + (kb % kGroup) * s_step;
+    const float* at = sh.scale[0] + ((kb / kGroup) & 1) * S::kScalePlace + (kb % kGroup) * s_step;
     const float sw0 = at[sw_at], sw1 = at[sw_at + 4 * s_row];
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
@@ -336,44 +349,58 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, Shared<UNI
     asm volatile("" : "+v"(acc[i / MF][i % MF]));  // here, not after the branches of the loads
   };
 
-  // where the loads of step kb + 2 come from, and the stage they go to, that of
-  // step kb
+  // where the loads of step kb + 2 come from and the stage they go to
   const uint8_t* wk = l.w0 + 2 * kDepth;
   const uint8_t* ak = l.a0 + 2 * kDepth;
-  uint32_t st = lds_address(sh.stage[0]) + wave * 1024;
-  const uint32_t st_sum = 2 * st + kStage;
-  auto first_load = [&](int kb, auto item) {
-    constexpr int I = decltype(item)::value;
-    if constexpr (I == 0) {
-      if (kb + 3 == nbK) step_back<UNITS>(l, past_end(g, wave));
-      if ((kb + 2) % kGroup == 0) load_scales(g, wave, sh, l, MF, (kb + 2) / kGroup);
-    }
-    if constexpr (I < 2) load_lds16<I * 2 * 8192>(wk, l.w[2 * I], st);
-    else load_lds16<kWBytes + (I - 2) * 8192>(ak, l.a[I - 2], st);
+  const uint32_t lds0 = lds_address(sh.stages) + wave * 1024;
+  uint32_t st = lds0 + (kThree ? 2 * kStage : 0);
+  auto prepare = [&](int kb) {
+    if (kb + 3 == nbK) step_back<UNITS>(l, past_end(g, wave));
+    if ((kb + 2) % kGroup == 0) load_scales(g, wave, sh, l, MF, (kb + 2) / kGroup);
   };
-  auto second_load = [&](auto item) {
+  auto weight_load = [&](auto item) {
     constexpr int I = decltype(item)::value;
-    load_lds16<(1 + 2 * I) * 8192>(wk, l.w[1 + 2 * I], st);
+    load_lds16<I * 8192>(wk, l.w[I], st);
+  };
+  auto row_load = [&](auto item) {
+    constexpr int I = decltype(item)::value;
+    if constexpr (I < MF) load_lds16<kWBytes + I * 8192>(ak, l.a[I], st);
+  };
+  auto loaded = [&] {
+    wk += kDepth;
+    ak += kDepth;
+    st = st == lds0 + kLast ? lds0 : st + kStage;
   };
   using std::integral_constant;
-  // The loads are spread over a step's matrix instructions, from number 4 MF on
-  // (the first part) and from 7 MF on, once the next step has begun: issued at
-  // once they would hold up every wave.
-  constexpr int kGap = MF == 1 ? 1 : 2;
+  using C0 = integral_constant<int, 0>;
+  using C1 = integral_constant<int, 1>;
+  using C2 = integral_constant<int, 2>;
+  using C3 = integral_constant<int, 3>;
+  // The loads are spread over a step's matrix instructions: issued at once they
+  // would hold up every wave. With two stages the first part comes once everyone
+  // has read the step's, before the next step begins, and the second after
+  // that; with three all come before it. The waits count on this order.
   auto spread = [&](int kb, int i) {
-    const int j = i - 4 * MF;
-    if (j == 0) first_load(kb, integral_constant<int, 0>{});
-    if (j == 1 * kGap) first_load(kb, integral_constant<int, 1>{});
-    if (j == 2 * kGap) first_load(kb, integral_constant<int, 2>{});
-    if constexpr (MF > 1) if (j == 3 * kGap) first_load(kb, integral_constant<int, 3>{});
-    if constexpr (MF > 2) if (j == 4 * kGap) first_load(kb, integral_constant<int, 4>{});
-    if constexpr (MF > 3) if (j == 5 * kGap) first_load(kb, integral_constant<int, 5>{});
-    if (i == 7 * MF) second_load(integral_constant<int, 0>{});
-    if (i == 8 * MF - 1) {
-      second_load(integral_constant<int, 1>{});
-      wk += kDepth;
-      ak += kDepth;
-      st = st_sum - st;
+    if constexpr (kThree) {
+      if (i == 0) prepare(kb), weight_load(C0{});
+      if (i == 1 * MF) weight_load(C1{});
+      if (i == 2 * MF) weight_load(C2{});
+      if (i == 3 * MF) weight_load(C3{});
+      if (i == 4 * MF) row_load(C0{});
+      if (i == 5 * MF) row_load(C1{});
+      if (i == 6 * MF - 1) loaded();
+    } else {
+      constexpr int kStart = (kPrecise ? 3 : 4) * MF;
+      static_assert(kStart + 2 * (MF + 1) < (kPrecise ? 6 : 7) * MF, "the first part is on its way before the next step begins");
+      const int j = i - kStart;
+      if (j == 0) prepare(kb), weight_load(C0{});
+      if (j == 2) weight_load(C2{});
+      if (j == 4) row_load(C0{});
+      if (j == 6) row_load(C1{});
+      if (j == 8) row_load(C2{});
+      if (j == 10) row_load(C3{});
+      if (i == 7 * MF) weight_load(C1{});
+      if (i == 8 * MF - 1) weight_load(C3{}), loaded();
     }
   };
   auto zero_tail = [&](int kb) {  // zeros for the weights past the end of K
@@ -382,7 +409,7 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, Shared<UNI
       if (static_cast<int>(chunk_of(me)) >= end_chunks) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          reinterpret_cast<uint4*>(sh.stage[kb & 1])[i * 512 + me] = make_uint4(0, 0, 0, 0);
+          reinterpret_cast<uint4*>(sh.stages + now)[i * 512 + me] = make_uint4(0, 0, 0, 0);
       }
       wait_reads();
     }
@@ -391,7 +418,7 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, Shared<UNI
   // One step. LOAD: there is a step kb + 2 to load; MORE: there is a step kb + 1.
   // That one begins before this one's last weight fragment is used, so its first
   // reads run under those instructions: its codes are in LDS and nobody reads
-  // this step any more; only the first part of the step after it may be in
+  // this step any more; only the step after it, or its first part, may be in
   // flight (scales among its loads make the wait longer than it has to be).
   v8i w[2];
   Wide wide[2];
@@ -399,9 +426,9 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, Shared<UNI
     constexpr bool LOAD = decltype(load)::value, MORE = decltype(has_next)::value;
     auto next = [&] {
       if constexpr (MORE) {
-        wait_loads<LOAD ? kFirst : 0>();
+        wait_loads<LOAD ? kInFlight : 0>();
+        next_stage();
         if constexpr (!LOAD) zero_tail(kb + 1);
-        other_stage();
       }
     };
     if constexpr (kPrecise) {
@@ -410,7 +437,7 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, Shared<UNI
       v4f p[2][MF];
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
-        if (n == 3) wait_reads();  // the step's first part is read
+        if (!kThree && n == 3) wait_reads();  // the step's first part is read
         if (n == 6) next();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -450,7 +477,7 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, Shared<UNI
       v4f p[3];
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
-        if (n == 4) wait_reads();  // the step's first part is read
+        if (!kThree && n == 4) wait_reads();  // the step's first part is read
         if (n == 7) next();
         if (n < 7) w[(n + 1) & 1] = read_w(n + 1);
         else if constexpr (MORE) w[0] = read_w(0);
@@ -499,7 +526,7 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, Shared<UNI
 
   const int seg = t.seg, m0 = t.m0, left = t.left, n_tile = t.n_tile;
   if constexpr (SWIGLU) {
-    uint32_t* amax = sh.amax[0];
+    uint32_t* amax = sh.amax;
     const int c0 = n_tile * 128 + wn * 64 + grp * 16;
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
@@ -516,14 +543,14 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, Shared<UNI
       if (c0 >= g.half) top = 0;
       top = umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16, kWave)));
       top = umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, kWave)));
-      if (grp == 0) amax[wn * Shared<UNITS>::kRows + (f * 4 + wm) * 16 + col] = top;
+      if (grp == 0) amax[wn * S::kRows + (f * 4 + wm) * 16 + col] = top;
     }
     wait_reads();
     const int nbH = scale_blocks(g.half);
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
       const int m = (f * 4 + wm) * 16 + col;
-      const float s = block_scale(umax(amax[m], amax[Shared<UNITS>::kRows + m]));
+      const float s = block_scale(umax(amax[m], amax[S::kRows + m]));
       if (m >= left) continue;
       const size_t r = static_cast<size_t>(seg) + m0 + m;
       if (c0 < g.half) {
@@ -572,8 +599,9 @@ template <bool SWIGLU, int ACT, bool F32>
 __global__ __launch_bounds__(kGemmThreads, 2) void expert_gemm_kernel(GemmArgs g) {
   constexpr int kUnits = SWIGLU || F32 ? 3 : kMaxUnits;
   extern __shared__ __align__(16) char smem[];
-  Shared<kUnits>& sh = *reinterpret_cast<Shared<kUnits>*>(smem);
-  static_assert(sizeof(Shared<kUnits>) <= 160 * 1024, "one block's LDS");
+  using S = Shared<kUnits, SWIGLU>;
+  static_assert(sizeof(S) <= 160 * 1024, "one block's LDS");
+  S& sh = *reinterpret_cast<S*>(smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   // Every expert's first tile. Counts are cut so that they never add up to more
@@ -651,7 +679,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void expert_gemm_kernel(GemmArgs g
   if (t >= last) return;
   Tile cur = find(t);
   __syncthreads();  // everyone has read the table's totals
-  fill_rows(g, wave, cur, sh.row, Shared<kUnits>::kRows);
+  fill_rows(g, wave, cur, sh.row, S::kRows);
   __syncthreads();
   Loads l = loads_of<kUnits, SWIGLU>(g, wave, cur, sh.row);
   load_ahead(g, wave, sh, l, cur.units);
@@ -664,7 +692,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void expert_gemm_kernel(GemmArgs g
     if (more) {
       next = find(t);
       wait_reads();  // everyone has read this tile's rows
-      fill_rows(g, wave, next, sh.row, Shared<kUnits>::kRows);
+      fill_rows(g, wave, next, sh.row, S::kRows);
     }
     Loads nl = l;
     auto then = [&] {
@@ -674,10 +702,10 @@ __global__ __launch_bounds__(kGemmThreads, 2) void expert_gemm_kernel(GemmArgs g
       }
     };
     switch (cur.units) {
-      case 1: run_tile<1, kUnits, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
-      case 2: run_tile<2, kUnits, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
-      case 3: run_tile<3, kUnits, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
-      default: run_tile<kUnits, kUnits, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
+      case 1: run_tile<1, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
+      case 2: run_tile<2, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
+      case 3: run_tile<3, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
+      default: run_tile<kUnits, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
     }
     if (!more) break;
     cur = next;
@@ -722,7 +750,7 @@ hipError_t launch_expert_gemm(const void* a, const float* a_scale, const int32_t
   g.scales16 = whole_groups(a_scale, w_scale, K);
   g.n_tiles = (N + kTileN - 1) / kTileN;
   g.y = y;
-  constexpr size_t kLds = sizeof(Shared<kMaxUnits>), kLds3 = sizeof(Shared<3>);
+  constexpr size_t kLds = sizeof(Shared<kMaxUnits, false>), kLds3 = sizeof(Shared<3, false>);
   if (out_f32) expert_gemm_kernel<false, 1, true><<<kGemmBlocks, kGemmThreads, kLds3, s>>>(g);
   else if (act == 1) expert_gemm_kernel<false, 1, false><<<kGemmBlocks, kGemmThreads, kLds, s>>>(g);
   else expert_gemm_kernel<false, 2, false><<<kGemmBlocks, kGemmThreads, kLds, s>>>(g);
@@ -752,7 +780,7 @@ hipError_t launch_expert_gemm_swiglu(const void* a, const float* a_scale, const 
   g.n_tiles = (I + 127) / 128;
   g.q = static_cast<uint8_t*>(q);
   g.q_scale = q_scale;
-  expert_gemm_kernel<true, 1, false><<<kGemmBlocks, kGemmThreads, sizeof(Shared<3>), s>>>(g);
+  expert_gemm_kernel<true, 1, false><<<kGemmBlocks, kGemmThreads, sizeof(Shared<3, true>), s>>>(g);
   return hipGetLastError();
 }
 
