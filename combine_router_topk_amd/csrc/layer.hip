@@ -23,7 +23,7 @@ namespace {
 constexpr int kMaxTokens = 64;
 constexpr int kMaxPairs = kMaxTokens * kMaxK;
 constexpr int kUpThreads = 256, kUpWaves = kUpThreads / kWave;
-constexpr int kUpBlocks = 1024;  // at most; four a CU
+constexpr int kUpBlocks = 1280;  // at most; five a CU
 constexpr int kDownThreads = 512, kDownWaves = kDownThreads / kWave;
 constexpr int kRowsPerTile = 16;
 
@@ -132,21 +132,26 @@ __device__ __forceinline__ void topk_wave(const float* __restrict__ row, int E, 
 
 // ---- launch 1: top-k, gate and up products, SwiGLU ---------------------------
 
-struct UpShared {
-  int idx[kMaxPairs];         // expert of each (token, slot) pair
-  int order[kMaxPairs];       // pairs by expert, then by token
-  int item[kMaxPairs];        // (expert, group of 16 of its pairs)
-  int count[kMaxE];
-  int offset[kMaxE];
-  int items;
-  float4 part[2][kUpWaves][2][kWave];
+// LDS beside the waves' sums, sized by the call, so that five blocks fit a CU
+// for a few tokens. (One token of 256 experts, top-8, 4096 x 2048, e4m3, both
+// launches: four blocks of two steps in flight 52.0 us, five of one step 49.5.)
+struct UpTables {
+  int* idx;     // [pairs] expert of each (token, slot) pair
+  int* order;   // [pairs] pairs by expert, then by token
+  int* item;    // [pairs] (expert, group of 16 of its pairs)
+  int* count;   // [E]
+  int* offset;  // [E]
 };
+constexpr size_t up_tables_bytes(int pairs, int E) { return (3 * static_cast<size_t>(pairs) + 2 * E) * sizeof(int); }
 
 template <int ACT, bool F8, int V>
-__global__ __launch_bounds__(kUpThreads, 4) void layer_up_kernel(LayerArgs g) {
-  __shared__ UpShared sh;
+__global__ __launch_bounds__(kUpThreads, 6) void layer_up_kernel(LayerArgs g) {
+  __shared__ float4 part[2][kUpWaves][2][kWave];
+  __shared__ int items;
+  extern __shared__ int tables[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int pairs = g.T * g.k;
+  const UpTables sh{tables, tables + pairs, tables + 2 * pairs, tables + 3 * pairs, tables + 3 * pairs + g.E};
 
   for (int t = wave; t < g.T; t += kUpWaves) {
     int e;
@@ -180,7 +185,7 @@ __global__ __launch_bounds__(kUpThreads, 4) void layer_up_kernel(LayerArgs g) {
       off = __builtin_amdgcn_readlane(o + c, kWave - 1);
       it = __builtin_amdgcn_readlane(i0 + n, kWave - 1);
     }
-    if (lane == 0) sh.items = it;
+    if (lane == 0) items = it;
   }
   __syncthreads();
   for (int p = tid; p < pairs; p += kUpThreads) {
@@ -197,7 +202,7 @@ __global__ __launch_bounds__(kUpThreads, 4) void layer_up_kernel(LayerArgs g) {
   const int steps = (g.H + S::kCols - 1) / S::kCols;
   const int nbK = scale_blocks(g.H), nbN = scale_blocks(2 * g.I);
   const size_t row_bytes = static_cast<size_t>(g.H) * (F8 ? 1 : 2);
-  const int work = sh.items * n_tiles;
+  const int work = items * n_tiles;
   int turn = 0;
   for (int i = blockIdx.x; i < work; i += gridDim.x, turn ^= 1) {
     const int it = sh.item[i / n_tiles];
@@ -213,7 +218,7 @@ __global__ __launch_bounds__(kUpThreads, 4) void layer_up_kernel(LayerArgs g) {
     const float* s_upr = g.s_up + (static_cast<size_t>(e) * nbN + (g.I + n0) / kScaleBlock) * nbK;
 
     v4f gate = {0, 0, 0, 0}, up = {0, 0, 0, 0};
-    constexpr int D = F8 ? 2 : 4;  // steps in flight
+    constexpr int D = F8 ? 1 : 2;  // steps in flight
     for (int kb0 = wave; kb0 < steps; kb0 += kUpWaves * D) {
       typename S::Rows a[D], b[D];
       typename S::Cols c[D];
@@ -244,16 +249,16 @@ __global__ __launch_bounds__(kUpThreads, 4) void layer_up_kernel(LayerArgs g) {
         }
       }
     }
-    sh.part[turn][wave][0][lane] = make_float4(gate[0], gate[1], gate[2], gate[3]);
-    sh.part[turn][wave][1][lane] = make_float4(up[0], up[1], up[2], up[3]);
+    part[turn][wave][0][lane] = make_float4(gate[0], gate[1], gate[2], gate[3]);
+    part[turn][wave][1][lane] = make_float4(up[0], up[1], up[2], up[3]);
     __syncthreads();
     // thread tid sums value tid % 4 of lane tid / 4
     const int c = (tid >> 2) & 15, n = (tid >> 6) * 4 + (tid & 3);
     float zg = 0.0f, zu = 0.0f;
 #pragma unroll
     for (int wv = 0; wv < kUpWaves; ++wv) {
-      zg += reinterpret_cast<const float*>(sh.part[turn][wv][0])[tid];
-      zu += reinterpret_cast<const float*>(sh.part[turn][wv][1])[tid];
+      zg += reinterpret_cast<const float*>(part[turn][wv][0])[tid];
+      zu += reinterpret_cast<const float*>(part[turn][wv][1])[tid];
     }
     if (c < have) {
       const float h = zg / (1.0f + expf(-zg)) * zu;
@@ -279,7 +284,7 @@ struct DownShared {
 // tokens: column c of a group's instruction is token c), its waves contiguous
 // shares of the (expert, step of K) sequence.
 template <int ACT, bool F8, int TT>
-__global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs g) {
+__global__ __launch_bounds__(kDownThreads, 4) void layer_down_kernel(LayerArgs g) {
   __shared__ DownShared<TT> sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int pairs = g.T * g.k;
@@ -340,7 +345,7 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs g
       wt[u] = on[u] ? sh.w[pair] : 0.0f;
       tok[u] = static_cast<const uint16_t*>(g.h) + static_cast<size_t>(on[u] ? pair : 0) * g.I;
     }
-    constexpr int D = TT == 1 ? 4 : 2;  // steps in flight
+    constexpr int D = 2;  // steps in flight
     for (int kb0 = k0; kb0 < k1; kb0 += D) {
       typename S::Rows a[D];
       float s[D];
@@ -389,9 +394,10 @@ template <int ACT, bool F8>
 hipError_t launch(const LayerArgs& g, hipStream_t s) {
   const int items = (g.T * g.k < g.E * ((g.T + 15) / 16) ? g.T * g.k : g.E * ((g.T + 15) / 16)) * (g.I / kRowsPerTile);
   const int blocks = items < kUpBlocks ? items : kUpBlocks;
-  if (g.E <= 64) layer_up_kernel<ACT, F8, 1><<<blocks, kUpThreads, 0, s>>>(g);
-  else if (g.E <= 256) layer_up_kernel<ACT, F8, 4><<<blocks, kUpThreads, 0, s>>>(g);
-  else layer_up_kernel<ACT, F8, 16><<<blocks, kUpThreads, 0, s>>>(g);
+  const size_t lds = up_tables_bytes(g.T * g.k, g.E);
+  if (g.E <= 64) layer_up_kernel<ACT, F8, 1><<<blocks, kUpThreads, lds, s>>>(g);
+  else if (g.E <= 256) layer_up_kernel<ACT, F8, 4><<<blocks, kUpThreads, lds, s>>>(g);
+  else layer_up_kernel<ACT, F8, 16><<<blocks, kUpThreads, lds, s>>>(g);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int tiles = g.H / kRowsPerTile;
