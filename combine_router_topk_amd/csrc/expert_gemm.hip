@@ -536,7 +536,7 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, con
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float gate = acc[n][f][i], up = acc[n + 4][f][i];
-          const float h = gate / (1.0f + expf(-gate)) * up;
+          const float h = silu(gate) * up;
           acc[n][f][i] = h;
           top = umax(top, __float_as_uint(h) & 0x7fffffffu);
         }

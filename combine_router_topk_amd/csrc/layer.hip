@@ -261,7 +261,7 @@ __global__ __launch_bounds__(kUpThreads, 6) void layer_up_kernel(LayerArgs g) {
       zu += reinterpret_cast<const float*>(part[turn][wv][1])[tid];
     }
     if (c < have) {
-      const float h = zg / (1.0f + expf(-zg)) * zu;
+      const float h = silu(zg) * zu;
       static_cast<uint16_t*>(g.h)[static_cast<size_t>(sh.order[off + c]) * g.I + n0 + n] =
           static_cast<uint16_t>(pack2<ACT>(h, 0.0f));
     }

@@ -24,6 +24,21 @@ __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
   return amax / kE4m3Max;
 }
 
+// g / (1 + exp(-g)): exp(-g) as 2^t (1 + d), t the rounded product of -g and
+// log2(e) and d what its rounding and the constant's leave out; the hardware's
+// 2^t and reciprocal are within one step of fp32, so the whole is within 8 half
+// steps. A reciprocal below the normal numbers is 0: so is the result from
+// g = -87.4 down; g of -infinity gives NaN, as the formula does.
+__device__ __forceinline__ float silu(float g) {
+  constexpr float kLog2e = 1.44269504f, kRest = 1.92596299e-8f, kLn2 = 0.693147181f;
+  const float t = -g * kLog2e;
+  const float d = fmaf(-g, kLog2e, -t) - g * kRest;
+  const float e = __builtin_amdgcn_exp2f(t);
+  // beyond that range 1 + e is 1, or d is of no use: it is NaN at infinities
+  const float x = fabsf(t) < 126.0f ? fmaf(e, d * kLn2, e) : e;
+  return g * __builtin_amdgcn_rcpf(1.0f + x);
+}
+
 // Two values in the activation format, the first in the low half; one
 // conversion for both in bf16.
 template <int ACT>
