@@ -124,7 +124,8 @@ def expert_gemm(a, a_scale, src, k, w, w_scale, counts, offsets, rows):
 
 
 def silu(t):
-    return t / (1.0 + np.exp(-t))
+    with np.errstate(over="ignore"):
+        return t / (1.0 + np.exp(-t))
 
 
 def moe_layer(x, idx, w, up, down, act):

@@ -137,6 +137,30 @@ def test_swiglu(T, E, k, K, I, gather):
     assert (q[n:].float() == 7.0).all() and (s[n:] == 7.0).all()
 
 
+def test_swiglu_over_all_gates():
+    """Gates that are exact (one code times powers of two, and 1.5) and beside
+    an up value of 2^60 that shows silu where exp(-gate) is no fp32 number any
+    more: 8 u of its value, and half of fp32's last step of 2^-149."""
+    say("[case] SwiGLU over all gates")
+    E, K, I, up = 128, 16, 128, 2.0 ** 60
+    gate_codes = np.arange(256, dtype=np.uint8)[[c for c in range(256) if c & 127 != 127]]
+    sa = np.array([1.0, 1.5, 0.25, 2.0 ** -20, 2.0 ** -60], np.float32)
+    for part in (gate_codes[:127], gate_codes[127:]):
+        E, T = len(part), len(part) * len(sa)
+        a, w = np.zeros((T, K), np.uint8), np.zeros((E, 2 * I, K), np.uint8)
+        a[:, 0], w[:, :I, 0], w[:, I:, 0] = 0x38, part[:, None], 0x38
+        sw = np.broadcast_to(np.array([1.0, up], np.float32)[:, None], (E, 2, 1)).copy()
+        counts, offsets = np.full(E, len(sa), np.int32), np.arange(E, dtype=np.int32) * len(sa)
+        rows = np.tile(sa, E)
+        q, s = torch.empty(T, I, device="cuda").to(B.E4M3), torch.empty(T, 1, device="cuda")
+        B.moe_expert_gemm_swiglu(B.make_problem(T, E, 1, 8, 1, B.MOE_BF16), K, I,
+                                 *(dev(i) for i in (a, rows[:, None].copy(), None, w, sw, counts, offsets)), q, s)
+        torch.cuda.synchronize()
+        z = np.repeat(L.decode8(part), len(sa)) * rows
+        v = np.repeat((L.silu(z) * up * rows)[:, None], I, axis=1)
+        check_rows8(codes_of(q), f64(s), v, 8 * U * np.abs(v) + 2.0 ** -150 * up * rows[:, None], "q")
+
+
 def test_neighbours_do_not_leak():
     """NaN in the rows, the columns and the experts beside those a result is
     made of, where loads past the end of K, of N or of a segment would meet

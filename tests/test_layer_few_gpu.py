@@ -106,6 +106,32 @@ def test_layer_fp32_output():
     check_layer(40, 8, 2, 144, 80, B.MOE_BF16, "16 bits", B.MOE_FLAG_OUT_F32)
 
 
+@pytest.mark.parametrize("act", ACTS)
+def test_swiglu_over_all_gates(act):
+    """Gates that are exact beside an up value of 2^60 (fp16: 1) that shows
+    silu where exp(-gate) is no fp32 number any more; the down product picks
+    one inner value. The bound is the inner value's rounding, 8 u of silu and
+    half of fp32's last step."""
+    say(f"[case] SwiGLU over all gates act={act}")
+    I, H, E, T = 32, 32, 1, 64
+    up = 1.0 if act == B.MOE_F16 else 2.0 ** 60
+    gates = np.concatenate([np.linspace(-120, -60, 61), [0.0, 90.0, 448.0]])
+    x = np.zeros((T, H), np.float32)
+    x[:, 0], x[:, 1] = gates, 1.0
+    wu, wd = np.zeros((E, 2 * I, H), np.float32), np.zeros((E, H, I), np.float32)
+    wu[0, :I, 0], wu[0, I:, 1] = 1.0, up
+    wd[0, :, 3] = 1.0
+    bits = lambda a: dev(oracle.encode16(a, act), act)  # noqa: E731
+    p = B.make_problem(T, E, 1, H, 1, act, B.MOE_FLAG_OUT_F32)
+    _, w, out = run_layer(p, I, np.zeros((T, E), np.float32), oracle.encode16(x, act), bits(wu), None, bits(wd), None,
+                          act)
+    g = oracle.decode16(oracle.encode16(x, act), act)[:, 0].astype(np.float64)
+    v = np.repeat((L.silu(g) * up)[:, None], H, axis=1)
+    assert (w == 1.0).all()
+    near = 8 * U * np.abs(v) + 2.0 ** -150 * up
+    assert_within(f64(out), v, near + round_bound(np.abs(v) + near, act), "out")
+
+
 def test_every_token_on_one_expert():
     T, E = 64, 9
     logits = np.zeros((T, E), np.float32)
