@@ -141,6 +141,14 @@ __device__ __forceinline__ Wide widen(const v8i& c) {
   return o;
 }
 
+// Of the matrix instructions of a step, in their order: weight fragment and row
+// fragment; and which of three places a weight fragment is held in.
+template <int MF>
+constexpr int order_n(int i) { return i < 6 * MF ? i / MF : 6 + (i & 1); }
+template <int MF>
+constexpr int order_f(int i) { return i < 6 * MF ? i % MF : (i - 6 * MF) / 2; }
+constexpr int place(int n) { return n == 1 || n == 4 || n == 6 ? 1 : n == 2 || n == 7 ? 2 : 0; }
+
 // A tile: `left` rows (64 units at most) from row m0 of the segment that starts
 // at row `seg`, against the weights n_tile of expert e.
 struct Tile {
@@ -390,8 +398,8 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, con
       if (i == 5 * MF) row_load(C1{});
       if (i == 6 * MF - 1) loaded();
     } else {
-      constexpr int kStart = (kPrecise ? 3 : 4) * MF;
-      static_assert(kStart + 2 * (MF + 1) < (kPrecise ? 6 : 7) * MF, "the first part is on its way before the next step begins");
+      constexpr int kStart = 3 * MF;
+      static_assert(kStart + 2 * (MF + 1) < 6 * MF, "the first part is on its way before the next step begins");
       const int j = i - kStart;
       if (j == 0) prepare(kb), weight_load(C0{});
       if (j == 2) weight_load(C2{});
@@ -416,11 +424,11 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, con
   };
 
   // One step. LOAD: there is a step kb + 2 to load; MORE: there is a step kb + 1.
-  // That one begins before this one's last weight fragment is used, so its first
-  // reads run under those instructions: its codes are in LDS and nobody reads
+  // That one begins before this one's last two weight fragments are used, so its
+  // first reads run under those instructions: its codes are in LDS and nobody reads
   // this step any more; only the step after it, or its first part, may be in
   // flight (scales among its loads make the wait longer than it has to be).
-  v8i w[2];
+  v8i w[3];
   Wide wide[2];
   auto step = [&](int kb, auto load, auto has_next) {
     constexpr bool LOAD = decltype(load)::value, MORE = decltype(has_next)::value;
@@ -473,26 +481,27 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, con
 #pragma unroll
       for (int f = 0; f < MF; ++f) add(p[1][f], 7 * MF + f);
     } else {
-      // a matrix instruction's multiply-adds follow two instructions later
+      // A matrix instruction's multiply-adds follow two instructions later. The
+      // last two fragments go through the rows' fragments together, so that the
+      // next step's take their places over twice as many instructions (16384
+      // rows, top-2 of 64 experts, K = N = 4096: 612 -> 598 us).
       v4f p[3];
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        if (!kThree && n == 4) wait_reads();  // the step's first part is read
-        if (n == 7) next();
-        if (n < 7) w[(n + 1) & 1] = read_w(n + 1);
-        else if constexpr (MORE) w[0] = read_w(0);
-#pragma unroll
-        for (int f = 0; f < MF; ++f) {
-          const int i = n * MF + f;
-          const v4f z = {0, 0, 0, 0};
-          p[i % 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[n & 1], b[f], z, 0, 0, 0, 0, 0, 0);
-          if (i >= 2) add(p[(i - 2) % 3], i - 2);
-          if constexpr (MORE) if (n == 7) b[f] = read_b(f);
-          if constexpr (LOAD) spread(kb, i);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+      for (int i = 0; i < 8 * MF; ++i) {
+        const int n = order_n<MF>(i), f = order_f<MF>(i);
+        if (i == 3 * MF && !kThree) wait_reads();  // the step's first part is read
+        if (i == 6 * MF) next();
+        if (i % MF == 0 && n < 5) w[place(n + 1)] = read_w(n + 1);
+        if (i == 5 * MF) w[place(6)] = read_w(6), w[place(7)] = read_w(7);
+        if constexpr (MORE) if (i == 6 * MF) w[0] = read_w(0);
+        const v4f z = {0, 0, 0, 0};
+        p[i % 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[place(n)], b[f], z, 0, 0, 0, 0, 0, 0);
+        if (i >= 2) add(p[(i - 2) % 3], order_n<MF>(i - 2) * MF + order_f<MF>(i - 2));
+        if constexpr (MORE) if (n == 7) b[f] = read_b(f);
+        if constexpr (LOAD) spread(kb, i);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      add(p[(8 * MF - 2) % 3], 8 * MF - 2);
+      add(p[(8 * MF - 2) % 3], 7 * MF - 1);
       add(p[(8 * MF - 1) % 3], 8 * MF - 1);
     }
     if constexpr (MORE) read_scales(kb + 1);
