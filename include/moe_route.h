@@ -485,10 +485,14 @@ moe_status moe_rms_norm_backward(const moe_problem* p, const void* dy, const voi
 /* Experts' products over the routed rows, in 8 bits:
  *   y[r, n] = sum over k of a[r', k] * w[e, n, k]
  * for every row r of expert e's segment [expert_offsets[e], + counts[e]), a
- * and w being the values that the codes and scales stand for. Each block of
- * 128 products is summed by the matrix cores, the blocks with their scales in
- * fp32; y is rounded once to the activation format, or written as fp32 with
- * MOE_FLAG_OUT_F32.
+ * and w being the values that the codes and scales stand for; y is rounded
+ * once to the activation format, or written as fp32 with MOE_FLAG_OUT_F32.
+ * Each block of 128 products is summed by the matrix cores, the blocks with
+ * their scales in fp32. A 16-bit y comes from 8-bit matrix instructions, which
+ * cut a product off at 2^-13 of a power of two that the largest of its eight
+ * neighbours reaches (about 1.4e-5 of the sum for normal values); an fp32 y
+ * from 16-bit ones on the same codes, exact products summed in fp32, at about
+ * half that rate.
  *   src NULL:  r' = r, a has T*k rows in send order
  *   src given: r' = src[r] / k, a has T rows in token order (the row dispatch
  *              happens in the product's loads)
@@ -505,8 +509,10 @@ moe_status moe_rms_norm_backward(const moe_problem* p, const void* dy, const voi
  *   y               [T*k, N] in the activation format or fp32 (write)
  * Codes are 16-byte aligned. Rows in no segment are left untouched; a src
  * outside [0, T*k) is clamped into it. H of the problem is not used. Sizes
- * whose offsets would not fit the kernel's 32 bits (an expert's or the rows'
- * codes of 64 GiB or more) return MOE_ERR_UNSUPPORTED.                       */
+ * that the kernel's 32-bit offsets do not hold return MOE_ERR_UNSUPPORTED: an
+ * expert's N * K codes, and with src the T * K codes of a, are fewer than 2^32
+ * (without src a may be of any size), K is at most 2^24 - 16 then, and there are
+ * fewer than 2^30 tiles of 64 rows by 256 columns.                          */
 moe_status moe_expert_gemm(const moe_problem* p, int32_t K, int32_t N, const void* a,
                            const float* a_scale, const int32_t* src, const void* w,
                            const float* w_scale, const int32_t* counts,
@@ -519,7 +525,8 @@ moe_status moe_expert_gemm(const moe_problem* p, int32_t K, int32_t N, const voi
  *   (q[r], q_scale[r]) = 8-bit row of v[r]
  *   I   a multiple of 16; w [E, 2I, K], w_scale [E, ceil(2I/128), ceil(K/128)]
  *   q, q_scale  codes [T*k, I], 16-byte aligned, f32 [T*k, ceil(I/128)] (write)
- * The other arguments are those of moe_expert_gemm; act_dtype and the output
+ * The products are exact and summed in fp32 (see moe_expert_gemm on an fp32
+ * y). The other arguments are those of moe_expert_gemm; act_dtype and the output
  * flag are not used.                                                         */
 moe_status moe_expert_gemm_swiglu(const moe_problem* p, int32_t K, int32_t I, const void* a,
                                   const float* a_scale, const int32_t* src, const void* w,
