@@ -563,7 +563,7 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, con
       if (m >= left) continue;
       const size_t r = static_cast<size_t>(seg) + m0 + m;
       if (c0 < g.half) {
-        const float inv = 1.0f / s;
+        const float inv = inverse(s);
         uint32_t o[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n)
