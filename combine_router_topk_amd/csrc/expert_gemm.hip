@@ -115,16 +115,18 @@ __device__ __forceinline__ void wait_reads() {
 }
 
 // Weight row of LDS row rho (0..255) of a tile. The order inside a wave's 128
-// rows gives each lane 16 neighbouring columns of the result: fragment f of a
-// group of four holds rows (a / 4) 16 + 4 f + a % 4 of the group's 64.
+// rows makes what a lane stores whole and its neighbours' follow: rows a of a
+// fragment go in fours to the four groups of lanes, and with SwiGLU the four
+// fragments of each half give a lane 16 neighbouring columns (16 bytes of
+// codes), else each two fragments 8 (16 bytes in 16 bits).
 template <bool SWIGLU>
 __device__ __forceinline__ int weight_row(const GemmArgs& g, int n_tile, int rho) {
   const int wn = rho >> 7, quad = (rho >> 6) & 1, f = (rho >> 4) & 3, a = rho & 15;
-  const int nn = (a >> 2) * 16 + f * 4 + (a & 3);
   if constexpr (SWIGLU) {
-    const int col = min(n_tile * 128 + wn * 64 + nn, g.half - 1);
+    const int col = min(n_tile * 128 + wn * 64 + (a >> 2) * 16 + f * 4 + (a & 3), g.half - 1);
     return quad * g.half + col;
   } else {
+    const int nn = (f >> 1) * 32 + (a >> 2) * 8 + (f & 1) * 4 + (a & 3);
     return min(n_tile * kTileN + wn * 128 + quad * 64 + nn, g.N - 1);
   }
 }
@@ -580,7 +582,7 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, con
       const size_t r = static_cast<size_t>(seg) + m0 + m;
 #pragma unroll
       for (int c8 = 0; c8 < 4; ++c8) {
-        const int n = n_tile * kTileN + wn * 128 + (c8 >> 1) * 64 + grp * 16 + (c8 & 1) * 8;
+        const int n = n_tile * kTileN + wn * 128 + c8 * 32 + grp * 8;
         if (n >= g.N) continue;
         const v4f lo = acc[c8 * 2][f], hi = acc[c8 * 2 + 1][f];
         if constexpr (F32) {
