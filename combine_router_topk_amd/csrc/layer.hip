@@ -11,7 +11,10 @@
 // first operand, up to 16 tokens as its second). Activations stay in 16
 // bits, as a few rows are not worth rounding to 8; e4m3 weights become 16-bit
 // numbers in registers, exactly, and a block's scale is applied to the fp32
-// sum of its 128 products.
+// sum of its 128 products. One token of 256 experts, top-8, 4096 x 2048 in
+// e4m3: 30.9 us + 15.4 us for 201 MB (4.3 TB/s; starting and ending two launches
+// is the rest); 8 tokens of top-2 of 64 in bf16: 139 us, 5.05 TB/s; 32 tokens of
+// top-8 of 256, 7168 x 2048: 1.41 ms, 5.1 TB/s.
 #include "device.hpp"
 #include "launch.hpp"
 #include "quant.hpp"
