@@ -1,7 +1,7 @@
 """The root-mean-square norm and its gradient on the GPU against the oracle.
 
-Bounds (u = 2^-24): mean(h^2) takes at most 16 fused multiply-adds a lane, 6
-additions in the wave, 16 over the waves, the division and eps: 40 u; its
+Bounds (u = 2^-24): mean(h^2) takes at most 8 fused multiply-adds and 2
+additions a lane, 8 in the wave, 16 over the waves, the division and eps: under 40 u; its
 square root halves that, and the root, the reciprocal and the products with h
 and gamma add one each: v is within 25 u. Of the gradient's sums, mean(u n)
 has the same chain and three more roundings a term: 48 u of mean |u n|.
@@ -63,6 +63,26 @@ def test_norm(T, H, act):
     check_norm(x, None, g, act)
     check_norm(x, r, g, act, q=False)
     check_norm(x, None, g, act, y=False, eps=0.0)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("T,H", [(13000, 72), (7000, 136), (4099, 2872), (1600, 8200)])
+def test_norm_many_rows(T, H, act):
+    """More rows than blocks: a block takes several, the next one read ahead;
+    in place over x and over the residual too."""
+    say(f"[case] norm T={T} H={H} act={act}")
+    rng = np.random.default_rng(T)
+    x, r, g = bits16(rng, (T, H), act), bits16(rng, (T, H), act, 2.0), bits16(rng, H, act)
+    o = check_norm(x, r, g, act)
+    p = problem(T, H, act)
+    for h_is, y_is in (("x", "r"), ("r", "x")):
+        t = {"x": dev(x, act), "r": dev(r, act)}
+        q, s = torch.empty(T, H, device="cuda").to(B.E4M3), torch.empty(T, L.blocks(H), device="cuda")
+        B.moe_rms_norm(p, t["x"], t["r"], dev(g, act), EPS, t[h_is], t[y_is], q, s, None)
+        torch.cuda.synchronize()
+        assert torch.equal(t[h_is].view(torch.int16), o["h"].view(torch.int16)), (h_is, y_is)
+        assert torch.equal(t[y_is].view(torch.int16), o["y"].view(torch.int16)), (h_is, y_is)
+        assert torch.equal(q.view(torch.uint8), o["q"].view(torch.uint8)) and torch.equal(s, o["s"]), (h_is, y_is)
 
 
 @pytest.mark.parametrize("act", ACTS)
