@@ -12,9 +12,9 @@
 // bits, as a few rows are not worth rounding to 8; e4m3 weights become 16-bit
 // numbers in registers, exactly, and a block's scale is applied to the fp32
 // sum of its 128 products. One token of 256 experts, top-8, 4096 x 2048 in
-// e4m3: 30.9 us + 15.4 us for 201 MB (4.3 TB/s; starting and ending two launches
+// e4m3: 30.2 us + 16.4 us for 201 MB (4.3 TB/s; starting and ending two launches
 // is the rest); 8 tokens of top-2 of 64 in bf16: 139 us, 5.05 TB/s; 32 tokens of
-// top-8 of 256, 7168 x 2048: 1.41 ms, 5.1 TB/s.
+// top-8 of 256, 7168 x 2048: 1.43 ms, 5.0 TB/s.
 #include "device.hpp"
 #include "launch.hpp"
 #include "quant.hpp"
@@ -70,6 +70,9 @@ struct Step {
       if (c < K) r.v[j] = *reinterpret_cast<const uint4*>(row + static_cast<size_t>(c) * (F8 ? 1 : 2));
     }
   }
+  // K = 0 for a lane without a token: it loads nothing (with the loads of some
+  // other token's row in its place 50 tokens of 16 experts, top-4, 2048 x 1024 took
+  // 67 us, not 61)
   static __device__ __forceinline__ void load_cols(Cols& b, const uint16_t* tok, int kb, int grp, int K) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -231,7 +234,7 @@ __global__ __launch_bounds__(kUpThreads, 6) void layer_up_kernel(LayerArgs g) {
         const int kb = kb0 + d * kUpWaves;
         S::load_rows(a[d], gate_row, kb, grp, g.H);
         S::load_rows(b[d], up_row, kb, grp, g.H);
-        S::load_cols(c[d], tok, kb, grp, g.H);
+        S::load_cols(c[d], tok, kb, grp, r < have ? g.H : 0);
         if constexpr (F8) {
           sg[d] = kb < steps ? s_gate[kb] : 0.0f;
           su[d] = kb < steps ? s_upr[kb] : 0.0f;
@@ -364,7 +367,7 @@ __global__ __launch_bounds__(kDownThreads, 4) void layer_down_kernel(LayerArgs g
         if (!any[u]) continue;
         typename S::Cols c[D];
 #pragma unroll
-        for (int d = 0; d < D; ++d) S::load_cols(c[d], tok[u], kb0 + d, grp, kb0 + d < k1 ? g.I : 0);
+        for (int d = 0; d < D; ++d) S::load_cols(c[d], tok[u], kb0 + d, grp, on[u] && kb0 + d < k1 ? g.I : 0);
 #pragma unroll
         for (int d = 0; d < D; ++d) {
           const v4f p = S::product(a[d], c[d]);
