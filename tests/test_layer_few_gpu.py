@@ -101,6 +101,14 @@ def test_layer_many_experts_and_wide_rows(T, E, k, H, I):
     check_layer(T, E, k, H, I, B.MOE_BF16, "e4m3")
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "16 bits"])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("T,E,k,H,I", [(2, 16, 3, 4096, 48), (20, 6, 2, 4112, 32), (40, 4, 2, 4240, 16)])
+def test_layer_rows_of_256_blocks_and_more(T, E, k, H, I, act, kind):
+    """The down product's blocks take 8 waves from 256 on, 16 below."""
+    check_layer(T, E, k, H, I, act, kind)
+
+
 def test_layer_fp32_output():
     check_layer(9, 8, 2, 144, 80, B.MOE_F16, "e4m3", B.MOE_FLAG_OUT_F32)
     check_layer(40, 8, 2, 144, 80, B.MOE_BF16, "16 bits", B.MOE_FLAG_OUT_F32)
