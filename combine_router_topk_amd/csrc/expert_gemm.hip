@@ -19,7 +19,7 @@
 // 8-bit rows.
 //
 // What bounds it: with few rows an expert the weights' bytes (gate and up of 256
-// experts, 4096 x 2048, 8 rows each: 797 us, 5.4 TB/s). With hundreds of rows
+// experts, 4096 x 2048, 8 rows each: 757 us, 5.7 TB/s). With hundreds of rows
 // the chip's power. A block per CU holds 256 weight rows by up to 256 rows, as
 // much as its registers accumulate: a step of 128 codes takes 64 KiB from L2,
 // 192 KiB of LDS reads (8 waves of 128 x 64) and 256 matrix instructions with
@@ -309,7 +309,12 @@ __device__ __forceinline__ void load_ahead(const GemmArgs& g, int wave, S& sh, L
 // for the step after next, and there is no barrier in the middle: such tiles
 // have little to do in a step and wait for memory (2042 rows in 8 segments at
 // K = 1424: 1.2 us a step of two units with two stages).
-template <int MF, bool SWIGLU, int ACT, bool F32, typename S, typename F>
+//
+// THIN: a tile of at most 16 rows, as in decode. All waves take the same rows,
+// and each two fragments of the weights (with SwiGLU one of the gate's and the
+// up's beside it) where three of four would have none of the rows: gate and up of
+// 8 rows for each of 256 experts 786 -> 757 us, of 8 rows in all 42.5 -> 25.1 us.
+template <int MF, bool SWIGLU, int ACT, bool F32, bool THIN, typename S, typename F>
 __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, const Tile& t, Loads& l,
                                          F&& then) {
   const int tid = thread_of(wave), lane = tid & 63;
@@ -322,10 +327,12 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, con
   constexpr int kInFlight = kThree ? 4 + MF : 2 + MF;
   constexpr bool kPrecise = SWIGLU || F32;
   constexpr int kStage = stage_bytes(MF), UNITS = S::kUnits;
+  constexpr int kFrags = THIN ? 2 : 8;  // of the weights, a wave
+  static_assert(!THIN || MF == 1, "one unit");
 
-  v4f acc[8][MF];
+  v4f acc[kFrags][MF];
 #pragma unroll
-  for (int n = 0; n < 8; ++n)
+  for (int n = 0; n < kFrags; ++n)
 #pragma unroll
     for (int f = 0; f < MF; ++f) acc[n][f] = v4f{0, 0, 0, 0};
   using Frag = std::conditional_t<kPrecise, Wide, v8i>;
@@ -335,20 +342,24 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, con
   // this lane's two chunks in the stage of the current step, of weight and of
   // row fragments
   const unsigned char* const stage0 = sh.stages;
-  const int w_lo = (wn * 128 + col) * 128 + ((2 * grp) ^ swizzle(col)) * 16;
-  const int w_hi = (wn * 128 + col) * 128 + ((2 * grp + 1) ^ swizzle(col)) * 16;
-  const int w_to_a = kWBytes + (wm * 16 - wn * 128) * 128;
+  // a wave's first fragment, and how far the next one is
+  const int w_row = wn * 128 + col + (THIN ? wm * (SWIGLU ? 16 : 32) : 0);
+  constexpr int kNext = THIN && SWIGLU ? 64 * 128 : 16 * 128;
+  const int a_row = col + (THIN ? 0 : wm * 16);
+  const int w_lo = w_row * 128 + ((2 * grp) ^ swizzle(col)) * 16;
+  const int w_hi = w_row * 128 + ((2 * grp + 1) ^ swizzle(col)) * 16;
+  const int w_to_a = kWBytes + (a_row - w_row) * 128;
   int now = 0;  // the current step's stage, in bytes
   int wl = w_lo, wh = w_hi, al = wl + w_to_a, ah = wh + w_to_a;
   auto read2 = [&](int lo, int hi) {
     const uint4 x = *reinterpret_cast<const uint4*>(stage0 + lo), y = *reinterpret_cast<const uint4*>(stage0 + hi);
     return v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
   };
-  auto read_w = [&](int n) { return read2(wl + n * 2048, wh + n * 2048); };
+  auto read_w = [&](int n) { return read2(wl + n * kNext, wh + n * kNext); };
   // Rows past the segment's end are zeros where all 16 of a fragment are: they
   // cost the least power, and no reads (gate and up of 8 rows for each of 256
   // experts: 866 -> 797 us).
-  const bool last_empty = ((MF - 1) * 4 + wm) * 16 >= t.left;
+  const bool last_empty = !THIN && ((MF - 1) * 4 + wm) * 16 >= t.left;
   auto read_b = [&](int f, Frag& to) {
     if (f == MF - 1 && last_empty) return;
     const v8i c = read2(al + f * 8192, ah + f * 8192);
@@ -364,7 +375,7 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, con
     ah = wh + w_to_a;
   };
   const int s_row = g.scales16 ? kGroup : 1, s_step = g.scales16 ? 1 : kUnit;
-  const int sa_at = (wm * 16 + col) * s_row, sw_at = MF * kUnit * kGroup + (wn * 8 + grp) * s_row;
+  const int sa_at = a_row * s_row, sw_at = MF * kUnit * kGroup + (wn * 8 + grp) * s_row;
   auto read_scales = [&](int kb) {
     const float* at = sh.scale[0] + ((kb / kGroup) & 1) * S::kScalePlace + (kb % kGroup) * s_step;
     const float sw0 = at[sw_at], sw1 = at[sw_at + 4 * s_row];
@@ -467,7 +478,38 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, con
         if constexpr (!LOAD) zero_tail(kb + 1);
       }
     };
-    if constexpr (kPrecise) {
+    if constexpr (THIN) {
+      if constexpr (LOAD) {
+        prepare(kb);
+        weight_load(C0{}), weight_load(C1{}), weight_load(C2{}), weight_load(C3{}), row_load(C0{});
+        loaded();
+      }
+      v4f p[2] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
+      if constexpr (kPrecise) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) wide[n] = widen(w[n]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) p[n] = mfma16<1>(wide[n].v[j], b[0].v[j], p[n]);
+      } else {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          p[n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[n], b[0], p[n], 0, 0, 0, 0, 0, 0);
+      }
+      next();
+      if constexpr (MORE) {
+        w[0] = read_w(0);
+        w[1] = read_w(1);
+        read_b(0, b[0]);
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[n][0][q] = fmaf(p[n][q], s[SWIGLU ? n : 0][0], acc[n][0][q]);
+        asm volatile("" : "+v"(acc[n][0]));  // fp32, not rounded to 16 bits in the same instruction
+      }
+    } else if constexpr (kPrecise) {
       // Under the matrix instructions of fragment n run the multiply-adds of
       // n - 1 and the widening of n + 1, whose codes were read under n - 1.
       v4f p[2][MF];
@@ -544,7 +586,9 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, con
     read_b(f, b[f]);
   }
   w[0] = read_w(0);
-  if constexpr (kPrecise) {
+  if constexpr (THIN) {
+    w[1] = read_w(1);
+  } else if constexpr (kPrecise) {
     wide[0] = widen(w[0]);
     w[1] = read_w(1);
   }
@@ -562,7 +606,30 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, con
   then();
 
   const int seg = t.seg, m0 = t.m0, left = t.left, n_tile = t.n_tile;
-  if constexpr (SWIGLU) {
+  if constexpr (THIN && SWIGLU) {
+    uint32_t* amax = sh.amax;
+    const int c0 = n_tile * 128 + wn * 64 + grp * 16 + wm * 4;
+    float h[4];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = silu(acc[0][0][i]) * acc[1][0][i];
+      top = umax(top, __float_as_uint(h[i]) & 0x7fffffffu);
+    }
+    if (c0 >= g.half) top = 0;
+    top = umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16, kWave)));
+    top = umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, kWave)));
+    if (grp == 0) amax[wave * 16 + col] = top;
+    wait_reads();
+    if (col >= left) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = umax(top, amax[i * 16 + col]);
+    const float s = block_scale(top);
+    const size_t r = static_cast<size_t>(seg) + m0 + col;
+    if (c0 < g.half)
+      *reinterpret_cast<uint32_t*>(g.q + r * g.half + c0) = quant4(h[0], h[1], h[2], h[3], inverse(s));
+    if (wave == 0 && grp == 0) g.q_scale[r * scale_blocks(g.half) + n_tile] = s;
+  } else if constexpr (SWIGLU) {
     uint32_t* amax = sh.amax;
     const int c0 = n_tile * 128 + wn * 64 + grp * 16;
 #pragma unroll
@@ -603,12 +670,12 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, con
   } else {
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
-      const int m = (f * 4 + wm) * 16 + col;
+      const int m = f * 64 + a_row;
       if (m >= left) continue;
       const size_t r = static_cast<size_t>(seg) + m0 + m;
 #pragma unroll
-      for (int c8 = 0; c8 < 4; ++c8) {
-        const int n = n_tile * kTileN + wn * 128 + c8 * 32 + grp * 8;
+      for (int c8 = 0; c8 < kFrags / 2; ++c8) {
+        const int n = n_tile * kTileN + wn * 128 + (THIN ? wm : c8) * 32 + grp * 8;
         if (n >= g.N) continue;
         const v4f lo = acc[c8 * 2][f], hi = acc[c8 * 2 + 1][f];
         if constexpr (F32) {
@@ -739,10 +806,13 @@ __global__ __launch_bounds__(kGemmThreads, 2) void expert_gemm_kernel(GemmArgs g
       }
     };
     switch (cur.units) {
-      case 1: run_tile<1, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
-      case 2: run_tile<2, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
-      case 3: run_tile<3, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
-      default: run_tile<kUnits, SWIGLU, ACT, F32>(g, wave, sh, cur, l, then); break;
+      case 1:
+        if (cur.left <= 16) run_tile<1, SWIGLU, ACT, F32, true>(g, wave, sh, cur, l, then);
+        else run_tile<1, SWIGLU, ACT, F32, false>(g, wave, sh, cur, l, then);
+        break;
+      case 2: run_tile<2, SWIGLU, ACT, F32, false>(g, wave, sh, cur, l, then); break;
+      case 3: run_tile<3, SWIGLU, ACT, F32, false>(g, wave, sh, cur, l, then); break;
+      default: run_tile<kUnits, SWIGLU, ACT, F32, false>(g, wave, sh, cur, l, then); break;
     }
     if (!more) break;
     cur = next;

@@ -266,6 +266,35 @@ def test_rows_past_four_gib():
     assert_within(f64(y[torch.from_numpy(rows).cuda()]), want, (K + K // 128 + 4) * 2 * U * mag, "y")
 
 
+@pytest.mark.parametrize("K,N", [(16, 16), (144, 272), (640, 512), (1424, 2096)])
+def test_a_row_does_not_depend_on_its_neighbours(K, N):
+    """The same rows in segments of 1 to 300: a segment of at most 16 takes
+    other waves than a larger one, and tiles have 1 to 4 units."""
+    say(f"[case] neighbours K={K} N={N}")
+    rng = np.random.default_rng(K)
+    T = 300
+    a, sa, _, w, sw, _, _ = inputs(rng, T, 1, 1, K, N, False)
+    zero = np.zeros(1, np.int32)
+    I = N // 2 // 16 * 16
+
+    def run(n):
+        inp = (a[:n], sa[:n], None, w, sw, np.array([n], np.int32), zero)
+        y = [run_gemm(n, 1, 1, K, N, inp, B.MOE_BF16), run_gemm(n, 1, 1, K, N, inp, B.MOE_F16, B.MOE_FLAG_OUT_F32)]
+        if I == 0:
+            return y
+        q, s = torch.empty(n, I, device="cuda").to(B.E4M3), torch.empty(n, L.blocks(I), device="cuda")
+        B.moe_expert_gemm_swiglu(B.make_problem(n, 1, 1, 8, 1, B.MOE_BF16), K, I,
+                                 *(dev(i) for i in (a[:n], sa[:n], None, w[:, :2 * I], sw[:, :L.blocks(2 * I)],
+                                                    inp[5], zero)), q, s)
+        torch.cuda.synchronize()
+        return y + [q, s]
+
+    want = run(T)
+    for n in (1, 3, 15, 16, 17, 33, 64, 65, 130, 250):
+        for i, (x, y) in enumerate(zip(run(n), want)):
+            assert torch.equal(x.view(torch.uint8), y[:n].contiguous().view(torch.uint8)), (n, i)
+
+
 def test_product_repeats_bit_for_bit_on_two_streams():
     T, E, k, K, N = 300, 16, 4, 512, 256
     rng = np.random.default_rng(16)
