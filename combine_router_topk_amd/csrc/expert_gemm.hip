@@ -710,10 +710,12 @@ __global__ __launch_bounds__(kGemmThreads, 2) void expert_gemm_kernel(GemmArgs g
 
   // Every expert's first tile. Counts are cut so that they never add up to more
   // than the rows there are, whatever the table holds.
+  for (int e = tid; e < g.E; e += kGemmThreads) sh.first_tile[e] = max(0, g.counts[e]);
+  __syncthreads();
   if (tid < kWave) {
     const int per = (g.E + kWave - 1) / kWave, e0 = lane * per, e1 = min(g.E, e0 + per);
     int sum = 0;
-    for (int e = e0; e < e1; ++e) sum += min(max(0, g.counts[e]), g.rows - sum);
+    for (int e = e0; e < e1; ++e) sum += min(sh.first_tile[e], g.rows - sum);
     // partial sums stay below 2^30: 64 lanes of at most 2^24 rows
     const int before = wave_incl_scan(sum, lane) - sum;
     // Units a tile: as many as give the shortest run of rounds. A round of
@@ -723,7 +725,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void expert_gemm_kernel(GemmArgs g
     for (int u = kUnits; u >= 1; --u) {
       int tiles = 0, left = g.rows - before;
       for (int e = e0; e < e1; ++e) {
-        const int c = max(0, min(max(0, g.counts[e]), left));
+        const int c = max(0, min(sh.first_tile[e], left));
         left -= c;
         tiles += tiles_of(c, u);
       }
@@ -734,7 +736,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void expert_gemm_kernel(GemmArgs g
     }
     int tiles = 0, left = g.rows - before;
     for (int e = e0; e < e1; ++e) {
-      const int c = max(0, min(max(0, g.counts[e]), left));
+      const int c = max(0, min(sh.first_tile[e], left));
       left -= c;
       sh.first_tile[e] = tiles;
       tiles += tiles_of(c, cap);
