@@ -25,7 +25,7 @@
 // 192 KiB of LDS reads (8 waves of 128 x 64) and 256 matrix instructions with
 // 1024 multiply-adds. 32768 rows of one expert, K = N = 4096: 544 us at a clock
 // of 1.63 GHz with random codes, 432 us at 2.22 GHz with codes of zero; matrix
-// cores are busy 59 % of the cycles, LDS 30 %, and 8 % go without any loads. The
+// cores are busy 59 % of the cycles, LDS 30 %; without any loads it is 8 % fewer. The
 // same rows in 64 segments: 590 us, 1.87 PFLOP/s (a library product of 8192^3 in
 // 8 bits reaches 2.66). In fp16 the widening adds 5.5 conversions to each 3 matrix
 // instructions, and the whole runs at 1.07 PFLOP/s (a bf16 library product: 1.30).
