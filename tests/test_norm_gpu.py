@@ -190,6 +190,44 @@ def test_norm_backward(T, H, act):
         assert torch.equal(dx.view(torch.int16), first[0].view(torch.int16)) and torch.equal(dg2, first[1])
 
 
+def test_norm_rows_past_four_gib():
+    """140000 rows of 16384: 2.3e9 elements, rows on both sides of 2^31
+    elements and of 4 GiB against the oracle, forward and backward."""
+    say("[case] norm of 140000 rows of 16384")
+    T, H, act = 140000, 16384, B.MOE_BF16
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(6)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    for part in x.split(20000):
+        part.normal_(generator=gen)
+    g = bits16(np.random.default_rng(6), H, act)
+    gd, p = dev(g, act), problem(T, H, act)
+    y, q = torch.empty_like(x), torch.empty(T, H, dtype=torch.uint8, device="cuda").view(B.E4M3)
+    s, rstd = torch.empty(T, H // 128, device="cuda"), torch.empty(T, device="cuda")
+    B.moe_rms_norm(p, x, None, gd, EPS, None, y, q, s, rstd)
+    rows = [0, 131071, 131072, 131073, T - 1]
+    xb = np.stack([tensor_bits(x[r]) for r in rows])
+    _, want, v = L.rms_norm(xb, None, g, EPS, act)
+    pick = lambda t: np.stack([f64(t[r]) for r in rows])  # noqa: E731
+    dv = 25 * U * np.abs(v)
+    assert_within(np.array([float(rstd[r]) for r in rows]), want, 23 * U * want, "rstd")
+    assert_within(pick(y), v, round_bound(v, act) + dv, "y")
+    check_rows8(np.stack([codes_of(q[r]) for r in rows]), pick(s), v, dv, "q")
+    # backward over y itself as dy, in place
+    yb = np.stack([tensor_bits(y[r]) for r in rows])
+    dg, ws = torch.empty(H, device="cuda"), torch.empty(B.moe_rms_norm_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    B.moe_rms_norm_backward(p, y, None, x, gd, rstd, y, dg, ws)
+    r32 = np.array([float(rstd[r]) for r in rows], np.float32)
+    want, _ = L.rms_norm_backward(yb, None, xb, g, r32, act)
+    hv, gv, dyv = (oracle.decode16(a, act).astype(np.float64) for a in (xb, g, yb))
+    r = r32[:, None].astype(np.float64)
+    n, u = hv * r, dyv * gv
+    mean, mag = (u * n).mean(axis=1, keepdims=True), np.abs(u * n).mean(axis=1, keepdims=True)
+    bound = r * (6 * U * (np.abs(u) + np.abs(n * mean)) + 48 * U * np.abs(n) * mag) + 2 * U * np.abs(want)
+    assert_within(pick(y), want, bound + round_bound(np.abs(want) + bound, act), "dx")
+    assert torch.isfinite(dg).all()
+
+
 def test_norm_backward_without_rows():
     p = problem(0, 64, B.MOE_BF16)
     dg = torch.full((64,), 3.0, device="cuda")
