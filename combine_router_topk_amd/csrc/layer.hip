@@ -1,4 +1,5 @@
-// A whole mixture-of-experts layer for at most 64 tokens, in two launches:
+// A whole mixture-of-experts layer for at most 64 tokens, in two launches, with
+// many pairs of token and expert three (the first then by itself):
 // top-k and gate weights, gate and up products with SwiGLU, then the down
 // product with the weighted combine.
 //
@@ -14,7 +15,7 @@
 // sum of its 128 products. One token of 256 experts, top-8, 4096 x 2048 in
 // e4m3: 30.2 us + 16.4 us for 201 MB (4.3 TB/s; starting and ending two launches
 // is the rest); 8 tokens of top-2 of 64 in bf16: 139 us, 5.05 TB/s; 32 tokens of
-// top-8 of 256, 7168 x 2048: 1.43 ms, 5.0 TB/s.
+// top-8 of 256, 7168 x 2048: 1.40 ms, 5.1 TB/s.
 #include "device.hpp"
 #include "launch.hpp"
 #include "quant.hpp"
@@ -26,8 +27,12 @@ namespace {
 constexpr int kMaxTokens = 64;
 constexpr int kMaxPairs = kMaxTokens * kMaxK;
 constexpr int kUpThreads = 256, kUpWaves = kUpThreads / kWave;
-constexpr int kUpBlocks = 1280;  // at most; five a CU
+// At most; five a CU with one step in flight each (one token of 256 experts, top-8,
+// 4096 x 2048, e4m3: four blocks of two steps 52.0 us, this 49.5).
+constexpr int kUpBlocks = 1280;
 constexpr int kRowsPerTile = 16;
+constexpr int kFewPairs = 224;  // (token, slot) pairs that every block of the first launch finds by itself
+constexpr int kRouteThreads = 1024;
 
 struct LayerArgs {
   const float* logits;
@@ -42,6 +47,9 @@ struct LayerArgs {
   void* h;
   void* out;
   bool out_f32;
+  int4* item;      // tables in the workspace, of more than kFewPairs pairs
+  int32_t* order;
+  int32_t* head;   // the items, and the next tile that nobody has taken
 };
 
 // One step of K for a tile of 16 weight rows and 16 tokens: 128 bytes of each
@@ -135,71 +143,127 @@ __device__ __forceinline__ void topk_wave(const float* __restrict__ row, int E, 
   }
 }
 
-// ---- launch 1: top-k, gate and up products, SwiGLU ---------------------------
+// ---- routing -----------------------------------------------------------------
 
-// LDS beside the waves' sums, sized by the call, so that five blocks fit a CU
-// for a few tokens. (One token of 256 experts, top-8, 4096 x 2048, e4m3, both
-// launches: four blocks of two steps in flight 52.0 us, five of one step 49.5.)
-struct UpTables {
-  int* idx;     // [pairs] expert of each (token, slot) pair
-  int* order;   // [pairs] pairs by expert, then by token
-  int* item;    // [pairs] (expert, group of 16 of its pairs)
-  int* count;   // [E]
-  int* offset;  // [E]
-};
-constexpr size_t up_tables_bytes(int pairs, int E) { return (3 * static_cast<size_t>(pairs) + 2 * E) * sizeof(int); }
-
-template <int ACT, bool F8, int V>
-__global__ __launch_bounds__(kUpThreads, 6) void layer_up_kernel(LayerArgs g) {
-  __shared__ float4 part[2][kUpWaves][2][kWave];
-  __shared__ int items;
-  extern __shared__ int tables[];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int pairs = g.T * g.k;
-  const UpTables sh{tables, tables + pairs, tables + 2 * pairs, tables + 3 * pairs, tables + 3 * pairs + g.E};
-
-  for (int t = wave; t < g.T; t += kUpWaves) {
-    int e;
-    uint32_t key, top;
-    topk_wave<V>(g.logits + static_cast<size_t>(t) * g.E, g.E, g.k, lane, e, key, top);
-    if (lane < g.k) sh.idx[t * g.k + lane] = e;
-    if (blockIdx.x == 0) {  // gate weights: softmax over the chosen logits in fp64
-      double ex = 0.0;
-      if (lane < g.k) ex = exp(static_cast<double>(key_logit(key)) - static_cast<double>(key_logit(top)));
-      const double sum = group_sum16_f64<kWave>(ex);
-      if (lane < g.k) {
-        g.idx[t * g.k + lane] = e;
-        g.w[t * g.k + lane] = static_cast<float>(ex / sum);
-      }
+// One token's top-k by one wave, its experts to idx[]; to memory with the gate
+// weights, a softmax over the chosen logits in fp64, if `write`.
+template <int V>
+__device__ __forceinline__ void route_token(const LayerArgs& g, int t, int lane, int* idx, bool write) {
+  int e;
+  uint32_t key, top;
+  topk_wave<V>(g.logits + static_cast<size_t>(t) * g.E, g.E, g.k, lane, e, key, top);
+  if (lane < g.k) idx[t * g.k + lane] = e;
+  if (write) {
+    double ex = 0.0;
+    if (lane < g.k) ex = exp(static_cast<double>(key_logit(key)) - static_cast<double>(key_logit(top)));
+    const double sum = group_sum16_f64<kWave>(ex);
+    if (lane < g.k) {
+      g.idx[t * g.k + lane] = e;
+      g.w[t * g.k + lane] = static_cast<float>(ex / sum);
     }
   }
-  for (int e = tid; e < g.E; e += kUpThreads) sh.count[e] = 0;
+}
+
+// What the chosen experts are made of: pairs (token, slot) by expert, then by
+// token, and items of at most 16 of one expert's: (expert, first place, pairs).
+// An expert's tokens are a mask of 64 bits, so a pair's place is a count of bits.
+struct Tables {
+  int4* item;      // [pairs]
+  int* order;      // [pairs]
+  int* idx;        // [pairs]
+  int* offset;     // [E]
+  uint32_t* mask;  // [2 E]
+  static size_t bytes(int pairs, int E) { return pairs * (sizeof(int4) + 2 * sizeof(int)) + 3 * E * sizeof(int); }
+  __device__ __forceinline__ Tables(void* lds, int pairs, int E) {
+    item = static_cast<int4*>(lds);
+    order = reinterpret_cast<int*>(item + pairs);
+    idx = order + pairs;
+    offset = idx + pairs;
+    mask = reinterpret_cast<uint32_t*>(offset + E);
+  }
+};
+
+template <int NT>
+__device__ __forceinline__ void build_tables(const LayerArgs& g, const Tables& sh, int* items) {
+  const int tid = threadIdx.x, lane = tid & 63, pairs = g.T * g.k;
+  for (int e = tid; e < 2 * g.E; e += NT) sh.mask[e] = 0;
+  __syncthreads();  // the experts of every token, too
+  for (int p = tid; p < pairs; p += NT) {
+    const int t = p / g.k;
+    atomicOr(&sh.mask[2 * sh.idx[p] + (t >> 5)], 1u << (t & 31));
+  }
   __syncthreads();
-  for (int p = tid; p < pairs; p += kUpThreads) atomicAdd(&sh.count[sh.idx[p]], 1);
-  __syncthreads();
-  if (wave == 0) {
+  if (tid < kWave) {
     int off = 0, it = 0;
     for (int e0 = 0; e0 < g.E; e0 += kWave) {
       const int e = e0 + lane;
-      const int c = e < g.E ? sh.count[e] : 0;
+      const int c = e < g.E ? __builtin_popcount(sh.mask[2 * e]) + __builtin_popcount(sh.mask[2 * e + 1]) : 0;
       const int n = (c + kRowsPerTile - 1) / kRowsPerTile;
       const int o = off + wave_incl_scan(c, lane) - c;
       const int i0 = it + wave_incl_scan(n, lane) - n;
       if (e < g.E) sh.offset[e] = o;
-      for (int i = 0; i < n; ++i) sh.item[i0 + i] = e | (i << 16);
+      for (int i = 0; i < n; ++i)
+        sh.item[i0 + i] = make_int4(e, o + i * kRowsPerTile, min(kRowsPerTile, c - i * kRowsPerTile), 0);
       off = __builtin_amdgcn_readlane(o + c, kWave - 1);
       it = __builtin_amdgcn_readlane(i0 + n, kWave - 1);
     }
-    if (lane == 0) items = it;
+    if (lane == 0) *items = it;
   }
   __syncthreads();
-  for (int p = tid; p < pairs; p += kUpThreads) {
-    const int e = sh.idx[p];
-    int rank = 0;
-    for (int o = 0; o < p; ++o) rank += sh.idx[o] == e ? 1 : 0;
+  for (int p = tid; p < pairs; p += NT) {
+    const int e = sh.idx[p], t = p / g.k;
+    const uint32_t lo = sh.mask[2 * e], hi = sh.mask[2 * e + 1], below = (1u << (t & 31)) - 1;
+    const int rank = t < 32 ? __builtin_popcount(lo & below) : __builtin_popcount(lo) + __builtin_popcount(hi & below);
     sh.order[sh.offset[e] + rank] = p;
   }
   __syncthreads();
+}
+
+// More than kFewPairs pairs are found by one block, in a launch of its own.
+template <int V>
+__global__ __launch_bounds__(kRouteThreads) void layer_route_kernel(LayerArgs g) {
+  __shared__ int items;
+  extern __shared__ __align__(16) char tables[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int pairs = g.T * g.k;
+  const Tables sh(tables, pairs, g.E);
+  for (int t = wave; t < g.T; t += kRouteThreads / kWave) route_token<V>(g, t, lane, sh.idx, true);
+  build_tables<kRouteThreads>(g, sh, &items);
+  for (int i = tid; i < items; i += kRouteThreads) g.item[i] = sh.item[i];
+  for (int p = tid; p < pairs; p += kRouteThreads) g.order[p] = sh.order[p];
+  if (tid == 0) {
+    g.head[0] = items;
+    g.head[1] = 0;
+  }
+}
+
+// ---- launch 1: top-k, gate and up products, SwiGLU ---------------------------
+
+// V > 0: every block routes the tokens itself, 0.08 us a pair, and takes tiles
+// in turn. V = 0: the tables are there, which takes a launch of 10 us, and a block
+// that is done takes the next tile that nobody has, as blocks' shares of the
+// memory's bandwidth differ by half. (8 tokens, top-4 of 64 experts: 51.8 us
+// with V > 0, 62.3 us with V = 0; 32, top-8 of 256: 1431 us and 1407 us; 64, top-16
+// of 128: 576 us and 511 us.)
+template <int ACT, bool F8, int V>
+__global__ __launch_bounds__(kUpThreads, 6) void layer_up_kernel(LayerArgs g) {
+  __shared__ float4 part[2][kUpWaves][2][kWave];
+  __shared__ int items, next_tile[2];
+  extern __shared__ __align__(16) char tables[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int pairs = g.T * g.k;
+  const Tables sh(tables, pairs, V > 0 ? g.E : 0);
+  if constexpr (V > 0) {
+    for (int t = wave; t < g.T; t += kUpWaves) route_token<V>(g, t, lane, sh.idx, blockIdx.x == 0);
+    build_tables<kUpThreads>(g, sh, &items);
+  } else {
+    if (tid == 0) items = g.head[0];
+    for (int i = tid; i < pairs; i += kUpThreads) {  // those past the items are not used
+      sh.item[i] = g.item[i];
+      sh.order[i] = g.order[i];
+    }
+    __syncthreads();
+  }
 
   using S = Step<ACT, F8>;
   const int r = lane & 15, grp = lane >> 4;
@@ -208,12 +272,16 @@ __global__ __launch_bounds__(kUpThreads, 6) void layer_up_kernel(LayerArgs g) {
   const int nbK = scale_blocks(g.H), nbN = scale_blocks(2 * g.I);
   const size_t row_bytes = static_cast<size_t>(g.H) * (F8 ? 1 : 2);
   const int work = items * n_tiles;
+  const int blocks = gridDim.x;
   int turn = 0;
-  for (int i = blockIdx.x; i < work; i += gridDim.x, turn ^= 1) {
-    const int it = sh.item[i / n_tiles];
+  for (int i = blockIdx.x; i < work; turn ^= 1) {
+    int next = i + blocks;
+    if constexpr (V == 0) {
+      if (tid == 0) next = blocks + atomicAdd(&g.head[1], 1);
+    }
+    const int4 it = sh.item[i / n_tiles];
     const int n0 = (i % n_tiles) * kRowsPerTile;
-    const int e = __builtin_amdgcn_readfirstlane(it & 0xffff), first = (it >> 16) * kRowsPerTile;
-    const int have = sh.count[e] - first, off = sh.offset[e] + first;
+    const int e = __builtin_amdgcn_readfirstlane(it.x), off = it.y, have = it.z;
     const unsigned char* gate_row = static_cast<const unsigned char*>(g.w_up) +
                                     (static_cast<size_t>(e) * 2 * g.I + n0 + r) * row_bytes;
     const unsigned char* up_row = gate_row + g.I * row_bytes;
@@ -256,7 +324,9 @@ __global__ __launch_bounds__(kUpThreads, 6) void layer_up_kernel(LayerArgs g) {
     }
     part[turn][wave][0][lane] = make_float4(gate[0], gate[1], gate[2], gate[3]);
     part[turn][wave][1][lane] = make_float4(up[0], up[1], up[2], up[3]);
+    if (V == 0 && tid == 0) next_tile[turn] = next;
     __syncthreads();
+    i = V == 0 ? __builtin_amdgcn_readfirstlane(next_tile[turn]) : next;
     // thread tid sums value tid % 4 of lane tid / 4
     const int c = (tid >> 2) & 15, n = (tid >> 6) * 4 + (tid & 3);
     float zg = 0.0f, zu = 0.0f;
@@ -400,10 +470,19 @@ template <int ACT, bool F8>
 hipError_t launch(const LayerArgs& g, hipStream_t s) {
   const int items = (g.T * g.k < g.E * ((g.T + 15) / 16) ? g.T * g.k : g.E * ((g.T + 15) / 16)) * (g.I / kRowsPerTile);
   const int blocks = items < kUpBlocks ? items : kUpBlocks;
-  const size_t lds = up_tables_bytes(g.T * g.k, g.E);
-  if (g.E <= 64) layer_up_kernel<ACT, F8, 1><<<blocks, kUpThreads, lds, s>>>(g);
-  else if (g.E <= 256) layer_up_kernel<ACT, F8, 4><<<blocks, kUpThreads, lds, s>>>(g);
-  else layer_up_kernel<ACT, F8, 16><<<blocks, kUpThreads, lds, s>>>(g);
+  const size_t lds = Tables::bytes(g.T * g.k, g.E);
+  if (g.T * g.k <= kFewPairs) {
+    if (g.E <= 64) layer_up_kernel<ACT, F8, 1><<<blocks, kUpThreads, lds, s>>>(g);
+    else if (g.E <= 256) layer_up_kernel<ACT, F8, 4><<<blocks, kUpThreads, lds, s>>>(g);
+    else layer_up_kernel<ACT, F8, 16><<<blocks, kUpThreads, lds, s>>>(g);
+  } else {
+    if (g.E <= 64) layer_route_kernel<1><<<1, kRouteThreads, lds, s>>>(g);
+    else if (g.E <= 256) layer_route_kernel<4><<<1, kRouteThreads, lds, s>>>(g);
+    else layer_route_kernel<16><<<1, kRouteThreads, lds, s>>>(g);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    layer_up_kernel<ACT, F8, 0><<<blocks, kUpThreads, Tables::bytes(g.T * g.k, 0), s>>>(g);
+  }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int tiles = g.H / kRowsPerTile;
@@ -422,15 +501,21 @@ hipError_t launch(const LayerArgs& g, hipStream_t s) {
 
 }  // namespace
 
+// The inner rows, then the tables.
+static size_t inner_bytes(int T, int k, int I) { return (static_cast<size_t>(T) * k * I * 2 + 255) / 256 * 256; }
+
 size_t layer_ws_bytes(int T, int k, int I) {
-  return (static_cast<size_t>(T) * k * I * 2 + 255) / 256 * 256;
+  const size_t pairs = static_cast<size_t>(T) * k;
+  return inner_bytes(T, k, I) + (pairs * (sizeof(int4) + sizeof(int32_t)) + 2 * sizeof(int32_t) + 255) / 256 * 256;
 }
 
 hipError_t launch_layer_few_tokens(const float* logits, const void* x, const void* w_up, const float* s_up,
                                    const void* w_down, const float* s_down, int T, int E, int k, int H, int I,
                                    int32_t* idx, float* w, void* out, void* ws, int act, bool out_f32,
                                    hipStream_t s) {
-  LayerArgs g{logits, x, w_up, s_up, w_down, s_down, T, E, k, H, I, idx, w, ws, out, out_f32};
+  int4* item = reinterpret_cast<int4*>(static_cast<char*>(ws) + inner_bytes(T, k, I));
+  int32_t* order = reinterpret_cast<int32_t*>(item + T * k);
+  LayerArgs g{logits, x, w_up, s_up, w_down, s_down, T, E, k, H, I, idx, w, ws, out, out_f32, item, order, order + T * k};
   if (act == 1) return s_up ? launch<1, true>(g, s) : launch<1, false>(g, s);
   return s_up ? launch<2, true>(g, s) : launch<2, false>(g, s);
 }
