@@ -102,6 +102,53 @@ def test_layer_many_experts_and_wide_rows(T, E, k, H, I):
 
 
 @pytest.mark.parametrize("kind", ["e4m3", "16 bits"])
+@pytest.mark.parametrize("T,E,k,H,I", [(64, 48, 8, 128, 64), (57, 200, 4, 144, 48), (45, 5, 5, 64, 528), (14, 300, 16, 64, 32),
+                                       (15, 300, 15, 64, 32)])
+def test_layer_around_224_pairs(T, E, k, H, I, kind):
+    """From 225 pairs on a block of its own routes, and tiles are taken in turn."""
+    check_layer(T, E, k, H, I, B.MOE_F16, kind)
+
+
+def test_many_pairs_on_two_streams_and_in_a_graph():
+    T, E, k, H, I, act = 64, 40, 6, 256, 512, B.MOE_BF16
+    rng = np.random.default_rng(12)
+    p = B.make_problem(T, E, k, H, 1, act)
+    wu, su, _ = weights(rng, E, 2 * I, H, act, "e4m3")
+    wd, sd, _ = weights(rng, E, H, I, act, "e4m3")
+    logits = [rng.standard_normal((T, E)).astype(np.float32) for _ in range(2)]
+    x = [bits16(rng, (T, H), act) for _ in range(2)]
+    want = [run_layer(p, I, lg, xx, wu, su, wd, sd, act) for lg, xx in zip(logits, x)]
+    ins = [(dev(lg), dev(xx, act)) for lg, xx in zip(logits, x)]
+    outs = [(torch.empty_like(want[0][0]), torch.empty_like(want[0][1]), torch.empty_like(want[0][2]),
+             torch.full((B.moe_layer_workspace_bytes(p, I),), 255, dtype=torch.uint8, device="cuda")) for _ in range(2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+
+    def call(i, stream=None):
+        B.moe_layer_few_tokens(p, I, *ins[i], wu, su, wd, sd, *outs[i], stream)
+
+    def check(i):
+        for a, b in zip(outs[i], want[i]):
+            assert torch.equal(a, b), i
+
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(2):
+            call(i, streams[i])
+    torch.cuda.synchronize()
+    check(0), check(1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0)
+    for turn in range(4):
+        for t in outs[0][:3]:
+            t.zero_()
+        call(1)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(0), check(1)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "16 bits"])
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("T,E,k,H,I", [(2, 16, 3, 4096, 48), (20, 6, 2, 4112, 32), (40, 4, 2, 4240, 16)])
 def test_layer_rows_of_256_blocks_and_more(T, E, k, H, I, act, kind):
