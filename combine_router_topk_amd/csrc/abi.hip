@@ -641,7 +641,7 @@ moe_status moe_layer_workspace_bytes(const moe_problem* p, int32_t I, size_t* by
   const char* fn = "moe_layer_workspace_bytes";
   CHECK(check_layer(p, I, fn));
   if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is NULL", fn);
-  *bytes = moe::layer_ws_bytes(p->T, p->k, I);
+  *bytes = moe::layer_ws_bytes(p->T, p->E, p->k, p->H, I);
   return MOE_OK;
 }
 
@@ -666,7 +666,7 @@ moe_status moe_layer_few_tokens(const moe_problem* p, int32_t I, const float* lo
   CHECK(need(w, 4, fn, "w"));
   CHECK(need(out, 16, fn, "out"));
   CHECK(need(ws, 256, fn, "ws"));
-  const size_t req = moe::layer_ws_bytes(p->T, p->k, I);
+  const size_t req = moe::layer_ws_bytes(p->T, p->E, p->k, p->H, I);
   if (ws_bytes < req) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, req);
   clear_stale_error();
   return hip_status(moe::launch_layer_few_tokens(logits, x, w_up, s_up, w_down, s_down, p->T, p->E, p->k,

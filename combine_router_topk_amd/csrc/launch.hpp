@@ -165,7 +165,7 @@ hipError_t launch_expert_gemm_swiglu(const void* a, const float* a_scale, const 
                                      int T, int E, int k, int K, int I, void* q, float* q_scale,
                                      hipStream_t s);
 
-size_t layer_ws_bytes(int T, int k, int I);
+size_t layer_ws_bytes(int T, int E, int k, int H, int I);
 // s_up and s_down null: weights in the activation format, else e4m3.
 hipError_t launch_layer_few_tokens(const float* logits, const void* x, const void* w_up, const float* s_up,
                                    const void* w_down, const float* s_down, int T, int E, int k, int H, int I,

@@ -1,5 +1,6 @@
 // A whole mixture-of-experts layer for at most 64 tokens, in two launches, with
-// many pairs of token and expert three (the first then by itself):
+// many pairs of token and expert three (the first then by itself), with large
+// weights one more that adds up the down product's shares:
 // top-k and gate weights, gate and up products with SwiGLU, then the down
 // product with the weighted combine.
 //
@@ -15,7 +16,7 @@
 // sum of its 128 products. One token of 256 experts, top-8, 4096 x 2048 in
 // e4m3: 30.2 us + 16.4 us for 201 MB (4.3 TB/s; starting and ending two launches
 // is the rest); 8 tokens of top-2 of 64 in bf16: 139 us, 5.05 TB/s; 32 tokens of
-// top-8 of 256, 7168 x 2048: 1.40 ms, 5.1 TB/s.
+// top-8 of 256, 7168 x 2048: 1.29 ms, 5.6 TB/s.
 #include "device.hpp"
 #include "launch.hpp"
 #include "quant.hpp"
@@ -50,6 +51,7 @@ struct LayerArgs {
   int4* item;      // tables in the workspace, of more than kFewPairs pairs
   int32_t* order;
   int32_t* head;   // the items, and the next tile that nobody has taken
+  float* part;     // [shares][T][H]: sums of the down product's shares
 };
 
 // One step of K for a tile of 16 weight rows and 16 tokens: 128 bytes of each
@@ -357,7 +359,8 @@ struct DownShared {
 
 // Each block owns 16 columns of the output for every token (TT groups of 16
 // tokens: column c of a group's instruction is token c), its waves contiguous
-// shares of the (expert, step of K) sequence.
+// parts of the (expert, step of K) sequence. With several shares blockIdx.y is the
+// share of the sequence, and layer_sum_kernel adds them up.
 template <int ACT, bool F8, int TT, int NT>
 __global__ __launch_bounds__(NT, 4) void layer_down_kernel(LayerArgs g) {
   constexpr int kThreads = NT, kWaves = NT / kWave;
@@ -392,8 +395,10 @@ __global__ __launch_bounds__(NT, 4) void layer_down_kernel(LayerArgs g) {
   const int steps = (g.I + S::kCols - 1) / S::kCols;
   const int nbK = scale_blocks(g.I), nbN = scale_blocks(g.H);
   const size_t row_bytes = static_cast<size_t>(g.I) * (F8 ? 1 : 2);
-  const int total = sh.n_active * steps;
-  int q = total / kWaves * wave + min(wave, total % kWaves);
+  const int shares = gridDim.y, share = blockIdx.y;
+  const int all = sh.n_active * steps;
+  const int total = all / shares + (share < all % shares ? 1 : 0);
+  int q = all / shares * share + min(share, all % shares) + total / kWaves * wave + min(wave, total % kWaves);
   const int q_end = q + total / kWaves + (wave < total % kWaves ? 1 : 0);
 
   v4f acc[TT];
@@ -460,10 +465,37 @@ __global__ __launch_bounds__(NT, 4) void layer_down_kernel(LayerArgs g) {
     for (int wv = 0; wv < kWaves; ++wv) z += reinterpret_cast<const float*>(sh.part[wv][u])[v];
     if (t < g.T) {
       const size_t at = static_cast<size_t>(t) * g.H + n;
-      if (g.out_f32) static_cast<float*>(g.out)[at] = z;
+      if (shares > 1) g.part[static_cast<size_t>(share) * g.T * g.H + at] = z;
+      else if (g.out_f32) static_cast<float*>(g.out)[at] = z;
       else static_cast<uint16_t*>(g.out)[at] = static_cast<uint16_t>(pack2<ACT>(z, 0.0f));
     }
   }
+}
+
+template <int ACT>
+__global__ __launch_bounds__(256) void layer_sum_kernel(LayerArgs g, int shares) {
+  const int n = g.T * g.H / 4, i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const float4* part = reinterpret_cast<const float4*>(g.part);
+  float4 z = part[i];
+  for (int y = 1; y < shares; ++y) {
+    const float4 v = part[static_cast<size_t>(y) * n + i];
+    z = make_float4(z.x + v.x, z.y + v.y, z.z + v.z, z.w + v.w);
+  }
+  if (g.out_f32) static_cast<float4*>(g.out)[i] = z;
+  else static_cast<uint2*>(g.out)[i] = make_uint2(pack2<ACT>(z.x, z.y), pack2<ACT>(z.z, z.w));
+}
+
+// Shares of the down product: with a block a tile and, say, 448 tiles, a CU has
+// one block or two, and blocks end at different times. Four blocks a tile come
+// one after the other where there is room (32 tokens, top-8 of 256 experts, 7168 x
+// 2048: 1355 -> 1286 us; 8 tokens: 492 -> 471 us), which pays for the launch that
+// adds them up where there are weights to read for some 100 us.
+constexpr int kShares = 4;
+bool in_shares(int T, int E, int k, int H, int I) {
+  const int tiles = H / kRowsPerTile;
+  const long long experts = T * k < E ? T * k : E;
+  return tiles > 256 && tiles % 256 != 0 && experts * H * I >= 1ll << 29;
 }
 
 template <int ACT, bool F8>
@@ -489,33 +521,44 @@ hipError_t launch(const LayerArgs& g, hipStream_t s) {
   // With fewer blocks than CUs a block has 16 waves (24 tokens of 64 experts,
   // top-4, 2048 x 1024 in 16 bits: 162 us with 8, 151 us), else 8 (one token of
   // 4096 x 2048 in e4m3: 50.9 us with 16, 49.4 us).
+  const int shares = in_shares(g.T, g.E, g.k, g.H, g.I) ? kShares : 1;
   auto down = [&](auto TT) {
     if (tiles < 256) layer_down_kernel<ACT, F8, TT, 1024><<<tiles, 1024, 0, s>>>(g);
-    else layer_down_kernel<ACT, F8, TT, 512><<<tiles, 512, 0, s>>>(g);
+    else layer_down_kernel<ACT, F8, TT, 512><<<dim3(tiles, shares), 512, 0, s>>>(g);
   };
   if (g.T <= 16) down(std::integral_constant<int, 1>{});
   else if (g.T <= 32) down(std::integral_constant<int, 2>{});
   else down(std::integral_constant<int, 4>{});
+  if (shares == 1) return hipGetLastError();
+  const hipError_t down_err = hipGetLastError();
+  if (down_err != hipSuccess) return down_err;
+  layer_sum_kernel<ACT><<<(g.T * g.H / 4 + 255) / 256, 256, 0, s>>>(g, shares);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// The inner rows, then the tables.
-static size_t inner_bytes(int T, int k, int I) { return (static_cast<size_t>(T) * k * I * 2 + 255) / 256 * 256; }
+// The inner rows, the tables, the shares' sums.
+static size_t whole(size_t bytes) { return (bytes + 255) / 256 * 256; }
+static size_t inner_bytes(int T, int k, int I) { return whole(static_cast<size_t>(T) * k * I * 2); }
+static size_t table_bytes(int T, int k) {
+  return whole(static_cast<size_t>(T) * k * (sizeof(int4) + sizeof(int32_t)) + 2 * sizeof(int32_t));
+}
 
-size_t layer_ws_bytes(int T, int k, int I) {
-  const size_t pairs = static_cast<size_t>(T) * k;
-  return inner_bytes(T, k, I) + (pairs * (sizeof(int4) + sizeof(int32_t)) + 2 * sizeof(int32_t) + 255) / 256 * 256;
+size_t layer_ws_bytes(int T, int E, int k, int H, int I) {
+  const size_t sums = in_shares(T, E, k, H, I) ? whole(static_cast<size_t>(kShares) * T * H * sizeof(float)) : 0;
+  return inner_bytes(T, k, I) + table_bytes(T, k) + sums;
 }
 
 hipError_t launch_layer_few_tokens(const float* logits, const void* x, const void* w_up, const float* s_up,
                                    const void* w_down, const float* s_down, int T, int E, int k, int H, int I,
                                    int32_t* idx, float* w, void* out, void* ws, int act, bool out_f32,
                                    hipStream_t s) {
-  int4* item = reinterpret_cast<int4*>(static_cast<char*>(ws) + inner_bytes(T, k, I));
+  char* tables = static_cast<char*>(ws) + inner_bytes(T, k, I);
+  int4* item = reinterpret_cast<int4*>(tables);
   int32_t* order = reinterpret_cast<int32_t*>(item + T * k);
-  LayerArgs g{logits, x, w_up, s_up, w_down, s_down, T, E, k, H, I, idx, w, ws, out, out_f32, item, order, order + T * k};
+  float* part = reinterpret_cast<float*>(tables + table_bytes(T, k));
+  LayerArgs g{logits, x, w_up, s_up, w_down, s_down, T, E, k, H, I, idx, w, ws, out, out_f32, item, order, order + T * k, part};
   if (act == 1) return s_up ? launch<1, true>(g, s) : launch<1, false>(g, s);
   return s_up ? launch<2, true>(g, s) : launch<2, false>(g, s);
 }

@@ -308,7 +308,7 @@ def run_layer(b: Buffers, l: Layer, w: ExpertWeights, stream=None) -> None:
 
 
 def layer_few_tokens(b: Buffers, w: ExpertWeights, ws: torch.Tensor, stream=None) -> None:
-    """The same layer for a few tokens in two launches or three, from b.logits and the
+    """The same layer for a few tokens in two to four launches, from b.logits and the
     16-bit rows b.x to b.out; `ws` has layer_workspace(b, I) bytes."""
     B.moe_layer_few_tokens(b.p, w.I, b.logits, b.x, w.w_up, w.s_up, w.w_down, w.s_down, b.idx, b.w,
                            b.out, ws, stream)

@@ -538,7 +538,8 @@ moe_status moe_expert_gemm_swiglu(const moe_problem* p, int32_t K, int32_t I, co
 moe_status moe_layer_workspace_bytes(const moe_problem* p, int32_t I, size_t* bytes);
 
 /* A whole mixture-of-experts layer for a few tokens (T <= 64) in two
- * launches (three for hundreds of pairs): top-k and gate weights as moe_route gives them, then
+ * launches, or up to four for hundreds of pairs and large weights: top-k and
+ * gate weights as moe_route gives them, then
  *   h[t, j] = round16(silu(g) * u),  (g; u) = w_up[e] x[t], e = idx[t, j]
  *   out[t]  = sum over j of w[t, j] * (w_down[e] h[t, j]), in fp32, rounded
  *             once to the activation format (fp32 with MOE_FLAG_OUT_F32)

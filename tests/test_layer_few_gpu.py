@@ -57,8 +57,13 @@ def check_layer(T, E, k, H, I, act, kind, flags=0, logits=None, seed=0):
     if logits is None:
         logits = rng.standard_normal((T, E)).astype(np.float32)
     x = bits16(rng, (T, H), act)
-    wu, su, up = weights(rng, E, 2 * I, H, act, kind)
-    wd, sd, down = weights(rng, E, H, I, act, kind)
+    return check_weights(p, I, logits, x, weights(rng, E, 2 * I, H, act, kind), weights(rng, E, H, I, act, kind), act)
+
+
+def check_weights(p, I, logits, x, w_up, w_down, act):
+    """The layer on these weights, as `weights` gives them, against the oracle."""
+    T, k, H, flags = p.T, p.k, p.H, p.flags
+    (wu, su, up), (wd, sd, down) = w_up, w_down
     idx, w, out = run_layer(p, I, logits, x, wu, su, wd, sd, act)
     ridx, rw = route(p, logits)
     assert torch.equal(idx, ridx) and torch.equal(w.view(torch.int32), rw.view(torch.int32))
@@ -99,6 +104,43 @@ def test_layer(T, E, k, H, I, act, kind):
                                        (1, 160, 6, 2048, 256)])
 def test_layer_many_experts_and_wide_rows(T, E, k, H, I):
     check_layer(T, E, k, H, I, B.MOE_BF16, "e4m3")
+
+
+class Chosen:
+    """The fp64 matrices of some of an operand's experts, made from the GPU's
+    codes and scales when they are asked for."""
+
+    def __init__(self, codes, scale):
+        self.codes, self.scale, self.shape, self.made = codes, scale, codes.shape, {}
+
+    def __getitem__(self, e):
+        if e not in self.made:
+            self.made[e] = L.matrix8(self.codes[int(e)].cpu().view(torch.uint8).numpy(), self.scale[int(e)].cpu().numpy())
+        return self.made[e]
+
+
+@pytest.mark.parametrize("T,k,flags", [(33, 2, 0), (64, 4, B.MOE_FLAG_OUT_F32), (7, 10, 0)])
+def test_layer_with_a_down_product_in_shares(T, k, flags):
+    """More blocks than CUs, unevenly, and weights enough for shares: 257 tiles,
+    64 experts of 4112 x 2048; tokens choose among 12 of them."""
+    say(f"[case] layer in shares T={T} k={k} flags={flags}")
+    E, H, I, act = 64, 4112, 2048, B.MOE_BF16
+    rng = np.random.default_rng(T)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(T)
+
+    def make(rows, cols):
+        c = torch.randint(0, 256, (E, rows, cols), dtype=torch.uint8, device="cuda", generator=gen)
+        c &= 0xf7  # no NaN
+        s = dev(scales(rng, (E, L.blocks(rows), L.blocks(cols)), 1 / (110 * cols ** 0.5)))
+        c = c.view(B.E4M3)
+        return c, s, Chosen(c, s)
+
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    logits[:, rng.permutation(E)[:12]] += 20
+    p = B.make_problem(T, E, k, H, 1, act, flags)
+    assert B.moe_layer_workspace_bytes(p, I) >= 4 * T * H * 4
+    check_weights(p, I, logits, bits16(rng, (T, H), act), make(2 * I, H), make(H, I), act)
 
 
 @pytest.mark.parametrize("kind", ["e4m3", "16 bits"])
