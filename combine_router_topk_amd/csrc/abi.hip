@@ -171,8 +171,10 @@ moe_status check_expert_gemm(const moe_problem* p, int32_t K, int64_t n, const v
 moe_status check_layer(const moe_problem* p, int32_t I, const char* fn) {
   CHECK(check_problem(p, fn));
   if (p->H % 16 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: H=%d is not a multiple of 16", fn, p->H);
-  if (I <= 0 || I % 16 != 0 || I > (1 << 24))
-    return fail(MOE_ERR_INVALID_ARG, "%s: I=%d is not a multiple of 16 in [16, 2^24]", fn, I);
+  if (I <= 0 || I % 16 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: I=%d is not a positive multiple of 16", fn, I);
+  // the kernels count elements of T rows of H, and columns, in 32 bits
+  if (p->H > (1 << 24)) return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d is over 2^24", fn, p->H);
+  if (I > (1 << 24)) return fail(MOE_ERR_UNSUPPORTED, "%s: I=%d is over 2^24", fn, I);
   if (p->T > MOE_MAX_FEW_TOKENS)
     return fail(MOE_ERR_UNSUPPORTED, "%s: T=%d is over %d", fn, p->T, MOE_MAX_FEW_TOKENS);
   return MOE_OK;

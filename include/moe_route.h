@@ -546,8 +546,8 @@ moe_status moe_layer_workspace_bytes(const moe_problem* p, int32_t I, size_t* by
  * Nothing is dispatched: a decode step reads the chosen experts' weights and
  * little else ([METRO] section "Add the expert-weight traffic term").
  * Activations stay in 16 bits.
- *   H and I are multiples of 16; T > MOE_MAX_FEW_TOKENS returns
- *   MOE_ERR_UNSUPPORTED. R is not used.
+ *   H and I are multiples of 16 and at most 2^24; more, and T >
+ *   MOE_MAX_FEW_TOKENS, return MOE_ERR_UNSUPPORTED. R is not used.
  *   logits  f32 [T, E] (read)       x  16-bit [T, H] (read)
  *   w_up    [E, 2I, H] (read), gate rows 0 .. I-1, up rows I .. 2I-1
  *   w_down  [E, H, I] (read)

@@ -130,6 +130,25 @@ def test_layer_limits():
     refused(lib.moe_layer_workspace_bytes(prob(T=65), 128, ctypes.byref(n)), B.MOE_ERR_UNSUPPORTED, "T=65")
 
 
+def test_layer_rows_past_the_kernels_counts():
+    """Rows whose count of elements, T H, or whose columns 32 bits do not hold
+    are refused: at T = 64, H = 2^26 + 16 the count came to 1024. Refused
+    before the workspace is looked at, so nothing is enqueued."""
+    most, n = 1 << 24, ctypes.c_size_t(0)
+    one = dict(T=64, E=1, k=1)
+    for H in (most + 16, (1 << 25) + 16, (1 << 26) + 16, (1 << 31) - 16):
+        refused(layer(prob(H=H, **one), 16, n=0), B.MOE_ERR_UNSUPPORTED, f"H={H}")
+        refused(lib.moe_layer_workspace_bytes(prob(H=H, **one), 16, ctypes.byref(n)), B.MOE_ERR_UNSUPPORTED, f"H={H}")
+    for I in (most + 16, (1 << 31) - 16):
+        refused(layer(prob(**one), I, n=0), B.MOE_ERR_UNSUPPORTED, f"I={I}")
+    # the widest rows that are taken, with the shares' sums in the workspace
+    # (shares from H I = 2^29 on, which I = 32 misses by 512)
+    assert lib.moe_layer_workspace_bytes(prob(H=most - 16, **one), 48, ctypes.byref(n)) == B.MOE_OK
+    assert n.value >= 4 * 64 * (most - 16) * 4
+    assert lib.moe_layer_workspace_bytes(prob(H=most, **one), most, ctypes.byref(n)) == B.MOE_OK
+    assert n.value >= 64 * most * 2
+
+
 def test_binding_checks_tensors_before_the_library():
     p = B.make_problem(4, 8, 2, 64, 1, B.MOE_BF16)
     with pytest.raises(ValueError, match="device tensor"):
