@@ -49,7 +49,8 @@ __device__ __forceinline__ float silu(float g) {
   float y = g * __builtin_amdgcn_rcpf(1.0f + x);
   if (ballot(t > 100.0f) != 0) {  // hardly ever
     const float r = __builtin_amdgcn_exp2f(64.0f - t);  // exp(g) 2^64: below 2^-126 the product is 0
-    if (t > 100.0f) y = g * 0x1p-64f * fmaf(r, -d, r);
+    // d has no use for an r of 0, and is infinite where t is (g below -2.36e38)
+    if (t > 100.0f) y = g * 0x1p-64f * (t < 256.0f ? fmaf(r, -d, r) : r);
   }
   return y;
 }

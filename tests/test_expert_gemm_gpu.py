@@ -161,6 +161,28 @@ def test_swiglu_over_all_gates():
         check_rows8(codes_of(q), f64(s), v, 8 * U * np.abs(v) + 2.0 ** -150 * up * rows[:, None], "q")
 
 
+def test_swiglu_at_gates_to_the_end_of_fp32():
+    """Gates that are exact, down to -FLT_MAX, where -gate log2(e) is no fp32
+    number any more and silu is -0. They spoil nothing of their block, whose
+    other gates are positive (2^-9 of the magnitude: silu is the gate), beside
+    up values of 2^-120 of it."""
+    say("[case] SwiGLU at gates to the end of fp32")
+    far = np.array([1e5, 1e20, 1e30, 2.3e38, 2.36e38, 2.4e38, 3e38, np.finfo(np.float32).max], np.float32)
+    T, K, I, up = len(far), 16, 128, 2.0 ** -120
+    a, w = np.zeros((T, K), np.uint8), np.zeros((1, 2 * I, K), np.uint8)
+    a[:, 0], w[0, :I, 0], w[0, I:, 0] = 0x38, 0x01, 0x38  # 1, 2^-9, 1
+    w[0, [0, 77], 0] = 0xb8                               # -1
+    sw = np.array([1.0, up], np.float32).reshape(1, 2, 1)
+    inp = (a, far[:, None].copy(), None, w, sw, np.array([T], np.int32), np.zeros(1, np.int32))
+    q, s = torch.empty(T, I, device="cuda").to(B.E4M3), torch.empty(T, 1, device="cuda")
+    B.moe_expert_gemm_swiglu(B.make_problem(T, 1, 1, 8, 1, B.MOE_BF16), K, I, *(dev(i) for i in inp), q, s)
+    torch.cuda.synchronize()
+    z = L.decode8(w[0, :, 0])[None] * far[:, None].astype(np.float64)
+    v = L.silu(z[:, :I]) * z[:, I:] * up
+    assert torch.isfinite(s).all(), s
+    check_rows8(codes_of(q), f64(s), v, 8 * U * np.abs(v), "q")
+
+
 def test_neighbours_do_not_leak():
     """NaN in the rows, the columns and the experts beside those a result is
     made of, where loads past the end of K, of N or of a segment would meet

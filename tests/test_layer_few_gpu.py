@@ -229,6 +229,25 @@ def test_swiglu_over_all_gates(act):
     assert_within(f64(out), v, near + round_bound(np.abs(v) + near, act), "out")
 
 
+@pytest.mark.parametrize("act", ACTS)
+def test_swiglu_at_gates_to_the_end_of_fp32(act):
+    """Gates down to nearly -FLT_MAX, where -gate log2(e) is no fp32 number any
+    more: silu is -0 and the output 0, exactly."""
+    say(f"[case] SwiGLU at gates to the end of fp32 act={act}")
+    I, H, E = 128, 16, 1
+    gates = np.array([-2.0 ** -14, -0.5, -1.0, -1.25, -1.375, -1.390625, -1.5, -1.75, -1.9921875], np.float32)
+    T = len(gates)
+    x = np.zeros((T, H), np.float32)
+    x[:, 0], x[:, 1] = gates, 1.0
+    wu, wd = np.zeros((E, 2 * I, H), np.uint8), np.zeros((E, H, I), np.uint8)
+    wu[0, :I, 0], wu[0, I:, 1], wd[0, :, 3] = 0x38, 0x38, 0x38
+    su = np.array([2.0 ** 127, 1.0], np.float32).reshape(E, 2, 1)
+    p = B.make_problem(T, E, 1, H, 1, act, B.MOE_FLAG_OUT_F32)
+    _, _, out = run_layer(p, I, np.zeros((T, E), np.float32), oracle.encode16(x, act), dev(wu), dev(su), dev(wd),
+                          dev(np.ones((E, 1, 1), np.float32)), act)
+    assert (out == 0).all(), out[:, 0]
+
+
 def test_every_token_on_one_expert():
     T, E = 64, 9
     logits = np.zeros((T, E), np.float32)
