@@ -488,11 +488,12 @@ moe_status moe_rms_norm_backward(const moe_problem* p, const void* dy, const voi
  * and w being the values that the codes and scales stand for; y is rounded
  * once to the activation format, or written as fp32 with MOE_FLAG_OUT_F32.
  * Each block of 128 products is summed by the matrix cores, the blocks with
- * their scales in fp32. A 16-bit y comes from 8-bit matrix instructions, which
- * cut a product off at 2^-13 of a power of two that the largest of its eight
- * neighbours reaches (about 1.4e-5 of the sum for normal values); an fp32 y
- * from 16-bit ones on the same codes, exact products summed in fp32, at about
- * half that rate.
+ * their scales in fp32. An fp16 or fp32 y comes from 16-bit matrix instructions
+ * on the codes: exact products, summed in fp32. A bf16 y comes from 8-bit ones,
+ * at up to twice the rate, which cut a product off at 2^-13 of a power of two
+ * that the largest of its eight neighbours reaches: at most 7 * 2^-13 of the
+ * largest product of each eight is lost. Of a sum of one sign that is 0.22 of
+ * half a bf16 step at worst (about 1.2e-5 of the sum for normal values).
  *   src NULL:  r' = r, a has T*k rows in send order
  *   src given: r' = src[r] / k, a has T rows in token order (the row dispatch
  *              happens in the product's loads)

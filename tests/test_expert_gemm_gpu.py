@@ -348,3 +348,66 @@ def test_half_a_step_of_the_output_is_reached():
     y = run_gemm(T, E, k, K, N, (a, one, None, w, np.ones((1, 1, 1), np.float32), np.array([T], np.int32),
                                  np.zeros(1, np.int32)), B.MOE_BF16)
     assert (y.float() == 256.0).all() and HALF[B.MOE_BF16] * 257 >= 1  # 257 to even
+
+
+def exact_sum_bound(y, mag, K, act):
+    """Exact products summed in fp32 (K + K / 128 + 4 truncations) and one
+    rounding to the activation format."""
+    d = (K + L.blocks(K) + 4) * 2 * U * mag
+    return d + round_bound(np.abs(y) + d, act)
+
+
+def with_outliers(K, rng, T, N):
+    """Codes of one large value beside seven small ones of one sign in every
+    group of eight, the small ones' products below 2^-13 of the large one's; in
+    every second row normal codes with one column in 128 at the format's end."""
+    a = np.full((T, K), 0x0f, np.uint8)           # 15 2^-9
+    a[:, ::8] = 0x78                              # 256
+    a[1::2] = codes8(rng, (T // 2, K)) & 0x9f     # at most 2^-3
+    a[1::2, ::128] = 0x7e                         # 448
+    return a, np.full((1, N, K), 0x38, np.uint8)  # 1
+
+
+@pytest.mark.parametrize("T", [4, 40, 150, 300])
+@pytest.mark.parametrize("K", [16, 256, 400, 1024])
+def test_fp16_sums_are_exact_beside_outliers(T, K):
+    """An fp16 row's only rounding beside fp32's is its own: with products cut
+    off below the largest of eight, the sum of 256 + 7 15 2^-9 a group came out
+    1.6 half steps low."""
+    say(f"[case] product with outliers T={T} K={K}")
+    rng, N, act = np.random.default_rng(T + K), 136, B.MOE_F16
+    a, w = with_outliers(K, rng, T, N)
+    one, seg = np.ones((T, L.blocks(K)), np.float32), (np.array([T], np.int32), np.zeros(1, np.int32))
+    inp = (a, one, None, w, np.ones((1, 2, L.blocks(K)), np.float32), *seg)
+    y, mag = L.expert_gemm(*inp[:3], 1, *inp[3:], T)
+    assert np.abs(y).max() < 65504
+    got = f64(run_gemm(T, 1, 1, K, N, inp, act))
+    print("worst error in half steps:", (np.abs(got - y) / (HALF[act] * np.abs(y))).max(), flush=True)
+    assert_within(got, y, exact_sum_bound(y, mag, K, act), "y")
+
+
+@pytest.mark.parametrize("T", [4, 40, 150, 300])
+@pytest.mark.parametrize("K", [16, 256, 400, 1024])
+def test_bf16_sums_beside_outliers(T, K):
+    """In bf16 the cut-off leaves at most 7 2^-13 of each group's largest
+    product, 0.22 of half a step of a sum of one sign."""
+    say(f"[case] product with outliers in bf16 T={T} K={K}")
+    rng, N, act = np.random.default_rng(T + K), 136, B.MOE_BF16
+    a, w = with_outliers(K, rng, T, N)
+    one, seg = np.ones((T, L.blocks(K)), np.float32), (np.array([T], np.int32), np.zeros(1, np.int32))
+    inp = (a, one, None, w, np.ones((1, 2, L.blocks(K)), np.float32), *seg)
+    y, mag = L.expert_gemm(*inp[:3], 1, *inp[3:], T)
+    got = f64(run_gemm(T, 1, 1, K, N, inp, act))
+    print("worst error in half steps:", (np.abs(got - y) / (HALF[act] * np.abs(y))).max(), flush=True)
+    lost = 7 / 8 * lost_in_groups(inp, 1, T, N)
+    assert_within(got, y, exact_sum_bound(y, mag, K, act) + lost * (1 + HALF[act]), "y")
+
+
+@pytest.mark.parametrize("T", [1, 40, 200])
+def test_fp16_rows_are_the_fp32_rows_rounded(T):
+    """The same sums under either output format, bit for bit."""
+    say(f"[case] exact sums in two formats T={T}")
+    E, k, K, N = 3, 2, 272, 520
+    inp = inputs(np.random.default_rng(T), T, E, k, K, N, True)
+    f32 = run_gemm(T, E, k, K, N, inp, B.MOE_BF16, B.MOE_FLAG_OUT_F32)
+    assert torch.equal(run_gemm(T, E, k, K, N, inp, B.MOE_F16).view(torch.int16), f32.half().view(torch.int16))
