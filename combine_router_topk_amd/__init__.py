@@ -10,7 +10,8 @@ gfx950 behind the C ABI in include/moe_route.h.
 whole path on torch-allocated device buffers. Importing the package loads
 libmoe_route.so and fails if it has not been built.
 """
-from .binding import (MOE_BF16, MOE_F16, MOE_FLAG_GREEDY_ID_ORDER, MOE_FLAG_OUT_F32,  # noqa: F401
+from .binding import (MOE_BF16, MOE_F16, MOE_FLAG_EXACT_SUMS, MOE_FLAG_GREEDY_ID_ORDER,  # noqa: F401
+                      MOE_FLAG_OUT_F32,
                       MoeError, Problem, make_problem, moe_assign_replicas, moe_combine,
                       moe_combine_backward, moe_dispatch_backward,
                       moe_dispatch, moe_expert_gemm, moe_expert_gemm_swiglu, moe_expert_standin,

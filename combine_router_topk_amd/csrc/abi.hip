@@ -46,7 +46,7 @@ moe_status hip_status(hipError_t err, const char* where) {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-constexpr uint32_t kKnownFlags = MOE_FLAG_GREEDY_ID_ORDER | MOE_FLAG_OUT_F32;
+constexpr uint32_t kKnownFlags = MOE_FLAG_GREEDY_ID_ORDER | MOE_FLAG_OUT_F32 | MOE_FLAG_EXACT_SUMS;
 
 moe_status check_problem(const moe_problem* p, const char* fn) {
   if (p == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: problem is NULL", fn);
@@ -615,6 +615,7 @@ moe_status moe_expert_gemm(const moe_problem* p, int32_t K, int32_t N, const voi
   return hip_status(moe::launch_expert_gemm(a, a_scale, src, w, w_scale, counts, expert_offsets, p->T,
                                             p->E, p->k, K, N, y, p->act_dtype,
                                             (p->flags & MOE_FLAG_OUT_F32) != 0,
+                                            (p->flags & MOE_FLAG_EXACT_SUMS) != 0,
                                             static_cast<hipStream_t>(stream)),
                     fn);
 }

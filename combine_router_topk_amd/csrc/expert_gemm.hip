@@ -14,8 +14,8 @@
 // its largest product, 8.5e-4. Normal codes lose 1.2e-5 of a sum; one large
 // product beside seven small ones of one sign in every group lost 8.0e-4, which
 // is 0.20 of half a step of a bf16 result and 1.64 of an fp16 one. So it is used
-// for bf16 results alone. fp16 and fp32 results, and the SwiGLU's, whose fp32
-// scales show it, come from the codes widened to fp16 instead, exact products
+// for bf16 results alone, and not for those of a caller who asks for exact sums.
+// These, fp16 and fp32 results, and the SwiGLU's, whose fp32 scales show it, come from the codes widened to fp16 instead, exact products
 // summed in fp32, at half the rate (EXACT below).
 // The epilogue writes z in the activation format or fp32, or takes the two
 // halves of the weights' rows as gate and up and writes silu(gate) up as
@@ -843,7 +843,7 @@ static bool whole_groups(const float* a_scale, const float* w_scale, int K) {
 hipError_t launch_expert_gemm(const void* a, const float* a_scale, const int32_t* src, const void* w,
                               const float* w_scale, const int32_t* counts, const int32_t* offsets,
                               int T, int E, int k, int K, int N, void* y, int act, bool out_f32,
-                              hipStream_t s) {
+                              bool exact, hipStream_t s) {
   GemmArgs g{};
   g.a = static_cast<const uint8_t*>(a);
   g.a_scale = a_scale;
@@ -864,6 +864,7 @@ hipError_t launch_expert_gemm(const void* a, const float* a_scale, const int32_t
   constexpr size_t kLds = sizeof(Shared<kMaxUnits, false>), kLds3 = sizeof(Shared<3, false>);
   if (out_f32) expert_gemm_kernel<false, 1, true, true><<<kGemmBlocks, kGemmThreads, kLds3, s>>>(g);
   else if (act == 1) expert_gemm_kernel<false, 1, false, true><<<kGemmBlocks, kGemmThreads, kLds3, s>>>(g);
+  else if (exact) expert_gemm_kernel<false, 2, false, true><<<kGemmBlocks, kGemmThreads, kLds3, s>>>(g);
   else expert_gemm_kernel<false, 2, false, false><<<kGemmBlocks, kGemmThreads, kLds, s>>>(g);
   return hipGetLastError();
 }

@@ -159,7 +159,7 @@ bool expert_gemm_fits(int T, int E, int k, int K, int n, bool gather);
 hipError_t launch_expert_gemm(const void* a, const float* a_scale, const int32_t* src, const void* w,
                               const float* w_scale, const int32_t* counts, const int32_t* offsets,
                               int T, int E, int k, int K, int N, void* y, int act, bool out_f32,
-                              hipStream_t s);
+                              bool exact, hipStream_t s);
 hipError_t launch_expert_gemm_swiglu(const void* a, const float* a_scale, const int32_t* src, const void* w,
                                      const float* w_scale, const int32_t* counts, const int32_t* offsets,
                                      int T, int E, int k, int K, int I, void* q, float* q_scale,

@@ -290,7 +290,8 @@ def expert_gate_up(b: Buffers, l: Layer, w: ExpertWeights, stream=None) -> None:
 
 
 def expert_down(b: Buffers, l: Layer, w: ExpertWeights, stream=None) -> None:
-    """The experts' outputs in send order (what standin writes otherwise)."""
+    """The experts' outputs in send order (what standin writes otherwise); bf16
+    rows from exact sums if the problem has MOE_FLAG_EXACT_SUMS."""
     p = b.p
     if p.flags & B.MOE_FLAG_OUT_F32:  # y stays in the activation format
         p = B.make_problem(p.T, p.E, p.k, p.H, p.R, p.act_dtype, p.flags & ~B.MOE_FLAG_OUT_F32)

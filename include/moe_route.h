@@ -70,7 +70,10 @@ enum {
    * of the default most-constrained-first order (fewest replicas, then id). */
   MOE_FLAG_GREEDY_ID_ORDER = 1u << 0,
   /* moe_combine writes fp32 rows instead of the activation format. */
-  MOE_FLAG_OUT_F32 = 1u << 1
+  MOE_FLAG_OUT_F32 = 1u << 1,
+  /* moe_expert_gemm sums exact products in fp32 for bf16 rows too. Other calls
+   * take the flag and do the same with and without it. */
+  MOE_FLAG_EXACT_SUMS = 1u << 2
 };
 
 /* Limits checked on the host. */
@@ -493,7 +496,9 @@ moe_status moe_rms_norm_backward(const moe_problem* p, const void* dy, const voi
  * at up to twice the rate, which cut a product off at 2^-13 of a power of two
  * that the largest of its eight neighbours reaches: at most 7 * 2^-13 of the
  * largest product of each eight is lost. Of a sum of one sign that is 0.22 of
- * half a bf16 step at worst (about 1.2e-5 of the sum for normal values).
+ * half a bf16 step at worst (about 1.2e-5 of the sum for normal values); where
+ * terms cancel it can be any part of the result. MOE_FLAG_EXACT_SUMS makes a
+ * bf16 y from exact products as well.
  *   src NULL:  r' = r, a has T*k rows in send order
  *   src given: r' = src[r] / k, a has T rows in token order (the row dispatch
  *              happens in the product's loads)

@@ -411,3 +411,42 @@ def test_fp16_rows_are_the_fp32_rows_rounded(T):
     inp = inputs(np.random.default_rng(T), T, E, k, K, N, True)
     f32 = run_gemm(T, E, k, K, N, inp, B.MOE_BF16, B.MOE_FLAG_OUT_F32)
     assert torch.equal(run_gemm(T, E, k, K, N, inp, B.MOE_F16).view(torch.int16), f32.half().view(torch.int16))
+
+
+@pytest.mark.parametrize("T", [4, 40, 150, 300])
+@pytest.mark.parametrize("K", [16, 256, 400, 1024])
+def test_bf16_sums_are_exact_when_asked_for(T, K):
+    """With MOE_FLAG_EXACT_SUMS nothing is cut off beside outliers, also where
+    the large products cancel and the small ones are the sum."""
+    say(f"[case] exact sums in bf16 T={T} K={K}")
+    rng, N, act = np.random.default_rng(T + K), 136, B.MOE_BF16
+    a, w = with_outliers(K, rng, T, N)
+    a[2::4, 8::16] |= 0x80  # the large ones of every second group: their sum is 0
+    a[2::4, :16] = 0x0f
+    a[2::4, 0], a[2::4, 8] = 0x78, 0xf8
+    if K % 32 == 16:
+        a[2::4, K - 16:] = 0x0f
+    one, seg = np.ones((T, L.blocks(K)), np.float32), (np.array([T], np.int32), np.zeros(1, np.int32))
+    inp = (a, one, None, w, np.ones((1, 2, L.blocks(K)), np.float32), *seg)
+    y, mag = L.expert_gemm(*inp[:3], 1, *inp[3:], T)
+    out = torch.full((T + 2, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    B.moe_expert_gemm(B.make_problem(T, 1, 1, 8, 1, act, B.MOE_FLAG_EXACT_SUMS), K, N, *(dev(i) for i in inp), out)
+    torch.cuda.synchronize()
+    assert (out[T:] == 7.0).all()
+    assert_within(f64(out[:T]), y, exact_sum_bound(y, mag, K, act), "y")
+
+
+@pytest.mark.parametrize("T", [1, 40, 200])
+def test_exact_bf16_rows_are_the_fp32_rows_rounded(T):
+    say(f"[case] exact sums in bf16 and fp32 T={T}")
+    E, k, K, N = 3, 2, 272, 520
+    for gather in (True, False):
+        inp = inputs(np.random.default_rng(T), T, E, k, K, N, gather)
+        f32 = run_gemm(T, E, k, K, N, inp, B.MOE_BF16, B.MOE_FLAG_OUT_F32)
+        both = run_gemm(T, E, k, K, N, inp, B.MOE_BF16, B.MOE_FLAG_OUT_F32 | B.MOE_FLAG_EXACT_SUMS)
+        assert torch.equal(both, f32)
+        out = torch.empty(T * k, N, dtype=torch.bfloat16, device="cuda")
+        B.moe_expert_gemm(B.make_problem(T, E, k, 8, 1, B.MOE_BF16, B.MOE_FLAG_EXACT_SUMS), K, N,
+                          *(dev(i) for i in inp), out)
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), f32.bfloat16().view(torch.int16))

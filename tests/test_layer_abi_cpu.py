@@ -175,3 +175,19 @@ def test_limits_match_the_header():
         m = re.search(rf"{name} = (\d+)", text)
         assert m and int(m.group(1)) == getattr(B, name), name
     assert [B.scale_blocks(c) for c in (1, 128, 129)] == [1, 1, 2]
+
+
+def test_flags_match_the_header():
+    import os
+    import re
+    from conftest import ROOT
+    text = open(os.path.join(ROOT, "include", "moe_route.h")).read()
+    for name in ("MOE_FLAG_GREEDY_ID_ORDER", "MOE_FLAG_OUT_F32", "MOE_FLAG_EXACT_SUMS"):
+        m = re.search(rf"{name} = 1u << (\d+)", text)
+        assert m and 1 << int(m.group(1)) == getattr(B, name), name
+    # every call takes the known flags, and no other
+    known, n = B.MOE_FLAG_EXACT_SUMS | B.MOE_FLAG_OUT_F32, ctypes.c_size_t(0)
+    assert gemm(prob(T=0, flags=known), y=None, **dict.fromkeys(("a", "sa", "w", "sw", "counts", "off"))) == B.MOE_OK
+    assert layer(prob(T=0, flags=known), 128, *(None,) * 10, n=0) == B.MOE_OK
+    assert lib.moe_workspace_bytes(prob(flags=known), ctypes.byref(n)) == B.MOE_OK
+    refused(gemm(prob(flags=B.MOE_FLAG_EXACT_SUMS << 1)), B.MOE_ERR_INVALID_ARG, "unknown flag")

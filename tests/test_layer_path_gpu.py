@@ -91,6 +91,26 @@ def test_expert_down_keeps_y_in_the_activation_format():
     assert torch.equal(outs[1][1].to(torch.bfloat16).view(torch.int16), outs[0][1].view(torch.int16))
 
 
+@pytest.mark.parametrize("flags", [B.MOE_FLAG_EXACT_SUMS, B.MOE_FLAG_EXACT_SUMS | B.MOE_FLAG_OUT_F32])
+def test_expert_down_takes_exact_sums_from_the_problem(flags):
+    """The path's y is the fp32 product of the same rows, rounded."""
+    T, E, k, H, I = 60, 4, 2, 144, 272
+    say(f"[case] path with exact sums flags={flags}")
+    rng = np.random.default_rng(3)
+    p = B.make_problem(T, E, k, H, 1, B.MOE_BF16, flags)
+    b = P.allocate(p, torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)),
+                   bits_to_tensor(bits16(rng, (T, H), B.MOE_BF16), B.MOE_BF16))
+    l, w = P.allocate_layer(b, I), expert_weights(rng, E, H, I)[0]
+    P.norm(b, l, b.x.clone(), None, torch.ones(H, dtype=torch.bfloat16, device="cuda"), EPS)
+    P.run_layer(b, l, w)
+    y = torch.empty(T * k, H, device="cuda")
+    B.moe_expert_gemm(B.make_problem(T, E, k, H, 1, B.MOE_BF16, B.MOE_FLAG_OUT_F32), I, H, l.hq, l.hq_scale, None,
+                      w.w_down, w.s_down, b.counts, b.expert_offsets, y)
+    torch.cuda.synchronize()
+    assert torch.equal(b.y.view(torch.int16).flatten(), y.bfloat16().view(torch.int16).flatten())
+    assert b.out.dtype == (torch.float32 if flags & B.MOE_FLAG_OUT_F32 else torch.bfloat16)
+
+
 @pytest.mark.parametrize("act", ACTS)
 def test_few_token_layer_against_its_parts(act):
     """The same weights through the 8-bit path and through the few-token
