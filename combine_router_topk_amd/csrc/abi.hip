@@ -184,7 +184,7 @@ moe_status check_layer(const moe_problem* p, int32_t I, const char* fn) {
 
 extern "C" {
 
-int32_t moe_version(void) { return 1 * 10000 + 3 * 100 + 0; }
+int32_t moe_version(void) { return 1 * 10000 + 4 * 100 + 0; }
 
 const char* moe_build_id(void) { return MOE_BUILD_ID; }
 

@@ -378,6 +378,8 @@ __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, con
   };
   const int s_row = g.scales16 ? kGroup : 1, s_step = g.scales16 ? 1 : kUnit;
   const int sa_at = a_row * s_row, sw_at = MF * kUnit * kGroup + (wn * 8 + grp) * s_row;
+  // One multiply-add a value takes the scales' product, which has to be finite
+  // (the header says so): one after the other would take two.
   auto read_scales = [&](int kb) {
     const float* at = sh.scale[0] + ((kb / kGroup) & 1) * S::kScalePlace + (kb % kGroup) * s_step;
     const float sw0 = at[sw_at], sw1 = at[sw_at + 4 * s_row];

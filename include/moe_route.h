@@ -437,7 +437,11 @@ moe_status moe_token_balanced_split(const moe_problem* p, const int32_t* idx,
  * are NaN. Rows of C columns have ceil(C / 128) scales.
  * Weight matrices in 8 bits are [rows, C] codes with one scale for each block
  * of 128 x 128, [ceil(rows / 128), ceil(C / 128)]; which scales they hold is
- * the caller's choice (any fp32 number).                                     */
+ * the caller's choice. The experts' products multiply a row's scale by a weight
+ * block's in fp32 before they apply them to the block's sum: where that product
+ * overflows, an infinity comes out, or NaN for a sum of 0, and below 2^-126 it
+ * loses bits. With weight scales of at most 256 no scale that this library
+ * writes for a row can overflow it.                                          */
 
 /* Root-mean-square norm of the activation rows, with the residual's addition
  * and 8-bit output: what makes the rows that the router scores and the

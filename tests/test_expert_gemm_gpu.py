@@ -450,3 +450,56 @@ def test_exact_bf16_rows_are_the_fp32_rows_rounded(T):
                           *(dev(i) for i in inp), out)
         torch.cuda.synchronize()
         assert torch.equal(out.view(torch.int16), f32.bfloat16().view(torch.int16))
+
+
+@pytest.mark.parametrize("T", [3, 100])
+def test_scales_whose_product_is_just_finite(T):
+    """Row scales of 2^70 by weight scales of 2^57: blocks of zeros are zeros,
+    and small codes what they stand for."""
+    say(f"[case] scales near the end of fp32 T={T}")
+    K, N = 400, 72
+    a, w = np.zeros((T, K), np.uint8), np.full((1, N, K), 0x01, np.uint8)  # 2^-9
+    a[1:, 130], a[2:, 399] = 0x01, 0x81  # 2^-9, -2^-9
+    sa, sw = np.full((T, 4), 2.0 ** 70, np.float32), np.full((1, 1, 4), 2.0 ** 57, np.float32)
+    inp = (a, sa, None, w, sw, np.array([T], np.int32), np.zeros(1, np.int32))
+    want = np.zeros((T, 1))
+    want[1] = 2.0 ** 109
+    for act, flags in ((B.MOE_BF16, 0), (B.MOE_BF16, B.MOE_FLAG_OUT_F32)):
+        assert (f64(run_gemm(T, 1, 1, K, N, inp, act, flags)) == want).all(), flags
+    q, s = torch.empty(T, 32, device="cuda").to(B.E4M3), torch.empty(T, 1, device="cuda")
+    B.moe_expert_gemm_swiglu(B.make_problem(T, 1, 1, 8, 1, B.MOE_BF16), K, 32,
+                             *(dev(i) for i in (a, sa, None, w[:, :64], sw, inp[5], inp[6])), q, s)
+    torch.cuda.synchronize()
+    rest = [0] + list(range(2, T))
+    assert (q[rest].float() == 0).all() and (s[rest] == np.float32(2.0 ** -100) / np.float32(448)).all()
+
+
+def test_largest_row_scale_by_a_weight_scale_of_256():
+    """What the header says of the rows this library writes: the largest scale
+    there is, of a row of FLT_MAX, by 256 is finite."""
+    say("[case] largest row scale")
+    T, K, N = 5, 128, 16
+    far = np.float32(np.finfo(np.float32).max)
+    # a row of FLT_MAX out of the SwiGLU: silu(FLT_MAX) * 1
+    a, w = np.zeros((T, 16), np.uint8), np.zeros((1, 2 * K, 16), np.uint8)
+    a[:, 0], a[:, 1], w[0, :K, 0], w[0, K:, 1] = 0x38, 0x38, 0x38, 0x38
+    one, seg = np.ones((T, 1), np.float32), (np.array([T], np.int32), np.zeros(1, np.int32))
+    q, s = torch.empty(T, K, device="cuda").to(B.E4M3), torch.empty(T, 1, device="cuda")
+    B.moe_expert_gemm_swiglu(B.make_problem(T, 1, 1, 8, 1, B.MOE_BF16), 16, K,
+                             *(dev(i) for i in (a, one, None, w, np.array([far, 1.0], np.float32).reshape(1, 2, 1),
+                                                *seg)), q, s)
+    torch.cuda.synchronize()
+    assert (q.float() == 448).all() and torch.isfinite(s).all()
+    assert (np.abs(f64(s) * 448 / float(far) - 1) <= 2 * U).all()
+    # rows of that scale with codes of 0 and of 1, by weights of 2^-9 in a block of scale 256
+    zero = np.zeros((T, K), np.uint8)
+    wv = np.zeros((1, N, K), np.uint8)
+    wv[0, :, 5] = 0x01
+    sw = np.full((1, 1, 1), 256.0, np.float32)
+    for flags in (0, B.MOE_FLAG_OUT_F32):
+        got = f64(run_gemm(T, 1, 1, K, N, (zero, s.cpu().numpy(), None, wv, sw, *seg), B.MOE_BF16, flags))
+        assert (got == 0).all()
+        one_code = np.full((T, K), 0x38, np.uint8)
+        got = f64(run_gemm(T, 1, 1, K, N, (one_code, s.cpu().numpy(), None, wv, sw, *seg), B.MOE_BF16, flags))
+        want = np.broadcast_to(f64(s) * 0.5, got.shape)  # 256 2^-9
+        assert_within(got, want, (U + HALF[B.MOE_BF16]) * want, "y")
