@@ -87,3 +87,102 @@ def test_no_unexpected_scratch(device_asm):
             if priv > SCRATCH_ALLOWED.get(short(name), 0):
                 bad.append((f, short(name), priv))
     assert not bad, bad
+
+
+# ---- wait states around inline assembly ---------------------------------------
+# The compiler inserts the wait states that gfx9 instructions need, but does not
+# look into inline assembly. A vector memory instruction may read a scalar
+# register no sooner than 5 wait states after a vector instruction (readfirstlane,
+# readlane, a compare) wrote it, and an LDS load its M0 no sooner than 1 after
+# any write.
+VMEM_AFTER_VALU, LDS_AFTER_M0 = 5, 1
+
+
+def lines_of(body: str):
+    """(instruction, its labels before it) in order."""
+    out, labels = [], []
+    for raw in body.split("\n"):
+        t = raw.split(";")[0].split("//")[0].strip()
+        if t.endswith(":"):
+            labels.append(t[:-1])
+        elif t and not t.startswith("."):
+            out.append((t, labels))
+            labels = []
+    return out
+
+
+def scalar_regs(text: str):
+    """Numbers of the scalar registers named in `text` ("m0" as it is)."""
+    regs = set()
+    for m in re.finditer(r"\bs\[(\d+):(\d+)\]|\bs(\d+)\b|\b(m0|vcc)\b", text):
+        if m[1]:
+            regs |= set(range(int(m[1]), int(m[2]) + 1))
+        else:
+            regs.add(int(m[3]) if m[3] else m[4])
+    return regs
+
+
+def too_soon(body: str):
+    """(reader, writer, wait states between) of every vector memory
+    instruction that reads scalar registers too soon, over all ways there."""
+    ins = lines_of(body)
+    jumps: dict[str, list[int]] = {}
+    for i, (t, _) in enumerate(ins):
+        m = re.match(r"s_c?branch\w* (\S+)", t)
+        if m:
+            jumps.setdefault(m[1], []).append(i)
+    bad = []
+
+    def back(i, waited, needs, reader):
+        """Walks back from before instruction i."""
+        for label in ins[i][1]:
+            for j in jumps.get(label, []):
+                look(j, waited, needs, reader)
+        if i > 0 and not re.match(r"s_branch|s_endpgm|s_setpc", ins[i - 1][0]):
+            look(i - 1, waited, needs, reader)
+
+    def look(i, waited, needs, reader):
+        needs = {r: n for r, n in needs.items() if n[0] > waited or n[1] > waited}
+        if not needs:
+            return
+        t = ins[i][0]
+        op, _, args = t.partition(" ")
+        first = scalar_regs(args.split(",")[0])
+        for r in first & set(needs):
+            valu, salu = needs[r]
+            if op.startswith("v_") and waited < valu or op.startswith("s_") and waited < salu:
+                bad.append((reader, t, waited))
+        left = {r: n for r, n in needs.items() if r not in first}
+        nop = re.match(r"s_nop (\d+)", t)
+        back(i, waited + (int(nop[1]) + 1 if nop else 1), left, reader)
+
+    for i, (t, _) in enumerate(ins):
+        m = re.match(r"(global|buffer|flat|scratch)_(load|store|atomic)", t)
+        if m:
+            needs = {r: (VMEM_AFTER_VALU, 0) for r in scalar_regs(t.partition(" ")[2])}
+            if "_lds_" in t:
+                needs["m0"] = (VMEM_AFTER_VALU, LDS_AFTER_M0)
+            back(i, 0, needs, t)
+    return bad
+
+
+def test_the_wait_states_are_counted():
+    load = "\tglobal_load_lds_dword v1, s[0:1]\n"
+    assert too_soon("\tv_readfirstlane_b32 s1, v3\n\ts_mov_b32 m0, s2\n\ts_nop 0\n" + load) \
+        == [(load.strip(), "v_readfirstlane_b32 s1, v3", 2)]
+    assert not too_soon("\tv_readfirstlane_b32 s1, v3\n\ts_mov_b32 m0, s2\n\ts_nop 3\n" + load)
+    assert too_soon("\ts_mov_b32 m0, s2\n" + load) and not too_soon("\ts_mov_b32 m0, s2\n\ts_nop 0\n" + load)
+    assert too_soon("\tv_readfirstlane_b32 m0, v2\n\ts_nop 3\n" + load)
+    # a later write of the register is the one that counts, and ways over branches too
+    assert not too_soon("\tv_readfirstlane_b32 s1, v3\n\ts_mov_b32 s1, s2\n" + load.replace("_lds", ""))
+    way = "\ts_nop 7\n\ts_branch .L1\n.L0:\n\tv_readlane_b32 s0, v3, 1\n\ts_cbranch_vccnz .L2\n\ts_endpgm\n.L1:\n.L2:\n"
+    assert ("v_readlane_b32 s0, v3, 1", 1) in [b[1:] for b in too_soon(way + load)]
+
+
+def test_scalar_operands_of_memory_instructions_are_not_read_too_soon(device_asm):
+    bad = []
+    for f, asm in device_asm.items():
+        for name, body, _ in kernels(asm):
+            for reader, writer, waited in too_soon(body):
+                bad.append((f, short(name), reader, writer, waited))
+    assert not bad, (len(bad), bad[:5])
