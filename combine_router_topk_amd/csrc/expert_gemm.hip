@@ -110,15 +110,17 @@ __device__ __forceinline__ uint64_t uniform(const void* p) {
   const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u >> 32));
   return lo | static_cast<uint64_t>(hi) << 32;
 }
+// The LDS address goes in as M0 itself, so that the compiler writes it and knows
+// what it holds.
 template <int PLUS = 0>  // added to lds
 __device__ __forceinline__ void load_lds16(const void* base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(
-                   __builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(uniform(base)), "n"(PLUS)
-               : "memory", "scc");
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(uniform(base)),
+               "{m0}"(__builtin_amdgcn_readfirstlane(lds) + PLUS)
+               : "memory");
 }
 __device__ __forceinline__ void load_lds4(const void* base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, %2" ::"s"(
-                   __builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(uniform(base))
+  asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, %1" ::"v"(offset), "s"(uniform(base)),
+               "{m0}"(__builtin_amdgcn_readfirstlane(lds))
                : "memory");
 }
 
