@@ -503,3 +503,29 @@ def test_largest_row_scale_by_a_weight_scale_of_256():
         got = f64(run_gemm(T, 1, 1, K, N, (one_code, s.cpu().numpy(), None, wv, sw, *seg), B.MOE_BF16, flags))
         want = np.broadcast_to(f64(s) * 0.5, got.shape)  # 256 2^-9
         assert_within(got, want, (U + HALF[B.MOE_BF16]) * want, "y")
+
+
+@pytest.mark.parametrize("flags", [0, B.MOE_FLAG_OUT_F32])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("T", [3, 90])
+def test_small_products_beside_large_ones_count(T, act, flags):
+    """Sums whose rounded value changes if any of their products is lost:
+    256 + 1 + 1 and 256 + 3 (258 and 260 in bf16, as they are in fp16 and fp32),
+    256 + 1 (exact in fp16 and fp32), 256 + 2 - 1 + 1."""
+    say(f"[case] small integers T={T} act={act} flags={flags}")
+    K, N = 32, 8
+    rows = [[(0x78, 1), (0x38, 1), (0x38, 1)], [(0x78, 1), (0x44, 1)], [(0x78, 1), (0x38, 1)],
+            [(0x78, 1), (0x40, 1), (0x38, -1), (0x38, 1)]]
+    want = np.array([258.0, 259.0, 257.0, 258.0])
+    if act == B.MOE_BF16 and not flags:
+        want = np.array([258.0, 260.0, 256.0, 258.0])  # 259 and 257 to even
+    one = np.ones((T, 1), np.float32)
+    for first in (0, 7, 15):  # of the places: one group of eight, two, two chunks
+        a, w = np.zeros((T, K), np.uint8), np.zeros((1, N, K), np.uint8)
+        w[0] = 0x38
+        for r in range(T):
+            for j, (c, sign) in enumerate(rows[r % 4]):
+                a[r, first + j] = c | (0x80 if sign < 0 else 0)
+        y = run_gemm(T, 1, 1, K, N, (a, one, None, w, np.ones((1, 1, 1), np.float32), np.array([T], np.int32),
+                                     np.zeros(1, np.int32)), act, flags)
+        assert (f64(y) == want[np.arange(T) % 4][:, None]).all(), first
