@@ -228,6 +228,45 @@ def test_norm_rows_past_four_gib():
     assert torch.isfinite(dg).all()
 
 
+@pytest.mark.parametrize("T,H", [(140000, 16384), (200003, 1032)])
+def test_norm_backward_weight_gradient_of_many_rows(T, H):
+    """dgamma over hundreds of rows a block against fp64 sums of the same
+    products, and dx of rows on both sides of 2^31 elements."""
+    say(f"[case] norm backward T={T} H={H}: dgamma")
+    act, p = B.MOE_BF16, problem(T, H, B.MOE_BF16)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(7)
+    h, dy = (torch.empty(T, H, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for t in (h, dy):
+        for part in t.split(20000):
+            part.normal_(generator=gen)
+    # means, so that the rows of a block add up: a lost block is 10 times the bound
+    for part in h.split(20000):
+        part += 0.5
+    for part in dy.split(20000):
+        part += 0.25
+    g = dev(bits16(np.random.default_rng(7), H, act), act)
+    rstd = torch.rand(T, device="cuda", generator=gen) + 0.5
+    dx, dg = torch.empty_like(h), torch.empty(H, device="cuda")
+    ws = torch.empty(B.moe_rms_norm_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    B.moe_rms_norm_backward(p, dy, None, h, g, rstd, dx, dg, ws)
+    want, mag = (torch.zeros(H, dtype=torch.float64, device="cuda") for _ in range(2))
+    for lo in range(0, T, 4000):
+        t = dy[lo:lo + 4000].double() * h[lo:lo + 4000].double() * rstd[lo:lo + 4000, None].double()
+        want += t.sum(0)
+        mag += t.abs().sum(0)
+    chain = -(-T // 1024) + 64 + 16 + 4  # a block's rows, the segments, the product's roundings
+    assert_within(f64(dg), want.cpu().numpy(), chain * U * mag.cpu().numpy(), "dgamma")
+    rows = [0, 131071, 131072, T - 1]
+    pick = lambda t: np.stack([f64(t[r]) for r in rows])  # noqa: E731
+    hv, dyv, r = pick(h), pick(dy), np.array([[float(rstd[i])] for i in rows])
+    n, u = hv * r, dyv * f64(g)
+    mean, most = (u * n).mean(axis=1, keepdims=True), np.abs(u * n).mean(axis=1, keepdims=True)
+    dxv = r * (u - n * mean)
+    bound = r * (6 * U * (np.abs(u) + np.abs(n * mean)) + 48 * U * np.abs(n) * most) + 2 * U * np.abs(dxv)
+    assert_within(pick(dx), dxv, bound + round_bound(np.abs(dxv) + bound, act), "dx")
+
+
 def test_norm_backward_without_rows():
     p = problem(0, 64, B.MOE_BF16)
     dg = torch.full((64,), 3.0, device="cuda")
