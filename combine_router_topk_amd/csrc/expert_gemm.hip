@@ -22,16 +22,21 @@
 // 8-bit rows.
 //
 // What bounds it: with few rows an expert the weights' bytes (gate and up of 256
-// experts, 4096 x 2048, 8 rows each: 757 us, 5.7 TB/s). With hundreds of rows
-// the chip's power. A block per CU holds 256 weight rows by up to 256 rows, as
-// much as its registers accumulate: a step of 128 codes takes 64 KiB from L2,
-// 192 KiB of LDS reads (8 waves of 128 x 64) and 256 matrix instructions with
-// 1024 multiply-adds. 32768 rows of one expert, K = N = 4096: 544 us at a clock
-// of 1.63 GHz with random codes, 432 us at 2.22 GHz with codes of zero; matrix
-// cores are busy 59 % of the cycles, LDS 30 %; without any loads it is 8 % fewer. The
-// same rows in 64 segments: 590 us, 1.87 PFLOP/s (a library product of 8192^3 in
-// 8 bits reaches 2.66). In fp16 the widening adds 5.5 conversions to each 3 matrix
-// instructions, and the whole runs at 1.07 PFLOP/s (a bf16 library product: 1.30).
+// experts, 4096 x 2048, 8 rows each: 768 us, 5.6 TB/s). With hundreds of rows
+// several things. A block per CU holds 256 weight rows by up to 256 rows, which
+// takes half of its registers: a step of 128 codes takes 64 KiB from L2, 192 KiB
+// of LDS reads (8 waves of 128 x 64) and 256 matrix instructions with 1024
+// multiply-adds. 32768 rows of one expert, K = N = 4096: matrix cores are busy
+// 55 % of the cycles, and power takes a part of the clock (475 us at 1.99 GHz with
+// random codes, 424 us at 2.32 GHz with codes of zero). The same rows in 64
+// segments: 590 us in a row, 1.87 PFLOP/s (a library product of 8192^3 in 8 bits
+// reaches 2.66). With K = 1024 there are 8 steps a tile, power makes no
+// difference (272 and 269 us, skewed top-6 of 16384 tokens), and 9 of a tile's 25
+// us pass without matrix instructions, in its look-up, its first loads and its
+// stores. In fp16 the widening adds 5.5 conversions to each 3 matrix
+// instructions, and the whole runs at 1.08 PFLOP/s (a bf16 library product: 1.30):
+// 22 us against 33 for 2042 rows in 8 segments of 1424 x 2872, 592 against 984 for
+// the 64 segments, 280 against 430 for the skewed ones.
 //
 // The weights are the instruction's first operand, the rows its second: a
 // lane then holds one row's results, so the row's scale is one value a lane,
@@ -322,7 +327,8 @@ __device__ __forceinline__ void load_ahead(const GemmArgs& g, int wave, S& sh, L
 // THIN: a tile of at most 16 rows, as in decode. All waves take the same rows,
 // and each two fragments of the weights (with SwiGLU one of the gate's and the
 // up's beside it) where three of four would have none of the rows: gate and up of
-// 8 rows for each of 256 experts 786 -> 757 us, of 8 rows in all 42.5 -> 25.1 us.
+// 8 rows for each of 256 experts 786 -> 757 us in one run (757 to 790 on other
+// cards), of 8 rows in all 42.5 -> 25.1 us.
 template <int MF, bool SWIGLU, int ACT, bool F32, bool EXACT, bool THIN, typename S, typename F>
 __device__ __forceinline__ void run_tile(const GemmArgs& g, int wave, S& sh, const Tile& t, Loads& l,
                                          F&& then) {

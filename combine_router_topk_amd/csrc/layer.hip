@@ -14,9 +14,10 @@
 // bits, as a few rows are not worth rounding to 8; e4m3 weights become 16-bit
 // numbers in registers, exactly, and a block's scale is applied to the fp32
 // sum of its 128 products. One token of 256 experts, top-8, 4096 x 2048 in
-// e4m3: 30.2 us + 16.4 us for 201 MB (4.3 TB/s; starting and ending two launches
-// is the rest); 8 tokens of top-2 of 64 in bf16: 139 us, 5.05 TB/s; 32 tokens of
-// top-8 of 256, 7168 x 2048: 1.29 ms, 5.6 TB/s.
+// e4m3: 29.5 us + 14.8 us for 201 MB (4.5 TB/s; starting and ending two launches
+// is the rest); 8 tokens of top-2 of 64 in bf16: 91 us + 49 us for 755 MB, 5.4
+// TB/s; 32 tokens of top-8 of 256, 7168 x 2048: 772 us + 474 us for 6.8 GB, 5.5
+// TB/s, and 15 us for the launches that route and add up.
 #include "device.hpp"
 #include "launch.hpp"
 #include "quant.hpp"
@@ -244,9 +245,17 @@ __global__ __launch_bounds__(kRouteThreads) void layer_route_kernel(LayerArgs g)
 // V > 0: every block routes the tokens itself, 0.08 us a pair, and takes tiles
 // in turn. V = 0: the tables are there, which takes a launch of 10 us, and a block
 // that is done takes the next tile that nobody has, as blocks' shares of the
-// memory's bandwidth differ by half. (8 tokens, top-4 of 64 experts: 51.8 us
-// with V > 0, 62.3 us with V = 0; 32, top-8 of 256: 1431 us and 1407 us; 64, top-16
-// of 128: 576 us and 511 us.)
+// memory's bandwidth differ by half. Which is faster depends on how long the
+// launch is beside that; kFewPairs lies between. The whole layer in us, V > 0 and
+// V = 0 (rounds of both in turn):
+//   pairs                                       32   64   96  128  160  192  224  256
+//   top-8 of 256, 4096 x 2048, e4m3    V > 0   149  272  379  490  580  660  726  796
+//                                      V = 0   162  279  385  477  573  650  718  782
+//   top-4 of 64, 2048 x 1024, 16 bits  V > 0    86  122  150  173  195  205  219  231
+//                                      V = 0    97  132  157  179  201  209  223  232
+//   top-16 of 128, 2048 x 1024, e4m3   V > 0         89       144       172  184
+//                                      V = 0        106       163       188  202
+// and with 1024 pairs (64 tokens, top-16 of 128) 576 and 511.
 template <int ACT, bool F8, int V>
 __global__ __launch_bounds__(kUpThreads, 6) void layer_up_kernel(LayerArgs g) {
   __shared__ float4 part[2][kUpWaves][2][kWave];
@@ -488,9 +497,16 @@ __global__ __launch_bounds__(256) void layer_sum_kernel(LayerArgs g, int shares)
 
 // Shares of the down product: with a block a tile and, say, 448 tiles, a CU has
 // one block or two, and blocks end at different times. Four blocks a tile come
-// one after the other where there is room (32 tokens, top-8 of 256 experts, 7168 x
-// 2048: 1355 -> 1286 us; 8 tokens: 492 -> 471 us), which pays for the launch that
-// adds them up where there are weights to read for some 100 us.
+// one after the other where there is room, which pays for the launch that adds
+// them up. The whole layer in us without and with shares, top-8 of 256 experts,
+// I = 2048, e4m3 (16 tokens; 8 tokens, 2^29 weights and more at each width):
+//   columns   4096       4112       5120       6144       7168       8192
+//   tiles     256        257        320        384        448        512
+//   16        478 489    632 528    716 613    782 712    852 813    917 912
+//   8         267 273    354 296    401 344    439 391    476 454    509 509
+// Whole rounds of 256 tiles gain nothing. The bound on the weights is wider than it
+// has to be: 2 tokens (2^27 weights) gain at 4112 to 6144 columns, too (108 and
+// 95 us at 4112), and 4 us of 146 at 7168.
 constexpr int kShares = 4;
 bool in_shares(int T, int E, int k, int H, int I) {
   const int tiles = H / kRowsPerTile;

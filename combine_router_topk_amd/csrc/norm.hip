@@ -13,11 +13,11 @@
 // in registers by one block, each lane owning 16-byte chunks (8 elements), so
 // every input is read once; a scale block of 128 elements is 16 lanes, one
 // DPP row, and its maximum never leaves the registers. At 16384 rows of 4096 in
-// bf16 the forward with all outputs takes 114 us (5.3 TB/s), 8-bit rows alone
-// 33.6 us, the backward without dh 81.6 us (4.9 TB/s). What a small batch waits
-// for is its instructions: with loads of 4 bytes under four branches each,
-// which the compiler makes of `c < n ? p[c] : zero`, 8-bit rows of 4099 x 2872
-// took 15.8 us and not 9.8.
+// bf16 the forward with all outputs takes 116 us (5.2 TB/s), 8-bit rows alone
+// 33.8 us, the backward without dh 75.4 us and 5 for dgamma's last sum. What a
+// small batch waits for is its instructions and its rounds: with loads of 4 bytes
+// under four branches each, which the compiler makes of `c < n ? p[c] : zero`,
+// 8-bit rows of 4099 x 2872 took 15.8 us and not 10.5.
 #include "device.hpp"
 #include "launch.hpp"
 #include "quant.hpp"
@@ -27,9 +27,10 @@ namespace moe {
 namespace {
 
 // Blocks of a forward launch: what the chip holds of NT threads at this
-// kernel's registers (24 waves a CU), fewer if that evens out the rows a block
-// takes: with a few rows left for another round, that round costs as much as a
-// full one.
+// kernel's registers (24 waves a CU; its narrow forms would fit 32), fewer if that
+// evens out the rows a block takes: with a few rows left for another round, that
+// round costs as much as a full one. (4099 rows of 2872 are three rounds of 1367
+// blocks, 16 waves a CU.)
 constexpr int norm_blocks(int T, int NT) {
   const int most = 256 * (24 * kWave / NT);
   const int rounds = (T + most - 1) / most;
@@ -87,7 +88,7 @@ __device__ __forceinline__ float larger(float a, float b) { return __builtin_ele
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ... The next row is loaded before
 // this one's sum goes round the block: with a block for each row a CU holds
 // 64 KiB in flight and then waits (16384 rows of 4096, y alone, with the loads of
-// then: 63.7 us, and 46.8 with the next row's ahead). h_out
+// then: 63.7 us, and 46.8 with the next row's ahead; 40.9 with today's). h_out
 // and y may be x or res themselves: a lane reads its chunks of a row before it
 // writes them. A lane past the row may read another's after it was written, but
 // its values go nowhere.
@@ -277,7 +278,7 @@ void by_row(int chunks, F&& launch) {
   MOE_NORM_CASE(64, 1);
   MOE_NORM_CASE(128, 1);
   MOE_NORM_CASE(256, 1);
-  MOE_NORM_CASE(192, 2);  // 8-bit rows of 4099 x 2872: 10.5 us with 256 x 2, 9.8 us
+  MOE_NORM_CASE(192, 2);  // 8-bit rows of 4099 x 2872: 11.2 us with 256 x 2, 10.5 us
   MOE_NORM_CASE(256, 2);
   MOE_NORM_CASE(512, 2);
   MOE_NORM_CASE(1024, 2);

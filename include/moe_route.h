@@ -432,7 +432,9 @@ moe_status moe_token_balanced_split(const moe_problem* p, const int32_t* idx,
  * infinities) with one fp32 scale for each block of 128 columns (the last
  * block may be shorter): a value is its code times its block's scale. For a
  * block of values v with the largest magnitude amax,
- *   scale = max(amax, 2^-100) / 448,  code = v / scale rounded to nearest even.
+ *   scale = max(amax, 2^-100) / 448,  code = v / scale rounded to nearest even
+ * (v times the scale's reciprocal: where that, within 1.5 steps of fp32 of v /
+ * scale, lies on the other side of the middle, the neighbouring code).
  * A block that holds an infinity or a NaN takes a NaN scale: all its values
  * are NaN. Rows of C columns have ceil(C / 128) scales.
  * Weight matrices in 8 bits are [rows, C] codes with one scale for each block
@@ -462,6 +464,7 @@ moe_status moe_token_balanced_split(const moe_problem* p, const int32_t* idx,
  *   q, q_scale  codes [T, H], 8-byte aligned, and f32 [T, ceil(H/128)]
  *             (write), or both NULL to skip
  *   rstd      f32 [T] (write), or NULL to skip
+ * q, q_scale and rstd must not overlap any other buffer.
  * At least one of y and q must be given when T > 0.                          */
 moe_status moe_rms_norm(const moe_problem* p, const void* x, const void* residual,
                         const void* gamma, float eps, void* h, void* y, void* q, float* q_scale,
@@ -555,7 +558,9 @@ moe_status moe_layer_workspace_bytes(const moe_problem* p, int32_t I, size_t* by
  *             once to the activation format (fp32 with MOE_FLAG_OUT_F32)
  * Nothing is dispatched: a decode step reads the chosen experts' weights and
  * little else ([METRO] section "Add the expert-weight traffic term").
- * Activations stay in 16 bits.
+ * Activations stay in 16 bits. With e4m3 weights the 128 products of a block are
+ * summed in fp32 before its scale is applied, so these sums have to be finite
+ * themselves (they are for values of x and h up to 2^112, so for any in fp16).
  *   H and I are multiples of 16 and at most 2^24; more, and T >
  *   MOE_MAX_FEW_TOKENS, return MOE_ERR_UNSUPPORTED. R is not used.
  *   logits  f32 [T, E] (read)       x  16-bit [T, H] (read)
