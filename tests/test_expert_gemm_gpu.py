@@ -1,10 +1,11 @@
 """The experts' products in 8 bits on the GPU against the oracle.
 
-Bounds (u = 2^-24). 8-bit matrix instructions sum groups of eight products
-cut off at 2^-13 of a power of two that the largest of them reaches: at most
-8 2^-13 of the group's largest product is lost, with rounded fp32 sums of the
-groups and blocks after that. fp32 outputs and the SwiGLU's come from products
-in fp16, exact, summed in fp32 with at most K + K / 128 + 2 truncations.
+Bounds (u = 2^-24). 8-bit matrix instructions, which bf16 outputs come from,
+sum groups of eight products cut off at 2^-13 of a power of two that the
+largest of them reaches: at most 8 2^-13 of the group's largest product is
+lost, with rounded fp32 sums of the groups and blocks after that. fp16 and fp32
+outputs, bf16 ones with exact sums and the SwiGLU's come from products in fp16,
+exact, summed in fp32 with at most K + K / 128 + 2 truncations.
 """
 import numpy as np
 import pytest
