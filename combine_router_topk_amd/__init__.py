@@ -12,7 +12,8 @@ libmoe_route.so and fails if it has not been built.
 """
 from .binding import (MOE_BF16, MOE_F16, MOE_FLAG_EXACT_SUMS, MOE_FLAG_GREEDY_ID_ORDER,  # noqa: F401
                       MOE_FLAG_OUT_F32,
-                      MoeError, Problem, make_problem, moe_assign_replicas, moe_combine,
+                      AdamW, AdamWTensors, MoeError, Problem, make_adamw, make_problem,
+                      moe_adamw_step, moe_assign_replicas, moe_combine,
                       moe_combine_backward, moe_dispatch_backward,
                       moe_dispatch, moe_expert_gemm, moe_expert_gemm_swiglu, moe_expert_standin,
                       moe_last_error, moe_layer_few_tokens, moe_layer_workspace_bytes, moe_layout,

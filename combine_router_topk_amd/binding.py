@@ -22,7 +22,7 @@ from . import build as _build
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_route.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
-MOE_F16, MOE_BF16 = 1, 2
+MOE_F16, MOE_BF16, MOE_F32 = 1, 2, 3
 MOE_FLAG_GREEDY_ID_ORDER = 1 << 0
 MOE_FLAG_OUT_F32 = 1 << 1
 MOE_FLAG_EXACT_SUMS = 1 << 2
@@ -40,10 +40,13 @@ EXPORTED = ("moe_version", "moe_build_id", "moe_status_string", "moe_last_error"
             "moe_routing_stats", "moe_token_balanced_split",
            "moe_rms_norm", "moe_rms_norm_workspace_bytes", "moe_rms_norm_backward",
            "moe_expert_gemm", "moe_expert_gemm_swiglu", "moe_layer_workspace_bytes",
-           "moe_layer_few_tokens")
+           "moe_layer_few_tokens", "moe_adamw_step")
 
 _TORCH_ACT = {MOE_F16: torch.float16, MOE_BF16: torch.bfloat16}
 E4M3 = torch.float8_e4m3fn
+
+
+_ADAMW_DTYPE = {torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
 
 
 class MoeError(RuntimeError):
@@ -60,6 +63,17 @@ class Problem(ctypes.Structure):
     def __repr__(self):
         return (f"Problem(T={self.T}, E={self.E}, k={self.k}, H={self.H}, R={self.R}, "
                 f"act_dtype={self.act_dtype}, flags={self.flags})")
+
+
+class AdamW(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
+                ("eps", ctypes.c_float), ("step", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("g_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32)]
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w", "master", "g", "m", "v", "m_scale", "v_scale")] \
+        + [("n", ctypes.c_int64), ("weight_decay", ctypes.c_float)]
 
 
 def _load() -> ctypes.CDLL:
@@ -101,6 +115,7 @@ def _load() -> ctypes.CDLL:
         "moe_expert_gemm_swiglu": (i32, [P, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
         "moe_layer_workspace_bytes": (i32, [P, i32, ctypes.POINTER(sz)]),
         "moe_layer_few_tokens": (i32, [P, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "moe_adamw_step": (i32, [ctypes.POINTER(AdamW), ctypes.POINTER(_AdamWTensor), i32, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -508,3 +523,68 @@ def moe_layer_few_tokens(p: Problem, I: int, logits, x, w_up, s_up, w_down, s_do
            a(s_up, f32, E * scale_blocks(2 * I) * nh, "s_up"), a(w_down, w_dt, E * H * I, "w_down"),
            a(s_down, f32, E * nh * ni, "s_down"), a(idx, torch.int32, n, "idx"), a(w, f32, n, "w"),
            a(out, out_dt, T * H, "out"), a(ws, None, None, "ws"), _nbytes(ws))
+
+
+def make_adamw(lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, step: int = 1) -> AdamW:
+    """The numbers of a step; the types come from its AdamWTensors."""
+    return AdamW(lr, beta1, beta2, eps, step, 0, 0, 0)
+
+
+class AdamWTensors:
+    """The tensors that moe_adamw_step updates, kept by an optimizer from step
+    to step. Each is a dict of w, g, m, v (contiguous, of one size), master (fp32
+    beside a 16-bit w, or None), weight_decay, and m_scale and v_scale with 8-bit
+    states (then m and v are float8_e4m3fn). All have the same types and device. The
+    object keeps the tensors alive; set_grads takes new gradients."""
+
+    def __init__(self, tensors):
+        self.tensors = [dict(t) for t in tensors]
+        self.array = (_AdamWTensor * len(self.tensors))()
+        self.w_dtype = self.g_dtype = MOE_F32
+        self.state_bits, self._arg = 32, _Args("AdamWTensors")
+        if self.tensors:
+            t = self.tensors[0]
+            for key in ("w", "g"):
+                if t[key].dtype not in _ADAMW_DTYPE:
+                    raise ValueError(f"{key}: dtype {t[key].dtype} is none of {list(_ADAMW_DTYPE)}")
+            self.w_dtype, self.g_dtype = _ADAMW_DTYPE[t["w"].dtype], _ADAMW_DTYPE[t["g"].dtype]
+            self.state_bits = 8 if t["m"].dtype == E4M3 else 32
+        first = self.tensors[0] if self.tensors else None
+        state = E4M3 if self.state_bits == 8 else torch.float32
+        for a, t in zip(self.array, self.tensors):
+            n = t["w"].numel()
+            for key, dtype in (("w", first["w"].dtype), ("master", torch.float32), ("g", first["g"].dtype),
+                               ("m", state), ("v", state)):
+                setattr(a, key, self._sized(t.get(key) if key == "master" else t[key], dtype, n, key))
+            if self.state_bits == 8:
+                for key in ("m_scale", "v_scale"):
+                    setattr(a, key, self._sized(t[key], torch.float32, scale_blocks(n), key))
+            a.n, a.weight_decay = n, t.get("weight_decay", 0.0)
+
+    def _sized(self, t, dtype, n, name):
+        if t is not None and isinstance(t, torch.Tensor) and t.numel() != n:
+            raise ValueError(f"{name}: {t.numel()} elements, its weights need {n}")
+        return self._arg(t, dtype, n, name)
+
+    def set_grads(self, grads) -> None:
+        """New gradients, one a tensor, of the same type."""
+        grads = list(grads)
+        if len(grads) != len(self.tensors):
+            raise ValueError(f"{len(grads)} gradients for {len(self.tensors)} tensors")
+        pointers = [self._sized(g, t["g"].dtype, t["w"].numel(), "g") for g, t in zip(grads, self.tensors)]
+        if any(p is None for p in pointers):
+            raise ValueError("g: expected a torch tensor")
+        for a, t, g, p in zip(self.array, self.tensors, grads, pointers):
+            a.g, t["g"] = p, g
+
+
+def moe_adamw_step(h: AdamW, tensors: AdamWTensors, control=None, stream=None) -> None:
+    """control: f32 [3] on the device (learning rate, step number, factor of the
+    gradients) in place of h's, or None."""
+    if not tensors.tensors:
+        return
+    a = _Args("moe_adamw_step")
+    a.dev = tensors._arg.dev
+    full = AdamW(h.lr, h.beta1, h.beta2, h.eps, h.step, tensors.w_dtype, tensors.g_dtype, tensors.state_bits)
+    a.call(_lib.moe_adamw_step, stream, ctypes.byref(full), tensors.array, len(tensors.array),
+           a(control, torch.float32, 3, "control"))

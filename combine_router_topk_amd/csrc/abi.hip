@@ -4,6 +4,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "launch.hpp"
@@ -184,7 +185,7 @@ moe_status check_layer(const moe_problem* p, int32_t I, const char* fn) {
 
 extern "C" {
 
-int32_t moe_version(void) { return 1 * 10000 + 4 * 100 + 0; }
+int32_t moe_version(void) { return 1 * 10000 + 5 * 100 + 0; }
 
 const char* moe_build_id(void) { return MOE_BUILD_ID; }
 
@@ -676,6 +677,59 @@ moe_status moe_layer_few_tokens(const moe_problem* p, int32_t I, const float* lo
                                                  p->H, I, idx, w, out, ws, p->act_dtype,
                                                  (p->flags & MOE_FLAG_OUT_F32) != 0,
                                                  static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+moe_status moe_adamw_step(const moe_adamw* h, const moe_adamw_tensor* tensors, int32_t n,
+                          const float* control, void* stream) {
+  const char* fn = "moe_adamw_step";
+  if (h == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: h is NULL", fn);
+  if (n < 0) return fail(MOE_ERR_INVALID_ARG, "%s: n=%d < 0", fn, n);
+  if (!std::isfinite(h->lr)) return fail(MOE_ERR_INVALID_ARG, "%s: lr=%g is not finite", fn, h->lr);
+  if (!(h->beta1 >= 0.0f && h->beta1 < 1.0f)) return fail(MOE_ERR_INVALID_ARG, "%s: beta1=%g outside [0, 1)", fn, h->beta1);
+  if (!(h->beta2 >= 0.0f && h->beta2 < 1.0f)) return fail(MOE_ERR_INVALID_ARG, "%s: beta2=%g outside [0, 1)", fn, h->beta2);
+  if (!(h->eps >= 0.0f) || !std::isfinite(h->eps))
+    return fail(MOE_ERR_INVALID_ARG, "%s: eps=%g is not finite and >= 0", fn, h->eps);
+  if (h->step < 1) return fail(MOE_ERR_INVALID_ARG, "%s: step=%d < 1", fn, h->step);
+  for (const int32_t d : {h->w_dtype, h->g_dtype})
+    if (d != MOE_F32 && d != MOE_F16 && d != MOE_BF16)
+      return fail(MOE_ERR_INVALID_ARG, "%s: type %d is none of MOE_F32, MOE_F16, MOE_BF16", fn, d);
+  if (h->w_dtype != MOE_F32 && h->g_dtype != MOE_F32 && h->w_dtype != h->g_dtype)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: w and g in two different 16-bit formats", fn);
+  if (h->state_bits != 32 && h->state_bits != 8)
+    return fail(MOE_ERR_INVALID_ARG, "%s: state_bits=%d is neither 32 nor 8", fn, h->state_bits);
+  if (control != nullptr) CHECK(need(control, 4, fn, "control"));
+  if (n == 0) return MOE_OK;
+  if (tensors == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: tensors is NULL", fn);
+  const bool s8 = h->state_bits == 8;
+  for (int32_t i = 0; i < n; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.n < 0) return fail(MOE_ERR_INVALID_ARG, "%s: tensor %d: n=%lld < 0", fn, i, static_cast<long long>(t.n));
+    if (t.n > moe::adamw_most_elements())
+      return fail(MOE_ERR_UNSUPPORTED, "%s: tensor %d: n=%lld is over %lld", fn, i, static_cast<long long>(t.n),
+                  static_cast<long long>(moe::adamw_most_elements()));
+    if (!std::isfinite(t.weight_decay))
+      return fail(MOE_ERR_INVALID_ARG, "%s: tensor %d: weight_decay=%g is not finite", fn, i, t.weight_decay);
+    if (t.master != nullptr && h->w_dtype == MOE_F32)
+      return fail(MOE_ERR_INVALID_ARG, "%s: tensor %d: a master beside fp32 weights", fn, i);
+    if ((t.m_scale != nullptr || t.v_scale != nullptr) && !s8)
+      return fail(MOE_ERR_INVALID_ARG, "%s: tensor %d: scales beside fp32 states", fn, i);
+    if (t.n == 0) continue;
+    CHECK(need(t.w, 16, fn, "w"));
+    if (t.master != nullptr) CHECK(need(t.master, 16, fn, "master"));
+    CHECK(need(t.g, 16, fn, "g"));
+    CHECK(need(t.m, s8 ? 8 : 16, fn, "m"));
+    CHECK(need(t.v, s8 ? 8 : 16, fn, "v"));
+    if (s8) {
+      CHECK(need(t.m_scale, 4, fn, "m_scale"));
+      CHECK(need(t.v_scale, 4, fn, "v_scale"));
+    }
+  }
+  clear_stale_error();
+  const moe::AdamWStep step{h->lr, h->beta1, h->beta2, h->eps, static_cast<float>(h->step), control};
+  const int act = h->w_dtype != MOE_F32 ? h->w_dtype : h->g_dtype != MOE_F32 ? h->g_dtype : MOE_F16;
+  return hip_status(moe::launch_adamw(step, tensors, n, h->w_dtype == MOE_F32, h->g_dtype == MOE_F32, act, s8,
+                                      static_cast<hipStream_t>(stream)),
                     fn);
 }
 

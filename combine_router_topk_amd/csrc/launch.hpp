@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "moe_route.h"
+
 namespace moe {
 
 // Token blocking used by the route and layout kernels. One function decides
@@ -171,5 +173,13 @@ hipError_t launch_layer_few_tokens(const float* logits, const void* x, const voi
                                    const void* w_down, const float* s_down, int T, int E, int k, int H, int I,
                                    int32_t* idx, float* w, void* out, void* ws, int act, bool out_f32,
                                    hipStream_t s);
+
+struct AdamWStep {
+  float lr, beta1, beta2, eps, step;
+  const float* control;
+};
+int64_t adamw_most_elements();  // of a tensor
+hipError_t launch_adamw(const AdamWStep& h, const moe_adamw_tensor* tensors, int n, bool w32, bool g32, int act, bool s8,
+                        hipStream_t s);
 
 }  // namespace moe

@@ -8,7 +8,8 @@
  * combine and the dispatch, routing statistics, and token-balanced replica
  * routing as the greedy's baseline; and the layer around the routing: the
  * norm that makes its rows with its gradient, the experts' products in
- * block-scaled 8-bit floating point, and the whole layer for a few tokens.
+ * block-scaled 8-bit floating point, and the whole layer for a few tokens; and
+ * the step that trains weights.
  *
  * Sources (web pages on MoE dispatch and combine):
  *   [METRO]  "METRO AllGather vs AllToAll for MoE decode".
@@ -63,6 +64,8 @@ typedef enum {
 
 /* Activation formats. */
 enum { MOE_F16 = 1, MOE_BF16 = 2 };
+/* What moe_adamw_step takes beside them. */
+enum { MOE_F32 = 3 };
 
 /* Flags (bit set). */
 enum {
@@ -577,6 +580,66 @@ moe_status moe_layer_few_tokens(const moe_problem* p, int32_t I, const float* lo
                                 const void* w_up, const float* s_up, const void* w_down,
                                 const float* s_down, int32_t* idx, float* w, void* out, void* ws,
                                 size_t ws_bytes, void* stream);
+
+/* ---- training the weights --------------------------------------------------- */
+
+/* One AdamW step.
+ *   lr, beta1, beta2, eps  finite, eps >= 0, 0 <= beta < 1
+ *   step        1 for the first one
+ *   w_dtype     MOE_F32, MOE_F16 or MOE_BF16, of every tensor's w
+ *   g_dtype     of every tensor's g: MOE_F32, or 16 bits (with 16-bit w the same
+ *               format, else MOE_ERR_UNSUPPORTED)
+ *   state_bits  32, or 8: m and v as 8-bit rows (e4m3 codes, one fp32 scale for
+ *               each 128 elements, counted from the tensor's start)             */
+typedef struct {
+  float lr, beta1, beta2, eps;
+  int32_t step, w_dtype, g_dtype, state_bits;
+} moe_adamw;
+
+/* One tensor of the step, n >= 0 elements in memory order.
+ *   w        [n] (read, write)
+ *   master   f32 [n] (read, write) beside a 16-bit w, which becomes its rounded
+ *            copy; NULL for none: w itself is updated and rounded
+ *   g        [n] (read)
+ *   m, v     f32 [n] (read, write), or with 8-bit states codes [n]; v's codes and
+ *            scales hold its square root
+ *   m_scale, v_scale  f32 [ceil(n / 128)] (read, write) with 8-bit states, else
+ *            NULL. All zeros is the state before the first step.
+ *   weight_decay  finite
+ * Arrays are 16-byte aligned, the codes 8-byte, the scales 4-byte. No array may
+ * overlap another of the same step (g aside, which several tensors may share). */
+typedef struct {
+  void* w;
+  float* master;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  float weight_decay;
+} moe_adamw_tensor;
+
+/* An AdamW step over n tensors at once, the way the routed layer's weights (the
+ * experts', gamma of the norm, the router's) are trained from their gradients:
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2, in fp32
+ *   w = w - lr weight_decay w - lr (m / c1) / (sqrt(v / c2) + eps)
+ *   c1 = 1 - beta1^step,  c2 = 1 - beta2^step
+ * w is taken from master where that is given, updated in fp32 and rounded once.
+ * With 8-bit states the step uses m and v before they are rounded to 8 bits; a
+ * root of v above 0 takes at least the smallest code, so that it stays above 0. A
+ * gradient that is not finite makes m and v of its 128 elements NaN for good;
+ * control's scale can skip such a step.
+ * `tensors` is a HOST array, read during the call; nothing of it is kept. Up to 56
+ * tensors go into one launch. A tensor has fewer than 2^37 elements
+ * (MOE_ERR_UNSUPPORTED).
+ *   control  f32 [3] on the device (read) or NULL: learning rate, step number and a
+ *            factor for the gradients in place of h->lr, h->step and 1, for
+ *            schedules and clipping under graph replay. A factor that is NaN or
+ *            infinite leaves every tensor as it was. The step number has to be a
+ *            whole number of at least 1.                                        */
+moe_status moe_adamw_step(const moe_adamw* h, const moe_adamw_tensor* tensors, int32_t n,
+                          const float* control, void* stream);
 
 #ifdef __cplusplus
 }

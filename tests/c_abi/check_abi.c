@@ -12,7 +12,8 @@
  *                           and the token-balanced split;
  *   moe_c_abi_check_layer() the layer around the routing: the norm and its
  *                           gradient, the experts' products in 8 bits, the
- *                           whole layer for a few tokens.
+ *                           whole layer for a few tokens;
+ *   moe_c_abi_check_weights() what trains weights.
  * Each returns 0 when every check holds and prints the first failure
  * otherwise.
  */
@@ -695,5 +696,41 @@ done:
   hipFree(hq);
   hipFree(hqs);
   hipFree(ws);
+  return rc;
+}
+
+int moe_c_abi_check_weights(void) {
+  enum { N1 = 300 };
+  enum { W_W, W_G, W_M, W_V, W_COUNT };
+  float h[W_COUNT][N1];
+  void* d[W_COUNT] = {NULL};
+  int rc = 0;
+  moe_adamw step = {0.25f, 0.5f, 0.75f, 0.0f, 1, MOE_F32, MOE_F32, 32};
+  moe_adamw_tensor t;
+
+  /* 1. AdamW's first step without decay moves every weight by lr against its
+     gradient's sign: m / c1 = g, sqrt(v / c2) = |g| */
+  for (int i = 0; i < N1; ++i) {
+    h[W_W][i] = (float)i, h[W_G][i] = (i & 1 ? -0.125f : 0.5f) * (float)(1 + i % 7), h[W_M][i] = h[W_V][i] = 0.0f;
+  }
+  for (int i = 0; i < W_COUNT; ++i) {
+    HIP_OK(hipMalloc(&d[i], sizeof(h[i])));
+    HIP_OK(hipMemcpy(d[i], h[i], sizeof(h[i]), hipMemcpyHostToDevice));
+  }
+  memset(&t, 0, sizeof(t));
+  t.w = d[W_W], t.g = d[W_G], t.m = d[W_M], t.v = d[W_V], t.n = N1;
+  MOE_OK_OR_FAIL(moe_adamw_step(&step, &t, 1, NULL, NULL));
+  HIP_OK(hipDeviceSynchronize());
+  for (int i = 0; i < W_COUNT; ++i) HIP_OK(hipMemcpy(h[i], d[i], sizeof(h[i]), hipMemcpyDeviceToHost));
+  for (int i = 0; i < N1; ++i) {
+    const double g = h[W_G][i], want = i - (g > 0 ? 0.25 : -0.25);
+    if (fabs(h[W_W][i] - want) > 1e-6 * (fabs(want) + 1)) FAIL("AdamW weight %d: %g against %g", i, h[W_W][i], want);
+    if (h[W_M][i] != 0.5 * g || fabs(h[W_V][i] - 0.25 * g * g) > 1e-6 * g * g) FAIL("AdamW states of %d", i);
+  }
+  if (moe_adamw_step(&step, &t, -1, NULL, NULL) != MOE_ERR_INVALID_ARG) FAIL("n = -1 was not refused");
+  printf("c-abi check (weights) ok\n");
+
+done:
+  for (int i = 0; i < W_COUNT; ++i) hipFree(d[i]);
   return rc;
 }
