@@ -66,8 +66,8 @@ class Problem(ctypes.Structure):
 
 
 class AdamW(ctypes.Structure):
-    _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
-                ("eps", ctypes.c_float), ("step", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
                 ("g_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32)]
 
 

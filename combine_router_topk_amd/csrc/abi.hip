@@ -686,9 +686,9 @@ moe_status moe_adamw_step(const moe_adamw* h, const moe_adamw_tensor* tensors, i
   if (h == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: h is NULL", fn);
   if (n < 0) return fail(MOE_ERR_INVALID_ARG, "%s: n=%d < 0", fn, n);
   if (!std::isfinite(h->lr)) return fail(MOE_ERR_INVALID_ARG, "%s: lr=%g is not finite", fn, h->lr);
-  if (!(h->beta1 >= 0.0f && h->beta1 < 1.0f)) return fail(MOE_ERR_INVALID_ARG, "%s: beta1=%g outside [0, 1)", fn, h->beta1);
-  if (!(h->beta2 >= 0.0f && h->beta2 < 1.0f)) return fail(MOE_ERR_INVALID_ARG, "%s: beta2=%g outside [0, 1)", fn, h->beta2);
-  if (!(h->eps >= 0.0f) || !std::isfinite(h->eps))
+  if (!(h->beta1 >= 0.0 && h->beta1 < 1.0)) return fail(MOE_ERR_INVALID_ARG, "%s: beta1=%g outside [0, 1)", fn, h->beta1);
+  if (!(h->beta2 >= 0.0 && h->beta2 < 1.0)) return fail(MOE_ERR_INVALID_ARG, "%s: beta2=%g outside [0, 1)", fn, h->beta2);
+  if (!(h->eps >= 0.0) || !std::isfinite(h->eps))
     return fail(MOE_ERR_INVALID_ARG, "%s: eps=%g is not finite and >= 0", fn, h->eps);
   if (h->step < 1) return fail(MOE_ERR_INVALID_ARG, "%s: step=%d < 1", fn, h->step);
   for (const int32_t d : {h->w_dtype, h->g_dtype})
@@ -726,7 +726,7 @@ moe_status moe_adamw_step(const moe_adamw* h, const moe_adamw_tensor* tensors, i
     }
   }
   clear_stale_error();
-  const moe::AdamWStep step{h->lr, h->beta1, h->beta2, h->eps, static_cast<float>(h->step), control};
+  const moe::AdamWStep step{h->lr, h->beta1, h->beta2, h->eps, h->step, control};
   const int act = h->w_dtype != MOE_F32 ? h->w_dtype : h->g_dtype != MOE_F32 ? h->g_dtype : MOE_F16;
   return hip_status(moe::launch_adamw(step, tensors, n, h->w_dtype == MOE_F32, h->g_dtype == MOE_F32, act, s8,
                                       static_cast<hipStream_t>(stream)),

@@ -175,7 +175,8 @@ hipError_t launch_layer_few_tokens(const float* logits, const void* x, const voi
                                    hipStream_t s);
 
 struct AdamWStep {
-  float lr, beta1, beta2, eps, step;
+  double lr, beta1, beta2, eps;
+  int step;
   const float* control;
 };
 int64_t adamw_most_elements();  // of a tensor

@@ -584,7 +584,8 @@ moe_status moe_layer_few_tokens(const moe_problem* p, int32_t I, const float* lo
 /* ---- training the weights --------------------------------------------------- */
 
 /* One AdamW step.
- *   lr, beta1, beta2, eps  finite, eps >= 0, 0 <= beta < 1
+ *   lr, beta1, beta2, eps  finite, eps >= 0, 0 <= beta < 1; in 64 bits, as 1 -
+ *               0.999 is off by 1.3e-5 of itself in 32
  *   step        1 for the first one
  *   w_dtype     MOE_F32, MOE_F16 or MOE_BF16, of every tensor's w
  *   g_dtype     of every tensor's g: MOE_F32, or 16 bits (with 16-bit w the same
@@ -592,7 +593,7 @@ moe_status moe_layer_few_tokens(const moe_problem* p, int32_t I, const float* lo
  *   state_bits  32, or 8: m and v as 8-bit rows (e4m3 codes, one fp32 scale for
  *               each 128 elements, counted from the tensor's start)             */
 typedef struct {
-  float lr, beta1, beta2, eps;
+  double lr, beta1, beta2, eps;
   int32_t step, w_dtype, g_dtype, state_bits;
 } moe_adamw;
 
@@ -626,12 +627,16 @@ typedef struct {
  *   w = w - lr weight_decay w - lr (m / c1) / (sqrt(v / c2) + eps)
  *   c1 = 1 - beta1^step,  c2 = 1 - beta2^step
  * w is taken from master where that is given, updated in fp32 and rounded once.
+ * m and v are sums of products each rounded to fp32, with no multiply-add in their
+ * place, an 8-bit state's scale is its largest magnitude times the rounded 1 / 448,
+ * and its code the rounded quotient of value and scale: the states are those of the
+ * same formulas in elementary fp32 operations, bit for bit.
  * With 8-bit states the step uses m and v before they are rounded to 8 bits; a
  * root of v above 0 takes at least the smallest code, so that it stays above 0. A
  * gradient that is not finite makes m and v of its 128 elements NaN for good;
  * control's scale can skip such a step.
  * `tensors` is a HOST array, read during the call; nothing of it is kept. Up to 56
- * tensors go into one launch. A tensor has fewer than 2^37 elements
+ * tensors go into one launch. A tensor has fewer than 2^35 elements
  * (MOE_ERR_UNSUPPORTED).
  *   control  f32 [3] on the device (read) or NULL: learning rate, step number and a
  *            factor for the gradients in place of h->lr, h->step and 1, for

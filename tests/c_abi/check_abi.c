@@ -705,7 +705,7 @@ int moe_c_abi_check_weights(void) {
   float h[W_COUNT][N1];
   void* d[W_COUNT] = {NULL};
   int rc = 0;
-  moe_adamw step = {0.25f, 0.5f, 0.75f, 0.0f, 1, MOE_F32, MOE_F32, 32};
+  moe_adamw step = {0.25, 0.5, 0.75, 0.0, 1, MOE_F32, MOE_F32, 32};
   moe_adamw_tensor t;
 
   /* 1. AdamW's first step without decay moves every weight by lr against its
