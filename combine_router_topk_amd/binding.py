@@ -40,7 +40,11 @@ EXPORTED = ("moe_version", "moe_build_id", "moe_status_string", "moe_last_error"
             "moe_routing_stats", "moe_token_balanced_split",
            "moe_rms_norm", "moe_rms_norm_workspace_bytes", "moe_rms_norm_backward",
            "moe_expert_gemm", "moe_expert_gemm_swiglu", "moe_layer_workspace_bytes",
-           "moe_layer_few_tokens", "moe_adamw_step")
+           "moe_layer_few_tokens", "moe_packed_weight_bytes", "moe_expert_gemm_packed",
+           "moe_expert_gemm_swiglu_packed", "moe_layer_packed_workspace_bytes", "moe_layer_few_tokens_packed",
+           "moe_adamw_step")
+
+MOE_PACKED_INT, MOE_PACKED_E2M1 = 1, 2
 
 _TORCH_ACT = {MOE_F16: torch.float16, MOE_BF16: torch.bfloat16}
 E4M3 = torch.float8_e4m3fn
@@ -65,6 +69,13 @@ class Problem(ctypes.Structure):
                 f"act_dtype={self.act_dtype}, flags={self.flags})")
 
 
+class PackedFormat(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_int32), ("group", ctypes.c_int32), ("scale_dtype", ctypes.c_int32)]
+
+    def __repr__(self):
+        return f"PackedFormat(codes={self.codes}, group={self.group}, scale_dtype={self.scale_dtype})"
+
+
 class AdamW(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("step", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
@@ -80,7 +91,7 @@ def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python combine_router_topk_amd/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
-    P = ctypes.POINTER(Problem)
+    P, F = ctypes.POINTER(Problem), ctypes.POINTER(PackedFormat)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     sig = {
         "moe_version": (i32, []),
@@ -115,6 +126,11 @@ def _load() -> ctypes.CDLL:
         "moe_expert_gemm_swiglu": (i32, [P, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
         "moe_layer_workspace_bytes": (i32, [P, i32, ctypes.POINTER(sz)]),
         "moe_layer_few_tokens": (i32, [P, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "moe_packed_weight_bytes": (i32, [F, i32, i32, i32, ctypes.POINTER(sz)]),
+        "moe_expert_gemm_packed": (i32, [P, F, i32, i32, vp, vp, vp, vp, vp, vp, vp]),
+        "moe_expert_gemm_swiglu_packed": (i32, [P, F, i32, i32, vp, vp, vp, vp, vp, vp, vp]),
+        "moe_layer_packed_workspace_bytes": (i32, [P, i32, ctypes.POINTER(sz)]),
+        "moe_layer_few_tokens_packed": (i32, [P, F, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "moe_adamw_step": (i32, [ctypes.POINTER(AdamW), ctypes.POINTER(_AdamWTensor), i32, vp, vp]),
     }
     for name, (res, args) in sig.items():
@@ -523,6 +539,65 @@ def moe_layer_few_tokens(p: Problem, I: int, logits, x, w_up, s_up, w_down, s_do
            a(s_up, f32, E * scale_blocks(2 * I) * nh, "s_up"), a(w_down, w_dt, E * H * I, "w_down"),
            a(s_down, f32, E * nh * ni, "s_down"), a(idx, torch.int32, n, "idx"), a(w, f32, n, "w"),
            a(out, out_dt, T * H, "out"), a(ws, None, None, "ws"), _nbytes(ws))
+
+
+def make_packed_format(codes: int, group: int, scale_dtype: int) -> PackedFormat:
+    return PackedFormat(codes, group, scale_dtype)
+
+
+def moe_packed_weight_bytes(f: PackedFormat, E: int, rows: int, cols: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.moe_packed_weight_bytes(ctypes.byref(f), E, rows, cols, ctypes.byref(n)), "moe_packed_weight_bytes")
+    return n.value
+
+
+def _packed_bytes(f: PackedFormat, E: int, rows: int, cols: int) -> int:
+    """The same, 0 for sizes that the call itself refuses."""
+    n = ctypes.c_size_t(0)
+    _lib.moe_packed_weight_bytes(ctypes.byref(f), E, rows, cols, ctypes.byref(n))
+    return n.value
+
+
+def moe_expert_gemm_packed(p: Problem, f: PackedFormat, K: int, N: int, a, src, w, counts, expert_offsets, y,
+                           stream=None) -> None:
+    """src None: a holds the T k rows in send order; given: the T token rows. w holds
+    uint8."""
+    act, n, arg = _TORCH_ACT.get(p.act_dtype), p.T * p.k, _Args("moe_expert_gemm_packed")
+    out_dt = torch.float32 if p.flags & MOE_FLAG_OUT_F32 else act
+    arg.call(_lib.moe_expert_gemm_packed, stream, ctypes.byref(p), ctypes.byref(f), K, N,
+             arg(a, act, (n if src is None else p.T) * K, "a"), arg(src, torch.int32, n, "src"),
+             arg(w, torch.uint8, _packed_bytes(f, p.E, N, K), "w"), arg(counts, torch.int32, p.E, "counts"),
+             arg(expert_offsets, torch.int32, p.E, "expert_offsets"), arg(y, out_dt, n * N, "y"))
+
+
+def moe_expert_gemm_swiglu_packed(p: Problem, f: PackedFormat, K: int, I: int, a, src, w, counts, expert_offsets, h,
+                                  stream=None) -> None:
+    """w holds 2 I rows an expert, the gate's first; src as in moe_expert_gemm_packed."""
+    act, n, arg = _TORCH_ACT.get(p.act_dtype), p.T * p.k, _Args("moe_expert_gemm_swiglu_packed")
+    arg.call(_lib.moe_expert_gemm_swiglu_packed, stream, ctypes.byref(p), ctypes.byref(f), K, I,
+             arg(a, act, (n if src is None else p.T) * K, "a"), arg(src, torch.int32, n, "src"),
+             arg(w, torch.uint8, _packed_bytes(f, p.E, 2 * I, K), "w"), arg(counts, torch.int32, p.E, "counts"),
+             arg(expert_offsets, torch.int32, p.E, "expert_offsets"), arg(h, act, n * I, "h"))
+
+
+def moe_layer_packed_workspace_bytes(p: Problem, I: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.moe_layer_packed_workspace_bytes(ctypes.byref(p), I, ctypes.byref(n)),
+           "moe_layer_packed_workspace_bytes")
+    return n.value
+
+
+def moe_layer_few_tokens_packed(p: Problem, f: PackedFormat, I: int, logits, x, w_up, w_down, idx, w, out, ws,
+                                stream=None) -> None:
+    """w_up and w_down hold uint8."""
+    act, T, E, H, n = _TORCH_ACT.get(p.act_dtype), p.T, p.E, p.H, p.T * p.k
+    out_dt = torch.float32 if p.flags & MOE_FLAG_OUT_F32 else act
+    a = _Args("moe_layer_few_tokens_packed")
+    a.call(_lib.moe_layer_few_tokens_packed, stream, ctypes.byref(p), ctypes.byref(f), I,
+           a(logits, torch.float32, T * E, "logits"), a(x, act, T * H, "x"),
+           a(w_up, torch.uint8, _packed_bytes(f, E, 2 * I, H), "w_up"),
+           a(w_down, torch.uint8, _packed_bytes(f, E, H, I), "w_down"), a(idx, torch.int32, n, "idx"),
+           a(w, torch.float32, n, "w"), a(out, out_dt, T * H, "out"), a(ws, None, None, "ws"), _nbytes(ws))
 
 
 def make_adamw(lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, step: int = 1) -> AdamW:

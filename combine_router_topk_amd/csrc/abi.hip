@@ -9,6 +9,7 @@
 
 #include "launch.hpp"
 #include "moe_route.h"
+#include "packed.hpp"
 
 // Scratch of moe_route_assign_layout_noalloc: a static device array, so the
 // call needs no allocation. Each GPU the library runs on holds its own copy
@@ -179,6 +180,34 @@ moe_status check_layer(const moe_problem* p, int32_t I, const char* fn) {
   if (p->T > MOE_MAX_FEW_TOKENS)
     return fail(MOE_ERR_UNSUPPORTED, "%s: T=%d is over %d", fn, p->T, MOE_MAX_FEW_TOKENS);
   return MOE_OK;
+}
+
+moe_status check_packed(const moe_packed_format* f, moe::PackedFormat* out, const char* fn) {
+  if (f == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: format is NULL", fn);
+  if (f->codes != MOE_PACKED_INT && f->codes != MOE_PACKED_E2M1)
+    return fail(MOE_ERR_INVALID_ARG, "%s: codes=%d is neither MOE_PACKED_INT nor MOE_PACKED_E2M1", fn, f->codes);
+  if (f->group != 32 && f->group != 64 && f->group != 128)
+    return fail(MOE_ERR_INVALID_ARG, "%s: group=%d is none of 32, 64, 128", fn, f->group);
+  if (f->scale_dtype != MOE_F16 && f->scale_dtype != MOE_BF16)
+    return fail(MOE_ERR_INVALID_ARG, "%s: scale_dtype=%d is neither MOE_F16 nor MOE_BF16", fn, f->scale_dtype);
+  *out = {f->codes, moe::kPackedCols / f->group, f->scale_dtype};
+  return MOE_OK;
+}
+
+// Checks shared by the two products with packed weights; n is the weight rows of an expert.
+moe_status check_packed_gemm(const moe_problem* p, int32_t K, int64_t n, const void* a, const int32_t* src,
+                             const void* w, const int32_t* counts, const int32_t* expert_offsets, const char* fn) {
+  if (K <= 0 || K % 8 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: K=%d is not a positive multiple of 8", fn, K);
+  if (K > (1 << 24)) return fail(MOE_ERR_UNSUPPORTED, "%s: K=%d is over 2^24", fn, K);
+  if (n > (1 << 24) || !moe::packed_gemm_fits(p->T, p->E, p->k, static_cast<int>(n)))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: T*k=%d rows and %lld weight rows have too many tiles", fn, p->T * p->k,
+                static_cast<long long>(n));
+  if (p->T == 0) return MOE_OK;
+  CHECK(need(a, 16, fn, "a"));
+  if (src != nullptr) CHECK(need(src, 4, fn, "src"));
+  CHECK(need(w, 16, fn, "w"));
+  CHECK(need(counts, 4, fn, "counts"));
+  return need(expert_offsets, 4, fn, "expert_offsets");
 }
 
 }  // namespace
@@ -677,6 +706,88 @@ moe_status moe_layer_few_tokens(const moe_problem* p, int32_t I, const float* lo
                                                  p->H, I, idx, w, out, ws, p->act_dtype,
                                                  (p->flags & MOE_FLAG_OUT_F32) != 0,
                                                  static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+moe_status moe_packed_weight_bytes(const moe_packed_format* f, int32_t E, int32_t rows, int32_t cols, size_t* bytes) {
+  const char* fn = "moe_packed_weight_bytes";
+  moe::PackedFormat fmt;
+  CHECK(check_packed(f, &fmt, fn));
+  if (E < 1 || rows < 1 || cols < 1)
+    return fail(MOE_ERR_INVALID_ARG, "%s: E=%d, rows=%d, cols=%d: at least 1 of each", fn, E, rows, cols);
+  if (E > MOE_MAX_E || rows > (1 << 24) || cols > (1 << 24))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: E=%d, rows=%d, cols=%d: over %d, 2^24, 2^24", fn, E, rows, cols, MOE_MAX_E);
+  if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is NULL", fn);
+  *bytes = static_cast<size_t>(E) * moe::packed_row_tiles(rows) * moe::packed_col_tiles(cols) *
+           moe::packed_tile_bytes(fmt.per);
+  return MOE_OK;
+}
+
+moe_status moe_expert_gemm_packed(const moe_problem* p, const moe_packed_format* f, int32_t K, int32_t N,
+                                  const void* a, const int32_t* src, const void* w, const int32_t* counts,
+                                  const int32_t* expert_offsets, void* y, void* stream) {
+  const char* fn = "moe_expert_gemm_packed";
+  moe::PackedFormat fmt;
+  CHECK(check_problem(p, fn));
+  CHECK(check_packed(f, &fmt, fn));
+  if (N <= 0 || N % 8 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: N=%d is not a positive multiple of 8", fn, N);
+  CHECK(check_packed_gemm(p, K, N, a, src, w, counts, expert_offsets, fn));
+  if (p->T == 0) return MOE_OK;
+  CHECK(need(y, 16, fn, "y"));
+  clear_stale_error();
+  return hip_status(moe::launch_packed_gemm(fmt, a, src, w, counts, expert_offsets, p->T, p->E, p->k, K, N, false, y,
+                                            p->act_dtype, (p->flags & MOE_FLAG_OUT_F32) != 0,
+                                            static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+moe_status moe_expert_gemm_swiglu_packed(const moe_problem* p, const moe_packed_format* f, int32_t K, int32_t I,
+                                         const void* a, const int32_t* src, const void* w, const int32_t* counts,
+                                         const int32_t* expert_offsets, void* h, void* stream) {
+  const char* fn = "moe_expert_gemm_swiglu_packed";
+  moe::PackedFormat fmt;
+  CHECK(check_problem(p, fn));
+  CHECK(check_packed(f, &fmt, fn));
+  if (I <= 0 || I % 16 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: I=%d is not a positive multiple of 16", fn, I);
+  CHECK(check_packed_gemm(p, K, 2 * static_cast<int64_t>(I), a, src, w, counts, expert_offsets, fn));
+  if (p->T == 0) return MOE_OK;
+  CHECK(need(h, 16, fn, "h"));
+  clear_stale_error();
+  return hip_status(moe::launch_packed_gemm(fmt, a, src, w, counts, expert_offsets, p->T, p->E, p->k, K, 2 * I, true, h,
+                                            p->act_dtype, false, static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+moe_status moe_layer_packed_workspace_bytes(const moe_problem* p, int32_t I, size_t* bytes) {
+  const char* fn = "moe_layer_packed_workspace_bytes";
+  CHECK(check_layer(p, I, fn));
+  if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is NULL", fn);
+  *bytes = moe::layer_packed_ws_bytes(p->T, p->E, p->k, p->H, I);
+  return MOE_OK;
+}
+
+moe_status moe_layer_few_tokens_packed(const moe_problem* p, const moe_packed_format* f, int32_t I, const float* logits,
+                                       const void* x, const void* w_up, const void* w_down, int32_t* idx, float* w,
+                                       void* out, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_layer_few_tokens_packed";
+  moe::PackedFormat fmt;
+  CHECK(check_layer(p, I, fn));
+  CHECK(check_packed(f, &fmt, fn));
+  if (p->T == 0) return MOE_OK;
+  CHECK(need(logits, 4, fn, "logits"));
+  CHECK(need(x, 16, fn, "x"));
+  CHECK(need(w_up, 16, fn, "w_up"));
+  CHECK(need(w_down, 16, fn, "w_down"));
+  CHECK(need(idx, 4, fn, "idx"));
+  CHECK(need(w, 4, fn, "w"));
+  CHECK(need(out, 16, fn, "out"));
+  CHECK(need(ws, 256, fn, "ws"));
+  const size_t req = moe::layer_packed_ws_bytes(p->T, p->E, p->k, p->H, I);
+  if (ws_bytes < req) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, req);
+  clear_stale_error();
+  return hip_status(moe::launch_layer_few_tokens_packed(fmt, logits, x, w_up, w_down, p->T, p->E, p->k, p->H, I, idx, w,
+                                                        out, ws, p->act_dtype, (p->flags & MOE_FLAG_OUT_F32) != 0,
+                                                        static_cast<hipStream_t>(stream)),
                     fn);
 }
 

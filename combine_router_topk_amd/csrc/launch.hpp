@@ -174,6 +174,22 @@ hipError_t launch_layer_few_tokens(const float* logits, const void* x, const voi
                                    int32_t* idx, float* w, void* out, void* ws, int act, bool out_f32,
                                    hipStream_t s);
 
+// packed.hpp
+struct PackedFormat {
+  int codes;      // MOE_PACKED_INT or MOE_PACKED_E2M1
+  int per;        // scales of a row in a tile: 1, 2 or 4
+  int scale_act;  // format of the scales: 1 fp16, 2 bf16
+};
+// Whether 32 bits hold the tiles of a problem of these sizes (n: weight rows of an expert).
+bool packed_gemm_fits(int T, int E, int k, int n);
+hipError_t launch_packed_gemm(const PackedFormat& f, const void* a, const int32_t* src, const void* w,
+                              const int32_t* counts, const int32_t* offsets, int T, int E, int k, int K, int n,
+                              bool swiglu, void* y, int act, bool out_f32, hipStream_t s);
+size_t layer_packed_ws_bytes(int T, int E, int k, int H, int I);
+hipError_t launch_layer_few_tokens_packed(const PackedFormat& f, const float* logits, const void* x, const void* w_up,
+                                          const void* w_down, int T, int E, int k, int H, int I, int32_t* idx, float* w,
+                                          void* out, void* ws, int act, bool out_f32, hipStream_t s);
+
 struct AdamWStep {
   double lr, beta1, beta2, eps;
   int step;

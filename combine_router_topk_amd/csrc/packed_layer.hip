@@ -1,0 +1,366 @@
+// A whole mixture-of-experts layer for at most 64 tokens with weights in 4 bits
+// (packed.hpp), in the launches of the layer in layer.hip:
+//
+//   h[t, j] = round16(silu(Wg x[t]) * (Wu x[t])),  (Wg; Wu) = expert idx[t, j]'s
+//   out[t]  = round(sum over j of w[t, j] (Wd h[t, j])), summed in fp32
+//
+// The tokens are the matrix instruction's first operand here and the weight rows
+// its second, so that a lane's results belong to one weight row and take one
+// scale.
+#include "device.hpp"
+#include "few_tokens.hpp"
+#include "launch.hpp"
+#include "packed.hpp"
+#include "quant.hpp"
+
+namespace moe {
+
+namespace {
+
+constexpr int kUpThreads = 256, kUpWaves = kUpThreads / kWave;
+constexpr int kUpBlocks = 1280;
+constexpr int kDownThreads = 512, kDownWaves = kDownThreads / kWave;
+
+struct PackedArgs : RouteArgs {
+  const void* x;
+  const unsigned char* w_up;
+  const unsigned char* w_down;
+  int H, I, scale_act;
+  void* h;
+  void* out;
+  bool out_f32;
+  float* part;  // [shares][T][H]: sums of the down product's shares
+};
+
+__device__ __forceinline__ void route_any(const RouteArgs& g, int t, int lane, int* idx, bool write) {
+  if (g.E <= 64) route_token<1>(g, t, lane, idx, write);
+  else if (g.E <= 256) route_token<4>(g, t, lane, idx, write);
+  else route_token<16>(g, t, lane, idx, write);
+}
+
+__global__ __launch_bounds__(kRouteThreads) void packed_route_kernel(RouteArgs g) {
+  __shared__ int items;
+  extern __shared__ __align__(16) char tables[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int pairs = g.T * g.k;
+  const Tables sh(tables, pairs, g.E);
+  for (int t = wave; t < g.T; t += kRouteThreads / kWave) route_any(g, t, lane, sh.idx, true);
+  build_tables<kRouteThreads>(g, sh, &items);
+  for (int i = tid; i < items; i += kRouteThreads) g.item[i] = sh.item[i];
+  for (int p = tid; p < pairs; p += kRouteThreads) g.order[p] = sh.order[p];
+  if (tid == 0) {
+    g.head[0] = items;
+    g.head[1] = 0;
+  }
+}
+
+// ---- gate and up products, SwiGLU ----------------------------------------------
+
+// ROUTES: every block routes the tokens itself and takes tiles in turn; else the
+// tables are there, and a block that is done takes the next tile that nobody has.
+template <int ACT, int CODES, int PER, bool ROUTES>
+__global__ __launch_bounds__(kUpThreads, 5) void packed_up_kernel(PackedArgs g) {
+  __shared__ float4 part[2][kUpWaves][2][kWave];
+  __shared__ int items, next_tile[2];
+  extern __shared__ __align__(16) char tables[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int pairs = g.T * g.k;
+  const Tables sh(tables, pairs, ROUTES ? g.E : 0);
+  if constexpr (ROUTES) {
+    for (int t = wave; t < g.T; t += kUpWaves) route_any(g, t, lane, sh.idx, blockIdx.x == 0);
+    build_tables<kUpThreads>(g, sh, &items);
+  } else {
+    if (tid == 0) items = g.head[0];
+    for (int i = tid; i < pairs; i += kUpThreads) {  // those past the items are not used
+      sh.item[i] = g.item[i];
+      sh.order[i] = g.order[i];
+    }
+    __syncthreads();
+  }
+
+  constexpr int TB = packed_tile_bytes(PER);
+  const int r = lane & 15, grp = lane >> 4;
+  const int n_tiles = g.I / kPackedRows, steps = packed_col_tiles(g.H);
+  const int work = items * n_tiles, blocks = gridDim.x;
+  const size_t strip = static_cast<size_t>(steps) * TB;  // a row of tiles
+  int turn = 0;
+  for (int i = blockIdx.x; i < work; turn ^= 1) {
+    int next = i + blocks;
+    if constexpr (!ROUTES) {
+      if (tid == 0) next = blocks + atomicAdd(&g.head[1], 1);
+    }
+    const int4 it = sh.item[i / n_tiles];
+    const int tile = i % n_tiles;
+    const int e = __builtin_amdgcn_readfirstlane(it.x), off = it.y, have = it.z;
+    const unsigned char* gate_row = g.w_up + (static_cast<size_t>(e) * 2 * n_tiles + tile) * strip;
+    const unsigned char* up_row = gate_row + n_tiles * strip;
+    const int my_pair = sh.order[off + min(r, have - 1)];
+    const uint16_t* tok = static_cast<const uint16_t*>(g.x) + static_cast<size_t>(my_pair / g.k) * g.H;
+    const int cols = r < have ? g.H : 0;
+
+    v4f gate = {0, 0, 0, 0}, up = {0, 0, 0, 0};
+    constexpr int D = 1;  // steps in flight
+    for (int kb0 = wave; kb0 < steps; kb0 += kUpWaves * D) {
+      PackedTile<PER> a[D], b[D];
+      PackedRows c[D];
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const int kb = kb0 + d * kUpWaves;
+        if (kb < steps) {
+          a[d].load(gate_row + static_cast<size_t>(kb) * TB, lane);
+          b[d].load(up_row + static_cast<size_t>(kb) * TB, lane);
+          c[d].load(tok, kb, grp, cols);
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (kb0 + d * kUpWaves < steps) {
+          float sg[PER], su[PER];
+          a[d].scales(g.scale_act, sg);
+          b[d].scales(g.scale_act, su);
+          v4f start[PER];
+          packed_start<ACT, CODES, PER>(c[d], start);
+          packed_product<ACT, CODES, PER>(c[d], a[d], sg, start, gate);
+          packed_product<ACT, CODES, PER>(c[d], b[d], su, start, up);
+        }
+      }
+    }
+    part[turn][wave][0][lane] = make_float4(gate[0], gate[1], gate[2], gate[3]);
+    part[turn][wave][1][lane] = make_float4(up[0], up[1], up[2], up[3]);
+    if (!ROUTES && tid == 0) next_tile[turn] = next;
+    __syncthreads();
+    i = ROUTES ? next : __builtin_amdgcn_readfirstlane(next_tile[turn]);
+    // thread tid sums value tid % 4 of lane tid / 4: token 4 (tid / 64) + tid % 4 of
+    // the item, weight row (tid / 4) % 16 of the tile
+    const int c = (tid >> 6) * 4 + (tid & 3), n = (tid >> 2) & 15;
+    float zg = 0.0f, zu = 0.0f;
+#pragma unroll
+    for (int wv = 0; wv < kUpWaves; ++wv) {
+      zg += reinterpret_cast<const float*>(part[turn][wv][0])[tid];
+      zu += reinterpret_cast<const float*>(part[turn][wv][1])[tid];
+    }
+    if (c < have) {
+      const float h = silu(zg) * zu;
+      static_cast<uint16_t*>(g.h)[static_cast<size_t>(sh.order[off + c]) * g.I + tile * kPackedRows + n] =
+          static_cast<uint16_t>(pack2<ACT>(h, 0.0f));
+    }
+  }
+}
+
+// ---- down product and weighted combine -------------------------------------------
+
+template <int TT>
+struct DownShared {
+  int idx[kMaxPairs];
+  float w[kMaxPairs];
+  int flag[kMaxE];
+  int active[kMaxPairs];
+  int n_active;
+  float4 part[kDownWaves][TT][kWave];
+};
+
+// Each block owns 16 columns of the output for every token (TT groups of 16), its
+// waves contiguous parts of the (expert, step of K) sequence. With several shares
+// blockIdx.y is the share of the sequence, and packed_sum_kernel adds them up.
+template <int ACT, int CODES, int PER, int TT>
+__global__ __launch_bounds__(kDownThreads, 4) void packed_down_kernel(PackedArgs g) {
+  __shared__ DownShared<TT> sh;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int pairs = g.T * g.k;
+  for (int e = tid; e < g.E; e += kDownThreads) sh.flag[e] = 0;
+  __syncthreads();
+  for (int p = tid; p < pairs; p += kDownThreads) {
+    const int e = min(max(g.idx[p], 0), g.E - 1);
+    sh.idx[p] = e;
+    sh.w[p] = g.w[p];
+    sh.flag[e] = 1;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    int n = 0;
+    for (int e0 = 0; e0 < g.E; e0 += kWave) {
+      const int e = e0 + lane;
+      const bool on = e < g.E && sh.flag[e] != 0;
+      const uint64_t m = ballot(on);
+      if (on) sh.active[n + __builtin_popcountll(m & lanemask_lt(lane))] = e;
+      n += __builtin_popcountll(m);
+    }
+    if (lane == 0) sh.n_active = n;
+  }
+  __syncthreads();
+
+  constexpr int TB = packed_tile_bytes(PER);
+  const int r = lane & 15, grp = lane >> 4;
+  const int tile = blockIdx.x, tiles = packed_row_tiles(g.H), steps = packed_col_tiles(g.I);
+  const size_t strip = static_cast<size_t>(steps) * TB;
+  const int shares = gridDim.y, share = blockIdx.y;
+  const int all = sh.n_active * steps;
+  const int total = all / shares + (share < all % shares ? 1 : 0);
+  int q = all / shares * share + min(share, all % shares) + total / kDownWaves * wave + min(wave, total % kDownWaves);
+  const int q_end = q + total / kDownWaves + (wave < total % kDownWaves ? 1 : 0);
+
+  v4f acc[TT];
+#pragma unroll
+  for (int u = 0; u < TT; ++u) acc[u] = v4f{0, 0, 0, 0};
+  while (q < q_end) {
+    const int ei = q / steps, k0 = q % steps, k1 = min(steps, k0 + q_end - q);
+    q += k1 - k0;
+    const int e = __builtin_amdgcn_readfirstlane(sh.active[ei]);
+    const unsigned char* row = g.w_down + (static_cast<size_t>(e) * tiles + tile) * strip;
+    const uint16_t* tok[TT];
+    float wt[TT];
+    bool on[TT], any[TT];
+    v4f sum[TT];
+#pragma unroll
+    for (int u = 0; u < TT; ++u) {
+      const int t = u * kPackedRows + r;
+      int pair = -1;
+      if (t < g.T)
+        for (int j = 0; j < g.k; ++j)
+          if (sh.idx[t * g.k + j] == e) pair = t * g.k + j;
+      on[u] = pair >= 0;
+      any[u] = ballot(on[u]) != 0;
+      wt[u] = on[u] ? sh.w[pair] : 0.0f;
+      tok[u] = static_cast<const uint16_t*>(g.h) + static_cast<size_t>(on[u] ? pair : 0) * g.I;
+      sum[u] = v4f{0, 0, 0, 0};
+    }
+    constexpr int D = TT == 4 ? 1 : 2;  // steps in flight
+    for (int kb0 = k0; kb0 < k1; kb0 += D) {
+      PackedTile<PER> a[D];
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        if (kb0 + d < k1) a[d].load(row + static_cast<size_t>(kb0 + d) * TB, lane);
+#pragma unroll
+      for (int u = 0; u < TT; ++u) {
+        if (!any[u]) continue;
+        PackedRows c[D];
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+          if (kb0 + d < k1) c[d].load(tok[u], kb0 + d, grp, on[u] ? g.I : 0);
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          if (kb0 + d < k1) {
+            float s[PER];
+            a[d].scales(g.scale_act, s);
+            v4f start[PER];
+            packed_start<ACT, CODES, PER>(c[d], start);
+            packed_product<ACT, CODES, PER>(c[d], a[d], s, start, sum[u]);
+          }
+        }
+      }
+    }
+    // the gate weights of this lane's four tokens
+#pragma unroll
+    for (int u = 0; u < TT; ++u) {
+      if (!any[u]) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = __shfl(wt[u], 4 * grp + i, kWave);
+        acc[u][i] = f != 0.0f ? fmaf(sum[u][i], f, acc[u][i]) : acc[u][i];
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < TT; ++u)
+    sh.part[wave][u][lane] = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
+  __syncthreads();
+  for (int o = tid; o < TT * 256; o += kDownThreads) {
+    const int u = o >> 8, v = o & 255;
+    const int t = u * kPackedRows + (v >> 6) * 4 + (v & 3), n = tile * kPackedRows + ((v >> 2) & 15);
+    float z = 0.0f;
+#pragma unroll
+    for (int wv = 0; wv < kDownWaves; ++wv) z += reinterpret_cast<const float*>(sh.part[wv][u])[v];
+    if (t < g.T) {
+      const size_t at = static_cast<size_t>(t) * g.H + n;
+      if (shares > 1) g.part[static_cast<size_t>(share) * g.T * g.H + at] = z;
+      else if (g.out_f32) static_cast<float*>(g.out)[at] = z;
+      else static_cast<uint16_t*>(g.out)[at] = static_cast<uint16_t>(pack2<ACT>(z, 0.0f));
+    }
+  }
+}
+
+template <int ACT>
+__global__ __launch_bounds__(256) void packed_sum_kernel(PackedArgs g, int shares) {
+  const int n = g.T * g.H / 4, i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const float4* part = reinterpret_cast<const float4*>(g.part);
+  float4 z = part[i];
+  for (int y = 1; y < shares; ++y) {
+    const float4 v = part[static_cast<size_t>(y) * n + i];
+    z = make_float4(z.x + v.x, z.y + v.y, z.z + v.z, z.w + v.w);
+  }
+  if (g.out_f32) static_cast<float4*>(g.out)[i] = z;
+  else static_cast<uint2*>(g.out)[i] = make_uint2(pack2<ACT>(z.x, z.y), pack2<ACT>(z.z, z.w));
+}
+
+constexpr int kShares = 4;
+int shares_of(int T, int E, int k, int H, int I) {
+  const int tiles = packed_row_tiles(H);
+  const long long experts = T * k < E ? T * k : E;
+  return tiles > 256 && tiles % 256 != 0 && experts * H * I >= 1ll << 30 ? kShares : 1;
+}
+
+size_t whole(size_t bytes) { return (bytes + 255) / 256 * 256; }
+size_t inner_bytes(int T, int k, int I) { return whole(static_cast<size_t>(T) * k * I * 2); }
+size_t table_bytes(int T, int k) {
+  return whole(static_cast<size_t>(T) * k * (sizeof(int4) + sizeof(int32_t)) + 2 * sizeof(int32_t));
+}
+
+template <int ACT, int CODES, int PER>
+hipError_t launch(const PackedArgs& g, hipStream_t s) {
+  const int per_token = g.E * ((g.T + 15) / 16);
+  const long long items = static_cast<long long>(g.T * g.k < per_token ? g.T * g.k : per_token) * (g.I / kPackedRows);
+  const int blocks = items < kUpBlocks ? static_cast<int>(items) : kUpBlocks;
+  const size_t lds = Tables::bytes(g.T * g.k, g.E);
+  if (g.T * g.k <= kFewPairs) {
+    packed_up_kernel<ACT, CODES, PER, true><<<blocks, kUpThreads, lds, s>>>(g);
+  } else {
+    packed_route_kernel<<<1, kRouteThreads, lds, s>>>(g);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    packed_up_kernel<ACT, CODES, PER, false><<<blocks, kUpThreads, Tables::bytes(g.T * g.k, 0), s>>>(g);
+  }
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const int shares = shares_of(g.T, g.E, g.k, g.H, g.I);
+  const dim3 grid(packed_row_tiles(g.H), shares);
+  if (g.T <= 16) packed_down_kernel<ACT, CODES, PER, 1><<<grid, kDownThreads, 0, s>>>(g);
+  else if (g.T <= 32) packed_down_kernel<ACT, CODES, PER, 2><<<grid, kDownThreads, 0, s>>>(g);
+  else packed_down_kernel<ACT, CODES, PER, 4><<<grid, kDownThreads, 0, s>>>(g);
+  err = hipGetLastError();
+  if (err != hipSuccess || shares == 1) return err;
+  packed_sum_kernel<ACT><<<(g.T * g.H / 4 + 255) / 256, 256, 0, s>>>(g, shares);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// The inner rows, the tables, the shares' sums.
+size_t layer_packed_ws_bytes(int T, int E, int k, int H, int I) {
+  const int shares = shares_of(T, E, k, H, I);
+  const size_t sums = shares > 1 ? whole(static_cast<size_t>(shares) * T * H * sizeof(float)) : 0;
+  return inner_bytes(T, k, I) + table_bytes(T, k) + sums;
+}
+
+hipError_t launch_layer_few_tokens_packed(const PackedFormat& f, const float* logits, const void* x, const void* w_up,
+                                          const void* w_down, int T, int E, int k, int H, int I, int32_t* idx, float* w,
+                                          void* out, void* ws, int act, bool out_f32, hipStream_t s) {
+  char* tables = static_cast<char*>(ws) + inner_bytes(T, k, I);
+  int4* item = reinterpret_cast<int4*>(tables);
+  int32_t* order = reinterpret_cast<int32_t*>(item + T * k);
+  float* part = reinterpret_cast<float*>(tables + table_bytes(T, k));
+  const PackedArgs g{{logits, T, E, k, idx, w, item, order, order + T * k},
+                     x,
+                     static_cast<const unsigned char*>(w_up),
+                     static_cast<const unsigned char*>(w_down),
+                     H,
+                     I,
+                     f.scale_act,
+                     ws,
+                     out,
+                     out_f32,
+                     part};
+  return with_packed(f, act, [&](auto A, auto C, auto P) { return launch<A(), C(), P()>(g, s); });
+}
+
+}  // namespace moe

@@ -289,12 +289,16 @@ def expert_gate_up(b: Buffers, l: Layer, w: ExpertWeights, stream=None) -> None:
                              b.expert_offsets, l.hq, l.hq_scale, stream)
 
 
+def _act_out(p: B.Problem) -> B.Problem:
+    """The problem with rows in the activation format, whatever b.out is in."""
+    return p if not p.flags & B.MOE_FLAG_OUT_F32 else \
+        B.make_problem(p.T, p.E, p.k, p.H, p.R, p.act_dtype, p.flags & ~B.MOE_FLAG_OUT_F32)
+
+
 def expert_down(b: Buffers, l: Layer, w: ExpertWeights, stream=None) -> None:
     """The experts' outputs in send order (what standin writes otherwise); bf16
     rows from exact sums if the problem has MOE_FLAG_EXACT_SUMS."""
-    p = b.p
-    if p.flags & B.MOE_FLAG_OUT_F32:  # y stays in the activation format
-        p = B.make_problem(p.T, p.E, p.k, p.H, p.R, p.act_dtype, p.flags & ~B.MOE_FLAG_OUT_F32)
+    p = _act_out(b.p)
     B.moe_expert_gemm(p, l.I, p.H, l.hq, l.hq_scale, None, w.w_down, w.s_down, b.counts,
                       b.expert_offsets, b.y, stream)
 
@@ -317,3 +321,108 @@ def layer_few_tokens(b: Buffers, w: ExpertWeights, ws: torch.Tensor, stream=None
 
 def layer_workspace(b: Buffers, I: int) -> torch.Tensor:
     return torch.empty(B.moe_layer_workspace_bytes(b.p, I), dtype=torch.uint8, device=b.idx.device)
+
+
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def _packed_places(f: B.PackedFormat, device) -> tuple[torch.Tensor, torch.Tensor]:
+    """Of each column of a tile, the place of its code in a row's 32 nibbles of
+    each of the four chunks: (chunk, nibble)."""
+    c = torch.arange(128, device=device)
+    j, g, i = c // 32, c % 32 // 8, c % 8
+    inner = 2 * (i % 4) + i // 4 if f.codes == B.MOE_PACKED_INT else i
+    return g, 8 * j + inner
+
+
+def pack_weights(w: torch.Tensor, f: B.PackedFormat) -> torch.Tensor:
+    """Weights [..., rows, cols] in 4 bits (see include/moe_route.h), each group of
+    columns with the scale that takes its largest magnitude to the largest code (7
+    or 6), each value to the nearest code (ties to the even one). Done once for a
+    model, in torch operations on w's device; returns uint8 [..., bytes]."""
+    if w.dim() < 2 or f.group not in (32, 64, 128):
+        raise ValueError("weights [..., rows, cols] and groups of 32, 64 or 128 columns")
+    lead, (rows, cols) = w.shape[:-2], w.shape[-2:]
+    nt, kt, per = -(-rows // 16), -(-cols // 128), 128 // f.group
+    ints = f.codes == B.MOE_PACKED_INT
+    out = []
+    for m in w.reshape(-1, rows, cols):  # one matrix at a time: the fp32 copy is eight times the result
+        v = torch.zeros(nt * 16, kt * 128, device=w.device)
+        v[:rows, :cols] = m.float()
+        if not bool(torch.isfinite(v).all()):
+            raise ValueError("weights that are not finite have no 4-bit form")
+        v = v.view(nt * 16, kt * per, f.group)
+        scale = (v.abs().amax(2) / (7.0 if ints else 6.0)).to(B._TORCH_ACT[f.scale_dtype])
+        if not bool(torch.isfinite(scale).all()):
+            raise ValueError("a group's scale is beyond its 16-bit format")
+        t = v / torch.where(scale == 0, 1.0, scale.float())[:, :, None]
+        if ints:
+            q = t.round().clamp_(-8, 7).add_(8)
+        else:
+            borders = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device=w.device)
+            a = t.abs()  # at a border the even code: below the even borders, above the odd ones
+            q = (a > borders[0]).float()
+            for n, b in enumerate(borders[1:].tolist(), 1):
+                q += (a >= b) if n % 2 else (a > b)
+            q += 8.0 * (t < 0)
+        q = q.view(nt, 16, kt, 128).to(torch.uint8)
+        g, nibble = _packed_places(f, w.device)
+        codes = torch.zeros(nt, kt, 4, 16, 32, dtype=torch.uint8, device=w.device)
+        codes[:, :, g, :, nibble] = q.permute(3, 0, 2, 1)
+        codes = codes[..., ::2] | codes[..., 1::2] << 4
+        scale = scale.view(nt, 16, kt, per).transpose(1, 2).contiguous()
+        out.append(torch.cat([codes.reshape(nt, kt, 1024), scale.view(torch.uint8).view(nt, kt, -1)], 2).view(-1))
+    return torch.stack(out).view(*lead, -1) if out else w.new_zeros((*lead, 0), dtype=torch.uint8)
+
+
+def unpack_weights(packed: torch.Tensor, rows: int, cols: int, f: B.PackedFormat) -> torch.Tensor:
+    """The fp32 values [..., rows, cols] that packed weights stand for."""
+    lead, nt, kt, per = packed.shape[:-1], -(-rows // 16), -(-cols // 128), 128 // f.group
+    p = packed.reshape(-1, nt, kt, 1024 + 32 * per)
+    b = p[..., :1024].reshape(-1, nt, kt, 4, 16, 16)
+    nibbles = torch.stack([b & 15, b >> 4], -1).flatten(-2)
+    g, nibble = _packed_places(f, packed.device)
+    q = nibbles[:, :, :, g, :, nibble].permute(1, 2, 4, 3, 0)  # [matrix, row tile, row, column tile, column]
+    if f.codes == B.MOE_PACKED_INT:
+        v = q.float() - 8
+    else:
+        v = torch.tensor([*E2M1, *(-x for x in E2M1)], device=packed.device)[q.long()]
+    s = p[..., 1024:].contiguous().view(B._TORCH_ACT[f.scale_dtype]).view(-1, nt, kt, 16, per).transpose(2, 3).float()
+    v = v.reshape(*s.shape, f.group) * s[..., None]
+    return v.reshape(-1, nt * 16, kt * 128)[:, :rows, :cols].reshape(*lead, rows, cols)
+
+
+@dataclass
+class PackedExperts:
+    """The experts' weights in 4 bits: E packed matrices w_up [2 I, H] (gate rows
+    first) and w_down [H, I]."""
+    I: int
+    format: B.PackedFormat
+    w_up: torch.Tensor
+    w_down: torch.Tensor
+
+
+def pack_experts(w_up: torch.Tensor, w_down: torch.Tensor, f: B.PackedFormat) -> PackedExperts:
+    """From weights [E, 2 I, H] and [E, H, I] in any float format."""
+    return PackedExperts(I=w_down.shape[-1], format=f, w_up=pack_weights(w_up, f), w_down=pack_weights(w_down, f))
+
+
+def run_layer_packed(b: Buffers, w: PackedExperts, h: torch.Tensor, stream=None) -> None:
+    """Routing, the experts' products with 4-bit weights and the combine, from
+    b.logits and the 16-bit rows b.x to b.out; h [T k, I] takes the inner rows."""
+    route_assign_layout(b, stream)
+    B.moe_expert_gemm_swiglu_packed(b.p, w.format, b.p.H, w.I, b.x, b.src, w.w_up, b.counts, b.expert_offsets, h,
+                                    stream)
+    B.moe_expert_gemm_packed(_act_out(b.p), w.format, w.I, b.p.H, h, None, w.w_down, b.counts, b.expert_offsets, b.y,
+                             stream)
+    combine(b, stream)
+
+
+def layer_few_tokens_packed(b: Buffers, w: PackedExperts, ws: torch.Tensor, stream=None) -> None:
+    """The same layer for a few tokens in two to four launches; `ws` has
+    layer_packed_workspace(b, I) bytes."""
+    B.moe_layer_few_tokens_packed(b.p, w.format, w.I, b.logits, b.x, w.w_up, w.w_down, b.idx, b.w, b.out, ws, stream)
+
+
+def layer_packed_workspace(b: Buffers, I: int) -> torch.Tensor:
+    return torch.empty(B.moe_layer_packed_workspace_bytes(b.p, I), dtype=torch.uint8, device=b.idx.device)

@@ -8,8 +8,8 @@
  * combine and the dispatch, routing statistics, and token-balanced replica
  * routing as the greedy's baseline; and the layer around the routing: the
  * norm that makes its rows with its gradient, the experts' products in
- * block-scaled 8-bit floating point, and the whole layer for a few tokens; and
- * the step that trains weights.
+ * block-scaled 8-bit floating point, and the whole layer for a few tokens, both
+ * with weights in 4 bits, too; and the step that trains weights.
  *
  * Sources (web pages on MoE dispatch and combine):
  *   [METRO]  "METRO AllGather vs AllToAll for MoE decode".
@@ -580,6 +580,79 @@ moe_status moe_layer_few_tokens(const moe_problem* p, int32_t I, const float* lo
                                 const void* w_up, const float* s_up, const void* w_down,
                                 const float* s_down, int32_t* idx, float* w, void* out, void* ws,
                                 size_t ws_bytes, void* stream);
+
+/* ---- weights in 4 bits -------------------------------------------------------
+ *
+ * A packed matrix [rows, cols] is ceil(rows / 16) x ceil(cols / 128) tiles of 16 rows
+ * by 128 columns, row of tiles after row of tiles; several experts' matrices follow
+ * each other. A tile is 1024 bytes of codes, then its rows' scales in 16 bits, [16]
+ * [128 / group]: one for each group of 32, 64 or 128 neighbouring columns. A value is
+ * its code's value times its group's scale. Of the tile's row r and column c = 32 j +
+ * 8 g + i (j, g < 4, i < 8) the code lies in the 32-bit word at byte 16 (16 g + r) + 4 j,
+ *   MOE_PACKED_INT:  bits 8 (i % 4) + 4 (i / 4) .. + 3, values 0 .. 15 for -8 .. 7
+ *   MOE_PACKED_E2M1: bits 4 i .. + 3, a sign and 0, 0.5, 1, 1.5, 2, 3, 4, 6 (the OCP
+ *                    format)
+ * (which scales and codes a matrix takes is the caller's choice; rows and columns
+ * past its end hold any codes and finite scales). So matrix instructions find their
+ * operands without a permutation, and a wave reads a tile in one run.            */
+enum { MOE_PACKED_INT = 1, MOE_PACKED_E2M1 = 2 };
+
+typedef struct {
+  int32_t codes;        /* MOE_PACKED_INT or MOE_PACKED_E2M1 */
+  int32_t group;        /* columns of a scale: 32, 64 or 128 */
+  int32_t scale_dtype;  /* of the scales: MOE_F16 or MOE_BF16 */
+} moe_packed_format;
+
+/* Bytes of E packed matrices [rows, cols] (all at least 1). Host only.          */
+moe_status moe_packed_weight_bytes(const moe_packed_format* f, int32_t E, int32_t rows,
+                                   int32_t cols, size_t* bytes);
+
+/* Experts' products over the routed rows in 16 bits with packed weights:
+ *   y[r, n] = sum over k of a[r', k] * w[e, n, k]
+ * for every row r of expert e's segment, r' as in moe_expert_gemm; rounded once to the
+ * activation format, or written as fp32 with MOE_FLAG_OUT_F32. Codes become 16-bit
+ * numbers exactly, products are exact, sums of 32 columns or more and their
+ * multiplication by the scale are in fp32. Integer codes are summed as 0 .. 15 with 8
+ * times the sum of the row's values taken off, so an infinity in a row makes its
+ * results NaN.
+ *   K   columns of a and w, a multiple of 8     N  rows of w, a multiple of 8
+ *   a   16-bit [rows, K] (read): T k rows in send order, or with src T token rows
+ *   src             i32 [T*k] (read) from moe_layout, or NULL
+ *   w   E packed matrices [N, K] (read)
+ *   counts          i32 [E] (read) from moe_route
+ *   expert_offsets  i32 [E] (read) from moe_layout
+ *   y               [T*k, N] in the activation format or fp32 (write)
+ * a, w and y are 16-byte aligned. Rows in no segment are left untouched; a src outside
+ * [0, T*k) is clamped into it, and segments are cut to the T k rows. H of the problem is
+ * not used. K and N are at most 2^24 and (T k / 16 + E) ceil(N / 32) is below 2^30
+ * (MOE_ERR_UNSUPPORTED).                                                      */
+moe_status moe_expert_gemm_packed(const moe_problem* p, const moe_packed_format* f, int32_t K,
+                                  int32_t N, const void* a, const int32_t* src, const void* w,
+                                  const int32_t* counts, const int32_t* expert_offsets, void* y,
+                                  void* stream);
+
+/* The gate and up products with SwiGLU in one pass: with z = the product above for
+ * weights of 2 I rows (gate rows 0 .. I-1, up rows I .. 2I-1),
+ *   h[r, i] = round16(z[r, i] / (1 + exp(-z[r, i])) * z[r, I + i])
+ *   I   a multiple of 16     h  16-bit [T*k, I] (write), 16-byte aligned
+ * The output flag is not used.                                                 */
+moe_status moe_expert_gemm_swiglu_packed(const moe_problem* p, const moe_packed_format* f,
+                                         int32_t K, int32_t I, const void* a, const int32_t* src,
+                                         const void* w, const int32_t* counts,
+                                         const int32_t* expert_offsets, void* h, void* stream);
+
+/* Bytes of device workspace that moe_layer_few_tokens_packed needs. Host only.  */
+moe_status moe_layer_packed_workspace_bytes(const moe_problem* p, int32_t I, size_t* bytes);
+
+/* moe_layer_few_tokens with packed weights: the same routing, formulas, limits and
+ * outputs, w_up E packed matrices [2I, H] and w_down E packed [H, I] (16-byte aligned),
+ * products and sums as in moe_expert_gemm_packed.
+ *   ws      workspace of at least moe_layer_packed_workspace_bytes() bytes,
+ *           256-byte aligned                                                   */
+moe_status moe_layer_few_tokens_packed(const moe_problem* p, const moe_packed_format* f, int32_t I,
+                                       const float* logits, const void* x, const void* w_up,
+                                       const void* w_down, int32_t* idx, float* w, void* out,
+                                       void* ws, size_t ws_bytes, void* stream);
 
 /* ---- training the weights --------------------------------------------------- */
 

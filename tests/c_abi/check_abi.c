@@ -13,7 +13,8 @@
  *   moe_c_abi_check_layer() the layer around the routing: the norm and its
  *                           gradient, the experts' products in 8 bits, the
  *                           whole layer for a few tokens;
- *   moe_c_abi_check_weights() what trains weights.
+ *   moe_c_abi_check_weights() what trains weights, and the products and the
+ *                           layer with weights in 4 bits.
  * Each returns 0 when every check holds and prints the first failure
  * otherwise.
  */
@@ -707,6 +708,18 @@ int moe_c_abi_check_weights(void) {
   int rc = 0;
   moe_adamw step = {0.25, 0.5, 0.75, 0.0, 1, MOE_F32, MOE_F32, 32};
   moe_adamw_tensor t;
+  enum { T = 3, H = 16, I = 16, N = 24 };
+  enum { P_X, P_W, P_LOGITS, P_CNT, P_OFF, P_IDX, P_GATE, P_Y, P_H, P_OUT, P_COUNT };
+  const size_t psz[P_COUNT] = {2u * T * H, 2u * 1056, 4u * T, 4, 4, 4u * T, 4u * T, 2u * T * N, 2u * T * I, 2u * T * H};
+  void *pd[P_COUNT] = {NULL}, *ws = NULL;
+  uint16_t x[T * H], y[T * N], hh[T * I], out[T * H];
+  uint8_t w[2 * 1056];
+  float logits[T] = {0.5f, 0.0f, -1.0f};
+  int32_t counts = T, offsets = 0;
+  size_t bytes = 0, ws_bytes = 0;
+  uint32_t seed = 99u;
+  moe_packed_format f = {MOE_PACKED_INT, 128, MOE_BF16};
+  moe_problem p;
 
   /* 1. AdamW's first step without decay moves every weight by lr against its
      gradient's sign: m / c1 = g, sqrt(v / c2) = |g| */
@@ -728,9 +741,52 @@ int moe_c_abi_check_weights(void) {
     if (h[W_M][i] != 0.5 * g || fabs(h[W_V][i] - 0.25 * g * g) > 1e-6 * g * g) FAIL("AdamW states of %d", i);
   }
   if (moe_adamw_step(&step, &t, -1, NULL, NULL) != MOE_ERR_INVALID_ARG) FAIL("n = -1 was not refused");
+  /* 2. packed weights that are all 1 (code 9, scale 1): every column of a product is
+     the sum of the row's values, and the layer's output I z sigmoid(z) z of it */
+  p.T = T; p.E = 1; p.k = 1; p.H = H; p.R = 1; p.act_dtype = MOE_BF16; p.flags = 0;
+  MOE_OK_OR_FAIL(moe_packed_weight_bytes(&f, 1, 2 * I, H, &bytes));
+  if (bytes != sizeof(w)) FAIL("packed bytes %zu", bytes);
+  memset(w, 0x99, sizeof(w));
+  for (int tile = 0; tile < 2; ++tile)
+    for (int r = 0; r < 16; ++r) {
+      const uint16_t one = bf16_bits(8);
+      memcpy(w + tile * 1056 + 1024 + 2 * r, &one, 2);
+    }
+  for (int i = 0; i < T * H; ++i) x[i] = bf16_bits((int)(lcg(&seed) >> 28) - 7);
+  for (int i = 0; i < P_COUNT; ++i) HIP_OK(hipMalloc(&pd[i], psz[i]));
+  HIP_OK(hipMemcpy(pd[P_X], x, sizeof(x), hipMemcpyHostToDevice));
+  HIP_OK(hipMemcpy(pd[P_W], w, sizeof(w), hipMemcpyHostToDevice));
+  HIP_OK(hipMemcpy(pd[P_LOGITS], logits, sizeof(logits), hipMemcpyHostToDevice));
+  HIP_OK(hipMemcpy(pd[P_CNT], &counts, 4, hipMemcpyHostToDevice));
+  HIP_OK(hipMemcpy(pd[P_OFF], &offsets, 4, hipMemcpyHostToDevice));
+  MOE_OK_OR_FAIL(moe_layer_packed_workspace_bytes(&p, I, &ws_bytes));
+  HIP_OK(hipMalloc(&ws, ws_bytes));
+  MOE_OK_OR_FAIL(moe_expert_gemm_packed(&p, &f, H, N, pd[P_X], NULL, pd[P_W], (const int32_t*)pd[P_CNT],
+                                        (const int32_t*)pd[P_OFF], pd[P_Y], NULL));
+  MOE_OK_OR_FAIL(moe_expert_gemm_swiglu_packed(&p, &f, H, I, pd[P_X], NULL, pd[P_W], (const int32_t*)pd[P_CNT],
+                                               (const int32_t*)pd[P_OFF], pd[P_H], NULL));
+  MOE_OK_OR_FAIL(moe_layer_few_tokens_packed(&p, &f, I, (const float*)pd[P_LOGITS], pd[P_X], pd[P_W], pd[P_W],
+                                             (int32_t*)pd[P_IDX], (float*)pd[P_GATE], pd[P_OUT], ws, ws_bytes, NULL));
+  HIP_OK(hipDeviceSynchronize());
+  HIP_OK(hipMemcpy(y, pd[P_Y], sizeof(y), hipMemcpyDeviceToHost));
+  HIP_OK(hipMemcpy(hh, pd[P_H], sizeof(hh), hipMemcpyDeviceToHost));
+  HIP_OK(hipMemcpy(out, pd[P_OUT], sizeof(out), hipMemcpyDeviceToHost));
+  for (int r = 0; r < T; ++r) {
+    double z = 0.0, v;
+    for (int c = 0; c < H; ++c) z += bf16_val(x[r * H + c]);
+    v = z / (1.0 + exp(-z)) * z;
+    for (int c = 0; c < N; ++c)
+      if (fabs(bf16_val(y[r * N + c]) - z) > fabs(z) / 256) FAIL("packed product %d, %d: %g", r, c, z);
+    for (int c = 0; c < I; ++c)
+      if (fabs(bf16_val(hh[r * I + c]) - v) > fabs(v) / 255 + 1e-6) FAIL("packed SwiGLU %d, %d: %g", r, c, v);
+    for (int c = 0; c < H; ++c)
+      if (fabs(bf16_val(out[r * H + c]) - I * v) > I * fabs(v) / 127 + 1e-5) FAIL("packed layer %d, %d: %g", r, c, I * v);
+  }
   printf("c-abi check (weights) ok\n");
 
 done:
   for (int i = 0; i < W_COUNT; ++i) hipFree(d[i]);
+  for (int i = 0; i < P_COUNT; ++i) hipFree(pd[i]);
+  hipFree(ws);
   return rc;
 }
