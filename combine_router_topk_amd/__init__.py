@@ -13,6 +13,7 @@ libmoe_route.so and fails if it has not been built.
 from .binding import (MOE_BF16, MOE_F16, MOE_FLAG_EXACT_SUMS, MOE_FLAG_GREEDY_ID_ORDER,  # noqa: F401
                       MOE_FLAG_OUT_F32, MOE_PACKED_E2M1, MOE_PACKED_INT, PackedFormat,
                       make_packed_format, moe_expert_gemm_packed, moe_expert_gemm_swiglu_packed,
+                      moe_expert_weight_grad, moe_expert_weight_grad_workspace_bytes,
                       moe_layer_few_tokens_packed, moe_layer_packed_workspace_bytes,
                       moe_packed_weight_bytes,
                       AdamW, AdamWTensors, MoeError, Problem, make_adamw, make_problem,

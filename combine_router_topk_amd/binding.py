@@ -42,7 +42,7 @@ EXPORTED = ("moe_version", "moe_build_id", "moe_status_string", "moe_last_error"
            "moe_expert_gemm", "moe_expert_gemm_swiglu", "moe_layer_workspace_bytes",
            "moe_layer_few_tokens", "moe_packed_weight_bytes", "moe_expert_gemm_packed",
            "moe_expert_gemm_swiglu_packed", "moe_layer_packed_workspace_bytes", "moe_layer_few_tokens_packed",
-           "moe_adamw_step")
+           "moe_expert_weight_grad_workspace_bytes", "moe_expert_weight_grad", "moe_adamw_step")
 
 MOE_PACKED_INT, MOE_PACKED_E2M1 = 1, 2
 
@@ -131,6 +131,8 @@ def _load() -> ctypes.CDLL:
         "moe_expert_gemm_swiglu_packed": (i32, [P, F, i32, i32, vp, vp, vp, vp, vp, vp, vp]),
         "moe_layer_packed_workspace_bytes": (i32, [P, i32, ctypes.POINTER(sz)]),
         "moe_layer_few_tokens_packed": (i32, [P, F, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "moe_expert_weight_grad_workspace_bytes": (i32, [P, i32, i32, ctypes.POINTER(sz)]),
+        "moe_expert_weight_grad": (i32, [P, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]),
         "moe_adamw_step": (i32, [ctypes.POINTER(AdamW), ctypes.POINTER(_AdamWTensor), i32, vp, vp]),
     }
     for name, (res, args) in sig.items():
@@ -598,6 +600,26 @@ def moe_layer_few_tokens_packed(p: Problem, f: PackedFormat, I: int, logits, x, 
            a(w_up, torch.uint8, _packed_bytes(f, E, 2 * I, H), "w_up"),
            a(w_down, torch.uint8, _packed_bytes(f, E, H, I), "w_down"), a(idx, torch.int32, n, "idx"),
            a(w, torch.float32, n, "w"), a(out, out_dt, T * H, "out"), a(ws, None, None, "ws"), _nbytes(ws))
+
+
+def moe_expert_weight_grad_workspace_bytes(p: Problem, K: int, N: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.moe_expert_weight_grad_workspace_bytes(ctypes.byref(p), K, N, ctypes.byref(n)),
+           "moe_expert_weight_grad_workspace_bytes")
+    return n.value
+
+
+def moe_expert_weight_grad(p: Problem, K: int, N: int, a, src, dy, counts, expert_offsets, add: bool, dw, ws,
+                           stream=None) -> None:
+    """src None: a holds the T k rows in send order; given: the T token rows. add: the
+    sum goes on top of dw."""
+    act, n, arg = _TORCH_ACT.get(p.act_dtype), p.T * p.k, _Args("moe_expert_weight_grad")
+    out_dt = torch.float32 if p.flags & MOE_FLAG_OUT_F32 else act
+    arg.call(_lib.moe_expert_weight_grad, stream, ctypes.byref(p), K, N,
+             arg(a, act, (n if src is None else p.T) * K, "a"), arg(src, torch.int32, n, "src"),
+             arg(dy, act, n * N, "dy"), arg(counts, torch.int32, p.E, "counts"),
+             arg(expert_offsets, torch.int32, p.E, "expert_offsets"), 1 if add else 0,
+             arg(dw, out_dt, p.E * N * K, "dw"), arg(ws, None, None, "ws"), _nbytes(ws))
 
 
 def make_adamw(lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, step: int = 1) -> AdamW:

@@ -210,6 +210,15 @@ moe_status check_packed_gemm(const moe_problem* p, int32_t K, int64_t n, const v
   return need(expert_offsets, 4, fn, "expert_offsets");
 }
 
+moe_status check_weight_grad(const moe_problem* p, int32_t K, int32_t N, const char* fn) {
+  CHECK(check_problem(p, fn));
+  if (K <= 0 || K % 8 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: K=%d is not a positive multiple of 8", fn, K);
+  if (N <= 0 || N % 8 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: N=%d is not a positive multiple of 8", fn, N);
+  if (!moe::weight_grad_fits(p->E, K, N))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: %d matrices of %d x %d have too many tiles", fn, p->E, N, K);
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -788,6 +797,38 @@ moe_status moe_layer_few_tokens_packed(const moe_problem* p, const moe_packed_fo
   return hip_status(moe::launch_layer_few_tokens_packed(fmt, logits, x, w_up, w_down, p->T, p->E, p->k, p->H, I, idx, w,
                                                         out, ws, p->act_dtype, (p->flags & MOE_FLAG_OUT_F32) != 0,
                                                         static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+moe_status moe_expert_weight_grad_workspace_bytes(const moe_problem* p, int32_t K, int32_t N, size_t* bytes) {
+  const char* fn = "moe_expert_weight_grad_workspace_bytes";
+  CHECK(check_weight_grad(p, K, N, fn));
+  if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is NULL", fn);
+  *bytes = moe::weight_grad_ws_bytes(p->T, p->E, p->k, K, N);
+  return MOE_OK;
+}
+
+moe_status moe_expert_weight_grad(const moe_problem* p, int32_t K, int32_t N, const void* a, const int32_t* src,
+                                  const void* dy, const int32_t* counts, const int32_t* expert_offsets, int32_t add,
+                                  void* dw, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_expert_weight_grad";
+  CHECK(check_weight_grad(p, K, N, fn));
+  const bool out_f32 = (p->flags & MOE_FLAG_OUT_F32) != 0;
+  if (add != 0 && !out_f32) return fail(MOE_ERR_UNSUPPORTED, "%s: sums are added to fp32 only", fn);
+  CHECK(need(dw, 16, fn, "dw"));
+  CHECK(need(counts, 4, fn, "counts"));
+  CHECK(need(expert_offsets, 4, fn, "expert_offsets"));
+  if (p->T > 0) {
+    CHECK(need(a, 16, fn, "a"));
+    if (src != nullptr) CHECK(need(src, 4, fn, "src"));
+    CHECK(need(dy, 16, fn, "dy"));
+  }
+  const size_t req = moe::weight_grad_ws_bytes(p->T, p->E, p->k, K, N);
+  if (req > 0) CHECK(need(ws, 256, fn, "ws"));
+  if (ws_bytes < req) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, req);
+  clear_stale_error();
+  return hip_status(moe::launch_weight_grad(a, src, dy, counts, expert_offsets, p->T, p->E, p->k, K, N, add != 0, dw, ws,
+                                            p->act_dtype, out_f32, static_cast<hipStream_t>(stream)),
                     fn);
 }
 

@@ -190,6 +190,13 @@ hipError_t launch_layer_few_tokens_packed(const PackedFormat& f, const float* lo
                                           const void* w_down, int T, int E, int k, int H, int I, int32_t* idx, float* w,
                                           void* out, void* ws, int act, bool out_f32, hipStream_t s);
 
+// Whether a launch holds the tiles of weights of these sizes.
+bool weight_grad_fits(int E, int K, int N);
+size_t weight_grad_ws_bytes(int T, int E, int k, int K, int N);
+hipError_t launch_weight_grad(const void* a, const int32_t* src, const void* dy, const int32_t* counts,
+                              const int32_t* offsets, int T, int E, int k, int K, int N, bool add, void* dw, void* ws,
+                              int act, bool out_f32, hipStream_t s);
+
 struct AdamWStep {
   double lr, beta1, beta2, eps;
   int step;

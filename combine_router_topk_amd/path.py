@@ -426,3 +426,29 @@ def layer_few_tokens_packed(b: Buffers, w: PackedExperts, ws: torch.Tensor, stre
 
 def layer_packed_workspace(b: Buffers, I: int) -> torch.Tensor:
     return torch.empty(B.moe_layer_packed_workspace_bytes(b.p, I), dtype=torch.uint8, device=b.idx.device)
+
+
+@dataclass
+class WeightGrad:
+    """The gradient of one of the experts' weights, dw [E, N, K] in fp32, and its
+    workspace."""
+    p: B.Problem
+    N: int
+    K: int
+    dw: torch.Tensor
+    ws: torch.Tensor
+
+
+def allocate_weight_grad(b: Buffers, N: int, K: int) -> WeightGrad:
+    E = b.p.E
+    p = B.make_problem(b.p.T, E, b.p.k, b.p.H, b.p.R, b.p.act_dtype, b.p.flags | B.MOE_FLAG_OUT_F32)
+    dev = b.idx.device
+    return WeightGrad(p=p, N=N, K=K, dw=torch.empty(E, N, K, dtype=torch.float32, device=dev),
+                      ws=torch.empty(B.moe_expert_weight_grad_workspace_bytes(p, K, N), dtype=torch.uint8, device=dev))
+
+
+def expert_weight_grad(b: Buffers, g: WeightGrad, a: torch.Tensor, src: torch.Tensor | None, dy: torch.Tensor,
+                       add: bool = False, stream=None) -> None:
+    """g.dw from the products' 16-bit inputs a (send rows, or with src = b.src the
+    token rows) and the gradient dy of their outputs; on top of g.dw with add."""
+    B.moe_expert_weight_grad(g.p, g.K, g.N, a, src, dy, b.counts, b.expert_offsets, add, g.dw, g.ws, stream)

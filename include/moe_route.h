@@ -9,7 +9,8 @@
  * routing as the greedy's baseline; and the layer around the routing: the
  * norm that makes its rows with its gradient, the experts' products in
  * block-scaled 8-bit floating point, and the whole layer for a few tokens, both
- * with weights in 4 bits, too; and the step that trains weights.
+ * with weights in 4 bits, too; and what trains weights: the gradient of the
+ * experts' and the step.
  *
  * Sources (web pages on MoE dispatch and combine):
  *   [METRO]  "METRO AllGather vs AllToAll for MoE decode".
@@ -655,6 +656,37 @@ moe_status moe_layer_few_tokens_packed(const moe_problem* p, const moe_packed_fo
                                        void* ws, size_t ws_bytes, void* stream);
 
 /* ---- training the weights --------------------------------------------------- */
+
+/* Bytes of device workspace that moe_expert_weight_grad needs (0 for most problems).
+ * Host only.                                                                  */
+moe_status moe_expert_weight_grad_workspace_bytes(const moe_problem* p, int32_t K, int32_t N,
+                                                  size_t* bytes);
+
+/* Gradient of the experts' weights in the products y[r] = W_e a[r'] (what
+ * moe_expert_gemm computes, from 16-bit rows here):
+ *   dw[e, n, k] = sum over rows r of e's segment of dy[r, n] * a[r', k]
+ * exact products of 16-bit values summed in fp32, written as fp32 with
+ * MOE_FLAG_OUT_F32, else rounded once to the activation format. The order of the sum
+ * depends on the sizes and counts alone, so results repeat bit for bit. An expert
+ * without rows gets zeros.
+ *   K, N  multiples of 8; E ceil(N/256) ceil(K/256) is below 2^22
+ *         (MOE_ERR_UNSUPPORTED)
+ *   a     16-bit [rows, K] (read): T k rows in send order, or with src T token rows
+ *   src             i32 [T*k] (read) from moe_layout, or NULL
+ *   dy    16-bit [T*k, N] (read) in send order, as moe_combine_backward writes it
+ *   counts          i32 [E] (read) from moe_route
+ *   expert_offsets  i32 [E] (read) from moe_layout
+ *   add   not 0: the sum is added to the fp32 dw that is there, in one more rounding
+ *         (over micro-batches; without MOE_FLAG_OUT_F32 MOE_ERR_UNSUPPORTED)
+ *   dw    [E, N, K] in the activation format or fp32 (write, with add read, too)
+ *   ws    workspace of at least moe_expert_weight_grad_workspace_bytes() bytes, 256-byte
+ *         aligned (may be NULL for 0 bytes)
+ * a, dy and dw are 16-byte aligned. A src outside [0, T*k) is clamped into it, and
+ * segments are cut to the T k rows. H of the problem is not used.               */
+moe_status moe_expert_weight_grad(const moe_problem* p, int32_t K, int32_t N, const void* a,
+                                  const int32_t* src, const void* dy, const int32_t* counts,
+                                  const int32_t* expert_offsets, int32_t add, void* dw, void* ws,
+                                  size_t ws_bytes, void* stream);
 
 /* One AdamW step.
  *   lr, beta1, beta2, eps  finite, eps >= 0, 0 <= beta < 1; in 64 bits, as 1 -

@@ -711,7 +711,8 @@ int moe_c_abi_check_weights(void) {
   enum { T = 3, H = 16, I = 16, N = 24 };
   enum { P_X, P_W, P_LOGITS, P_CNT, P_OFF, P_IDX, P_GATE, P_Y, P_H, P_OUT, P_COUNT };
   const size_t psz[P_COUNT] = {2u * T * H, 2u * 1056, 4u * T, 4, 4, 4u * T, 4u * T, 2u * T * N, 2u * T * I, 2u * T * H};
-  void *pd[P_COUNT] = {NULL}, *ws = NULL;
+  void *pd[P_COUNT] = {NULL}, *ws = NULL, *dw = NULL;
+  float hdw[H * H];
   uint16_t x[T * H], y[T * N], hh[T * I], out[T * H];
   uint8_t w[2 * 1056];
   float logits[T] = {0.5f, 0.0f, -1.0f};
@@ -782,9 +783,26 @@ int moe_c_abi_check_weights(void) {
     for (int c = 0; c < H; ++c)
       if (fabs(bf16_val(out[r * H + c]) - I * v) > I * fabs(v) / 127 + 1e-5) FAIL("packed layer %d, %d: %g", r, c, I * v);
   }
+  /* 3. the weights' gradient of the three rows against themselves is symmetric with the
+     columns' sums of squares on the diagonal */
+  MOE_OK_OR_FAIL(moe_expert_weight_grad_workspace_bytes(&p, H, H, &bytes));
+  if (bytes != 0) FAIL("workspace of the weights' gradient: %zu", bytes);
+  p.flags = MOE_FLAG_OUT_F32;
+  HIP_OK(hipMalloc(&dw, sizeof(hdw)));
+  MOE_OK_OR_FAIL(moe_expert_weight_grad(&p, H, H, pd[P_X], NULL, pd[P_X], (const int32_t*)pd[P_CNT],
+                                        (const int32_t*)pd[P_OFF], 0, dw, NULL, 0, NULL));
+  HIP_OK(hipDeviceSynchronize());
+  HIP_OK(hipMemcpy(hdw, dw, sizeof(hdw), hipMemcpyDeviceToHost));
+  for (int i = 0; i < H; ++i)
+    for (int c = 0; c < H; ++c) {
+      double want = 0.0;
+      for (int r = 0; r < T; ++r) want += bf16_val(x[r * H + i]) * bf16_val(x[r * H + c]);
+      if (hdw[i * H + c] != want) FAIL("weight gradient %d, %d: %g against %g", i, c, hdw[i * H + c], want);
+    }
   printf("c-abi check (weights) ok\n");
 
 done:
+  hipFree(dw);
   for (int i = 0; i < W_COUNT; ++i) hipFree(d[i]);
   for (int i = 0; i < P_COUNT; ++i) hipFree(pd[i]);
   hipFree(ws);

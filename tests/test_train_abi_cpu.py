@@ -79,3 +79,43 @@ def test_adamw_tensors_are_checked_by_the_binding():
     with pytest.raises(KeyError):
         B.AdamWTensors([dict(w=torch.zeros(4), g=torch.zeros(4))])
     B.moe_adamw_step(B.make_adamw(1e-3), B.AdamWTensors([]))  # no tensors: nothing happens
+
+
+# ---- the weights' gradient --------------------------------------------------------
+
+FAKE, OFF8 = ctypes.c_void_p(BASE), ctypes.c_void_p(BASE + 8)
+
+
+def prob(**kw):
+    d = dict(T=32, E=8, k=2, H=128, R=1, act_dtype=B.MOE_BF16, flags=0)
+    d.update(kw)
+    return ctypes.byref(B.make_problem(d["T"], d["E"], d["k"], d["H"], d["R"], d["act_dtype"], d["flags"]))
+
+
+def grad(p=None, K=128, N=128, a=FAKE, src=None, dy=FAKE, counts=FAKE, off=FAKE, add=0, dw=FAKE, ws=None, n=0):
+    return lib.moe_expert_weight_grad(p or prob(), K, N, a, src, dy, counts, off, add, dw, ws, n, None)
+
+
+@pytest.mark.parametrize("kw,text", [
+    (dict(K=0), "K=0"), (dict(K=12), "K=12"), (dict(N=0), "N=0"), (dict(N=-8), "N=-8"), (dict(N=20), "N=20"),
+    (dict(a=None), "a is NULL"), (dict(a=OFF8), "a is not 16-byte"), (dict(dy=None), "dy is NULL"),
+    (dict(dy=OFF8), "dy is not 16-byte"), (dict(dw=None), "dw is NULL"), (dict(dw=OFF8), "dw is not 16-byte"),
+    (dict(counts=None), "counts is NULL"), (dict(off=None), "expert_offsets is NULL"),
+    (dict(src=ctypes.c_void_p(BASE + 1)), "src is not 4-byte")])
+def test_weight_grad_refusals(kw, text):
+    refused(grad(**kw), B.MOE_ERR_INVALID_ARG, text)
+
+
+def test_weight_grad_limits():
+    refused(grad(add=1), B.MOE_ERR_UNSUPPORTED, "fp32 only")
+    refused(grad(prob(E=1024), K=16392, N=16384), B.MOE_ERR_UNSUPPORTED, "too many tiles")
+    n = ctypes.c_size_t(7)
+    size = lambda p, K=128, N=128: lib.moe_expert_weight_grad_workspace_bytes(p, K, N, ctypes.byref(n))  # noqa: E731
+    assert size(prob(E=64, T=16384), 4096, 4096) == B.MOE_OK and n.value == 0
+    few = prob(T=16384, E=2)
+    assert size(few) == B.MOE_OK and n.value > 0 and n.value % (2 * 128 * 128 * 4) == 0
+    refused(grad(few), B.MOE_ERR_INVALID_ARG, "ws is NULL")
+    refused(grad(few, ws=FAKE, n=n.value - 1), B.MOE_ERR_WORKSPACE, "workspace")
+    refused(grad(few, ws=OFF8, n=n.value), B.MOE_ERR_INVALID_ARG, "ws is not 256-byte")
+    refused(lib.moe_expert_weight_grad_workspace_bytes(prob(), 128, 128, None), B.MOE_ERR_INVALID_ARG, "bytes is NULL")
+    refused(size(prob(), 12), B.MOE_ERR_INVALID_ARG, "K=12")
