@@ -669,7 +669,7 @@ moe_status moe_expert_weight_grad_workspace_bytes(const moe_problem* p, int32_t 
  * MOE_FLAG_OUT_F32, else rounded once to the activation format. The order of the sum
  * depends on the sizes and counts alone, so results repeat bit for bit. An expert
  * without rows gets zeros.
- *   K, N  multiples of 8; E ceil(N/256) ceil(K/256) is below 2^22
+ *   K, N  multiples of 8; E ceil(N/128) ceil(K/256) is below 2^23
  *         (MOE_ERR_UNSUPPORTED)
  *   a     16-bit [rows, K] (read): T k rows in send order, or with src T token rows
  *   src             i32 [T*k] (read) from moe_layout, or NULL
