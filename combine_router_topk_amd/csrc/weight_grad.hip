@@ -48,6 +48,8 @@ struct Shared {
 };
 constexpr uint32_t kStageBytes = kStep * (kChunksN + kChunksK) * 16, kABytes = kStep * kChunksN * 16;
 
+constexpr int kWaveBytes = kStages * kStageBytes / kWaves;  // for a wave's results
+
 // What is loaded in place of rows past the segment's end and columns past the matrix's.
 __device__ const uint4 zeros = {0, 0, 0, 0};
 
@@ -206,32 +208,60 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
     ahead = ahead == 2 * kStageBytes ? 0 : ahead + kStageBytes;
   }
 
-  // a lane's four results of a fragment are four neighbouring k of one n
+  // A lane's four results of a fragment are four neighbouring k of one n, so that stores
+  // straight from there would take 16 rows' lines for 32 or 64 bytes each. The wave's
+  // results go through its part of the stages instead, and whole lines of a row are
+  // stored: without that 64 experts of 4096 x 4096 take 1650 us.
+  __syncthreads();  // all waves have read the last step
+  unsigned char* const mine = reinterpret_cast<unsigned char*>(lds) + wave * kWaveBytes;
+  const bool whole = g.splits > 1 || g.out_f32;  // fp32
+  const size_t matrix = static_cast<size_t>(e) * g.N * g.K;
+  const int k0 = tk * kTileK + wk * 128;
+  auto pass = [&](auto F32) {
+    constexpr bool f32 = F32;
+    constexpr int kFrags = f32 ? 2 : 4;  // along N at a time
+    constexpr int kLine = 128 * (f32 ? 4 : 2), kPitch = kLine + 16;
+    constexpr int kLanes = kLine / 16;  // of a row
+    static_assert(16 * kFrags * kPitch <= kWaveBytes, "");
 #pragma unroll
-  for (int j = 0; j < kFragsN; ++j) {
-    const int n = tn * kTileN + wn * 64 + j * 16 + (lane & 15);
-    if (n >= g.N) continue;
-    const size_t line = (static_cast<size_t>(e) * g.N + n) * g.K;
+    for (int j0 = 0; j0 < kFragsN; j0 += kFrags) {
 #pragma unroll
-    for (int i = 0; i < kFragsK; ++i) {
-      const int k = tk * kTileK + wk * 128 + i * 16 + grp * 4;
-      if (k >= g.K) continue;
-      float4 v = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
-      if (g.splits > 1) {
-        *reinterpret_cast<float4*>(g.part + static_cast<size_t>(split) * g.E * g.N * g.K + line + k) = v;
-      } else if (g.out_f32) {
-        float4* to = reinterpret_cast<float4*>(static_cast<float*>(g.dw) + line + k);
-        if (g.add) {
-          const float4 o = *to;
-          v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+      for (int j = 0; j < kFrags; ++j) {
+#pragma unroll
+        for (int i = 0; i < kFragsK; ++i) {
+          const v4f v = acc[i][j0 + j];
+          unsigned char* to = mine + (16 * j + (lane & 15)) * kPitch + (16 * i + 4 * grp) * (f32 ? 4 : 2);
+          if constexpr (f32) *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+          else *reinterpret_cast<uint2*>(to) = make_uint2(pack2<ACT>(v[0], v[1]), pack2<ACT>(v[2], v[3]));
         }
-        *to = v;
-      } else {
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.dw) + line + k) =
-            make_uint2(pack2<ACT>(v.x, v.y), pack2<ACT>(v.z, v.w));
       }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's lanes exchange them
+#pragma unroll
+      for (int r = 0; r < 16 * kFrags; r += kWave / kLanes) {
+        const int row = r + lane / kLanes, n = tn * kTileN + wn * 64 + 16 * j0 + row;
+        const int k = k0 + lane % kLanes * (f32 ? 4 : 8);
+        const uint4 v = *reinterpret_cast<const uint4*>(mine + row * kPitch + lane % kLanes * 16);
+        if (n >= g.N || k >= g.K) continue;
+        const size_t at = matrix + static_cast<size_t>(n) * g.K + k;
+        if constexpr (!f32) {
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.dw) + at) = v;
+        } else if (g.splits > 1) {
+          *reinterpret_cast<uint4*>(g.part + static_cast<size_t>(split) * g.E * g.N * g.K + at) = v;
+        } else {
+          float4 f = __builtin_bit_cast(float4, v);
+          float4* to = reinterpret_cast<float4*>(static_cast<float*>(g.dw) + at);
+          if (g.add) {
+            const float4 o = *to;
+            f = make_float4(o.x + f.x, o.y + f.y, o.z + f.z, o.w + f.w);
+          }
+          *to = f;
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
-  }
+  };
+  if (whole) pass(std::true_type{});
+  else pass(std::false_type{});
 }
 
 // The splits' sums, in their order.
