@@ -7,6 +7,8 @@
 // memory. Rows go to LDS as they are, and the LDS reads transpose: four lanes read
 // 16 neighbouring values of one row, and each lane of 16 gets four rows of one
 // column.
+#include <limits.h>
+
 #include "device.hpp"
 #include "launch.hpp"
 #include "quant.hpp"
@@ -33,11 +35,16 @@ struct GradArgs {
   const int32_t* src;
   const int32_t* counts;
   const int32_t* offsets;
-  int rows, a_rows, E, K, N, n_tiles, k_tiles, splits;
+  int rows, a_rows, E, K, N, n_tiles, k_tiles;
   uint32_t inverse;  // 2^32 / k, rounded up: i / k is the product's high half (i < 2^24, k <= 16); 0 for k = 1
   bool out_f32, add;
   void* dw;
-  float* part;  // [splits][E][N][K] with more than one
+  // With a plan (see below), else null:
+  int most;     // parts more than experts
+  int* found;   // units, and experts that are cut
+  int4* unit;   // expert, first step, end, place of its sums or -1
+  int4* cut;    // expert, first place, places
+  float* part;  // [place][N][K]: sums of a part of an expert's rows
 };
 
 // A step: 32 rows of dy's 128 columns and of a's 256, 16-byte chunk c of row r at place
@@ -93,16 +100,16 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
   Shared& sh = *reinterpret_cast<Shared*>(lds);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tiles = g.n_tiles * g.k_tiles;
-  const int e = blockIdx.x / tiles, in = blockIdx.x % tiles;
+  const int u = blockIdx.x / tiles, in = blockIdx.x % tiles;
+  if (g.unit != nullptr && u >= g.found[0]) return;
+  const int4 unit = g.unit != nullptr ? g.unit[u] : make_int4(u, 0, INT_MAX, -1);
+  const int e = unit.x, slot = unit.w;
   int tn, tk;
   tile_of(g, in, tn, tk);
 
-  // this block's share of the expert's rows, whole steps but for the last one
   const int at = min(max(g.offsets[e], 0), g.rows), have = min(max(g.counts[e], 0), g.rows - at);
-  const int all_steps = (have + kStep - 1) / kStep, split = blockIdx.y;
-  const int s0 = static_cast<int>(static_cast<long long>(all_steps) * split / g.splits);
-  const int s1 = static_cast<int>(static_cast<long long>(all_steps) * (split + 1) / g.splits);
-  if (g.add && g.splits == 1 && s0 == s1) return;
+  const int s0 = unit.y, s1 = min(unit.z, (have + kStep - 1) / kStep);
+  if (g.add && slot < 0 && s0 >= s1) return;
 
   // What this lane loads: chunk of dy's rows 4 q + lane / 16 and of a's 2 q + lane / 32, q
   // the wave's first load of a step and each fourth from there.
@@ -115,11 +122,13 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
     dy[i] = g.dy + (static_cast<size_t>(at) + s0 * kStep + dy_row[i]) * g.N + col;
     if (col >= g.N) dy_row[i] = 1 << 30;
   }
-  int a_col[kALoads];
+  const unsigned char* a0[kALoads];
+  uint32_t a_stride[kALoads];
 #pragma unroll
   for (int i = 0; i < kALoads; ++i) {
     const int col = tk * kTileK + ((lane & 31) ^ ((2 * (wave + kWaves * i) + (lane >> 5)) & 15)) * 8;
-    a_col[i] = col < g.K ? col : -1;
+    a0[i] = reinterpret_cast<const unsigned char*>(col < g.K ? static_cast<const void*>(g.a + col) : &zeros);
+    a_stride[i] = col < g.K ? static_cast<uint32_t>(g.K) * 2 : 0;
   }
   // the sources of rows from step s on, -1 past the end
   auto fill = [&](int s) {
@@ -138,21 +147,22 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
     __syncthreads();
   };
   const uint32_t lds0 = lds_address(&sh.stage[0][0]) + wave * 1024;
-  auto load = [&](int s, uint32_t stage) {
-#pragma unroll
-    for (int i = 0; i < kDyLoads; ++i) {
-      const void* from = s * kStep + dy_row[i] < have ? static_cast<const void*>(dy[i]) : &zeros;
-      load_lds(from, lds0 + stage + i * (kWaves * 1024));
-      dy[i] += static_cast<size_t>(kStep) * g.N;
-    }
+  auto load_dy = [&](int i, int s, uint32_t stage) {
+    const uint64_t zero = reinterpret_cast<uint64_t>(&zeros), from = reinterpret_cast<uint64_t>(dy[i]);
+    load_lds(reinterpret_cast<const void*>(s * kStep + dy_row[i] < have ? from : zero), lds0 + stage + i * (kWaves * 1024));
+    dy[i] += static_cast<size_t>(kStep) * g.N;
+  };
+  int source[kALoads];  // of the rows of the next step that is loaded
+  auto read_sources = [&](int s) {
     const int window = (s - s0) * kStep % kWindow;
 #pragma unroll
-    for (int i = 0; i < kALoads; ++i) {
-      const int from = sh.source[window + 2 * (wave + kWaves * i) + (lane >> 5)];
-      const void* p = from >= 0 && a_col[i] >= 0
-                          ? static_cast<const void*>(g.a + static_cast<size_t>(from) * g.K + a_col[i]) : &zeros;
-      load_lds(p, lds0 + stage + kABytes + i * (kWaves * 1024));
-    }
+    for (int i = 0; i < kALoads; ++i) source[i] = sh.source[window + 2 * (wave + kWaves * i) + (lane >> 5)];
+  };
+  auto load_a = [&](int i, uint32_t stage) {
+    const uint64_t zero = reinterpret_cast<uint64_t>(&zeros);
+    const uint64_t from = reinterpret_cast<uint64_t>(a0[i]) +
+                          static_cast<uint64_t>(static_cast<uint32_t>(source[i])) * a_stride[i];
+    load_lds(reinterpret_cast<const void*>(source[i] >= 0 ? from : zero), lds0 + stage + kABytes + i * (kWaves * 1024));
   };
 
   // where this lane reads: row 4 (lane / 16) + (lane / 4) % 4 and 16 rows further, piece
@@ -173,20 +183,26 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
 #pragma unroll
     for (int j = 0; j < kFragsN; ++j) acc[i][j] = v4f{0, 0, 0, 0};
 
-  // Two steps' loads are in flight while a third is multiplied.
+  // Two steps' loads are in flight while a third is multiplied. A step's are issued
+  // between the products, their rows' sources read from LDS a step before that: all at
+  // the step's beginning they kept the products waiting for 800 of its 1600 cycles.
   uint32_t now = 0, ahead = 2 * kStageBytes;
   if (s0 < s1) {
     fill(s0);
-    load(s0, 0);
-    if (s0 + 1 < s1) load(s0 + 1, kStageBytes);
+    for (int s = s0; s < min(s0 + 2, s1); ++s) {
+      read_sources(s);
+#pragma unroll
+      for (int i = 0; i < kDyLoads; ++i) load_dy(i, s, (s - s0) * kStageBytes);
+#pragma unroll
+      for (int i = 0; i < kALoads; ++i) load_a(i, (s - s0) * kStageBytes);
+    }
+    read_sources(s0 + 2);
   }
   for (int s = s0; s < s1; ++s) {
     if (s + 1 < s1) wait_loads<kDyLoads + kALoads>();
     else wait_loads<0>();
-    if (s + 2 < s1) {
-      if ((s + 2 - s0) % (kWindow / kStep) == 0) fill(s + 2);
-      load(s + 2, ahead);
-    }
+    if ((s + 3 - s0) % (kWindow / kStep) == 0 && s + 3 < s1) fill(s + 3);
+    const bool more = s + 2 < s1;
     uint4 n[kFragsN], k[2];
     auto read = [&](uint32_t from, uint32_t half) {
       const uint2 lo = read_transposed(from + now), hi = read_transposed(from + now + half);
@@ -203,6 +219,11 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
 #pragma unroll
       for (int j = 0; j < kFragsN; ++j) acc[i][j] = mfma16<ACT>(k[i & 1], n[j], acc[i][j]);
       __builtin_amdgcn_sched_barrier(0);
+      if (more) {
+        if (i < kDyLoads) load_dy(i, s + 2, ahead);
+        else if (i < kDyLoads + kALoads) load_a(i - kDyLoads, ahead);
+        else if (i == kDyLoads + kALoads) read_sources(s + 3);
+      }
     }
     now = now == 2 * kStageBytes ? 0 : now + kStageBytes;
     ahead = ahead == 2 * kStageBytes ? 0 : ahead + kStageBytes;
@@ -214,7 +235,7 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
   // stored: without that 64 experts of 4096 x 4096 take 1650 us.
   __syncthreads();  // all waves have read the last step
   unsigned char* const mine = reinterpret_cast<unsigned char*>(lds) + wave * kWaveBytes;
-  const bool whole = g.splits > 1 || g.out_f32;  // fp32
+  const bool whole = slot >= 0 || g.out_f32;  // fp32
   const size_t matrix = static_cast<size_t>(e) * g.N * g.K;
   const int k0 = tk * kTileK + wk * 128;
   auto pass = [&](auto F32) {
@@ -245,8 +266,8 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
         const size_t at = matrix + static_cast<size_t>(n) * g.K + k;
         if constexpr (!f32) {
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.dw) + at) = v;
-        } else if (g.splits > 1) {
-          *reinterpret_cast<uint4*>(g.part + static_cast<size_t>(split) * g.E * g.N * g.K + at) = v;
+        } else if (slot >= 0) {
+          *reinterpret_cast<uint4*>(g.part + static_cast<size_t>(slot) * g.N * g.K + at - matrix) = v;
         } else {
           float4 f = __builtin_bit_cast(float4, v);
           float4* to = reinterpret_cast<float4*>(static_cast<float*>(g.dw) + at);
@@ -254,7 +275,8 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
             const float4 o = *to;
             f = make_float4(o.x + f.x, o.y + f.y, o.z + f.z, o.w + f.w);
           }
-          *to = f;
+          // 131 MB in odd rows 60 us with ordinary stores, 49 (rows in 16 bits: 1547 for 1434)
+          __builtin_nontemporal_store(__builtin_bit_cast(v4f, f), reinterpret_cast<v4f*>(to));
         }
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -264,65 +286,161 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
   else pass(std::false_type{});
 }
 
-// The splits' sums, in their order.
+// ---- the plan ------------------------------------------------------------------------
+//
+// Where routing is skewed one expert's rows can be more than a block's share of all the
+// work, and where an expert has few tiles there are too few blocks. Then experts with
+// more than C steps of rows are cut into parts of at most that many, the longest parts
+// are first in the grid, and a kernel adds up the parts' sums in their order. C is half
+// of what a block takes if the steps of all tiles are dealt out to kSlots blocks: all
+// steps / most, most = 2 kSlots / tiles. So parts are at most `most` more than experts,
+// whatever the counts are, and the parts of cut experts at most 2 most: their sums take
+// about 4 kSlots tiles of 128 x 256 at most, 268 MB.
+
+constexpr int kSlots = 512;      // blocks that run at once
+constexpr int kLeastSteps = 8;   // C is no less
+constexpr int kPlanThreads = 1024;
+
+__global__ __launch_bounds__(kPlanThreads) void weight_grad_plan_kernel(GradArgs g) {
+  __shared__ int sums[kPlanThreads / kWave];
+  __shared__ int2 key[kMaxE];  // steps of a part, parts
+  const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
+  int steps = 0;
+  if (e < g.E) {
+    const int at = min(max(g.offsets[e], 0), g.rows);
+    steps = (min(max(g.counts[e], 0), g.rows - at) + kStep - 1) / kStep;
+  }
+  const int upto = wave_incl_scan(steps, lane);
+  if (lane == kWave - 1) sums[wave] = upto;
+  __syncthreads();
+  long long all = 0;  // segments that overlap, which moe_layout does not write, add up to more than the rows
+  for (int w = 0; w < kPlanThreads / kWave; ++w) all += sums[w];
+  const int c = max(kLeastSteps, static_cast<int>((all + g.most - 1) / g.most));
+  const int parts = steps > c ? (steps + c - 1) / c : 1;
+  if (e < g.E) key[e] = make_int2((steps + parts - 1) / parts, parts);
+  __syncthreads();
+  if (e >= g.E) return;
+  int units = 0, places = 0, cuts = 0;  // of the experts before this one
+  for (int j = 0; j < g.E; ++j) {
+    const int2 k = key[j];
+    if (k.x > key[e].x || (k.x == key[e].x && j < e)) {
+      units += k.y;
+      if (k.y > 1) {
+        places += k.y;
+        ++cuts;
+      }
+    }
+  }
+  for (int i = 0; i < parts; ++i)
+    g.unit[units + i] = make_int4(e, static_cast<int>(static_cast<long long>(steps) * i / parts),
+                                  static_cast<int>(static_cast<long long>(steps) * (i + 1) / parts),
+                                  parts > 1 ? places + i : -1);
+  if (parts > 1) g.cut[cuts] = make_int4(e, places, parts, 0);
+  // the last expert of the order knows the sums
+  bool last = true;
+  for (int j = 0; j < g.E; ++j) last = last && !(key[j].x < key[e].x || (key[j].x == key[e].x && j > e));
+  if (last) {
+    g.found[0] = units + parts;
+    g.found[1] = cuts + (parts > 1);
+  }
+}
+
 template <int ACT>
-__global__ __launch_bounds__(256) void weight_grad_sum_kernel(GradArgs g, long long fours) {
-  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+__global__ __launch_bounds__(256) void weight_grad_sum_kernel(GradArgs g) {
+  if (static_cast<int>(blockIdx.y) >= g.found[1]) return;
+  const int4 cut = g.cut[blockIdx.y];
+  const size_t fours = static_cast<size_t>(g.N) * g.K / 4, i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= fours) return;
-  const float4* part = reinterpret_cast<const float4*>(g.part);
-  float4 v = part[i];
-  for (int s = 1; s < g.splits; ++s) {
-    const float4 p = part[s * fours + i];
+  const float4* part = reinterpret_cast<const float4*>(g.part) + cut.y * fours + i;
+  float4 v = part[0];
+  for (int s = 1; s < cut.z; ++s) {
+    const float4 p = part[s * fours];
     v = make_float4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
   }
   if (g.out_f32) {
-    float4* to = static_cast<float4*>(g.dw) + i;
+    float4* to = static_cast<float4*>(g.dw) + cut.x * fours + i;
     if (g.add) {
       const float4 o = *to;
       v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
     }
     *to = v;
   } else {
-    static_cast<uint2*>(g.dw)[i] = make_uint2(pack2<ACT>(v.x, v.y), pack2<ACT>(v.z, v.w));
+    static_cast<uint2*>(g.dw)[cut.x * fours + i] = make_uint2(pack2<ACT>(v.x, v.y), pack2<ACT>(v.z, v.w));
   }
 }
 
-long long tiles_of(int E, int K, int N) {
-  return static_cast<long long>(E) * ((N + kTileN - 1) / kTileN) * ((K + kTileK - 1) / kTileK);
-}
-int splits_of(int T, int E, int k, int K, int N) {
-  const long long blocks = tiles_of(E, K, N), steps = static_cast<long long>(T) * k / E / kStep;
-  if (blocks >= 256 || steps < 8) return 1;
-  const long long want = 512 / blocks, most = steps / 4;
-  const long long s = want < most ? want : most;
-  return static_cast<int>(s < 1 ? 1 : s > 16 ? 16 : s);
-}
+int n_tiles_of(int N) { return (N + kTileN - 1) / kTileN; }
+int k_tiles_of(int K) { return (K + kTileK - 1) / kTileK; }
+
+// The plan's sizes; `units` 0 for no plan. A token chooses an expert once, so no tile has
+// more than T rows; with k tiles >= kSlots that is no more than a block's share of the
+// work, and below a thousand tokens the plan's two launches take longer than it saves.
+struct Plan {
+  int most = 0, units = 0, places = 0, cuts = 0;
+  size_t unit_bytes = 0, cut_bytes = 0, bytes = 0;
+  Plan(int T, int E, int k, int K, int N) {
+    const long long tiles = static_cast<long long>(n_tiles_of(N)) * k_tiles_of(K);
+    if (k * tiles >= kSlots || T < 1024) return;
+    const long long steps = static_cast<long long>(T) * k / kStep + E;
+    const long long by_share = 2 * kSlots / tiles, by_least = steps / kLeastSteps;
+    most = static_cast<int>(by_share < by_least ? by_share : by_least);  // at least 2
+    units = E + most;
+    places = 2 * most;
+    cuts = E < most ? E : most;
+    unit_bytes = (units * sizeof(int4) + 255) / 256 * 256;
+    cut_bytes = (cuts * sizeof(int4) + 255) / 256 * 256;
+    bytes = 256 + unit_bytes + cut_bytes + static_cast<size_t>(places) * N * K * sizeof(float);
+  }
+};
 
 }  // namespace
 
-bool weight_grad_fits(int E, int K, int N) { return tiles_of(E, K, N) < 1ll << 23; }
-
-size_t weight_grad_ws_bytes(int T, int E, int k, int K, int N) {
-  const int splits = splits_of(T, E, k, K, N);
-  return splits > 1 ? static_cast<size_t>(splits) * E * N * K * sizeof(float) : 0;
+bool weight_grad_fits(int E, int K, int N) {
+  return static_cast<long long>(E) * n_tiles_of(N) * k_tiles_of(K) < 1ll << 23;
 }
+
+size_t weight_grad_ws_bytes(int T, int E, int k, int K, int N) { return Plan(T, E, k, K, N).bytes; }
 
 hipError_t launch_weight_grad(const void* a, const int32_t* src, const void* dy, const int32_t* counts,
                               const int32_t* offsets, int T, int E, int k, int K, int N, bool add, void* dw, void* ws,
                               int act, bool out_f32, hipStream_t s) {
-  const int splits = splits_of(T, E, k, K, N);
-  const GradArgs g{static_cast<const uint16_t*>(a), static_cast<const uint16_t*>(dy), src, counts, offsets, T * k,
-                   src != nullptr ? T : T * k, E, K, N, (N + kTileN - 1) / kTileN, (K + kTileK - 1) / kTileK, splits,
-                   k == 1 ? 0 : static_cast<uint32_t>(((1ull << 32) + k - 1) / k), out_f32, add, dw, static_cast<float*>(ws)};
-  const dim3 grid(static_cast<unsigned>(tiles_of(E, K, N)), splits);
+  const Plan plan(T, E, k, K, N);
+  GradArgs g{};
+  g.a = static_cast<const uint16_t*>(a);
+  g.dy = static_cast<const uint16_t*>(dy);
+  g.src = src;
+  g.counts = counts;
+  g.offsets = offsets;
+  g.rows = T * k;
+  g.a_rows = src != nullptr ? T : T * k;
+  g.E = E;
+  g.K = K;
+  g.N = N;
+  g.n_tiles = n_tiles_of(N);
+  g.k_tiles = k_tiles_of(K);
+  g.inverse = k == 1 ? 0 : static_cast<uint32_t>(((1ull << 32) + k - 1) / k);
+  g.out_f32 = out_f32;
+  g.add = add;
+  g.dw = dw;
+  if (plan.units > 0) {
+    char* p = static_cast<char*>(ws);
+    g.most = plan.most;
+    g.found = reinterpret_cast<int*>(p);
+    g.unit = reinterpret_cast<int4*>(p + 256);
+    g.cut = reinterpret_cast<int4*>(p + 256 + plan.unit_bytes);
+    g.part = reinterpret_cast<float*>(p + 256 + plan.unit_bytes + plan.cut_bytes);
+    weight_grad_plan_kernel<<<1, kPlanThreads, 0, s>>>(g);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  const unsigned grid = static_cast<unsigned>(plan.units > 0 ? plan.units : E) * g.n_tiles * g.k_tiles;
   if (act == 1) weight_grad_kernel<1><<<grid, kThreads, sizeof(Shared), s>>>(g);
   else weight_grad_kernel<2><<<grid, kThreads, sizeof(Shared), s>>>(g);
   const hipError_t err = hipGetLastError();
-  if (err != hipSuccess || splits == 1) return err;
-  const long long fours = static_cast<long long>(E) * N * K / 4;
-  const unsigned blocks = static_cast<unsigned>((fours + 255) / 256);
-  if (act == 1) weight_grad_sum_kernel<1><<<blocks, 256, 0, s>>>(g, fours);
-  else weight_grad_sum_kernel<2><<<blocks, 256, 0, s>>>(g, fours);
+  if (err != hipSuccess || plan.units == 0) return err;
+  const dim3 sums(static_cast<unsigned>((static_cast<size_t>(N) * K / 4 + 255) / 256), plan.cuts);
+  if (act == 1) weight_grad_sum_kernel<1><<<sums, 256, 0, s>>>(g);
+  else weight_grad_sum_kernel<2><<<sums, 256, 0, s>>>(g);
   return hipGetLastError();
 }
 

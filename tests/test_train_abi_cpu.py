@@ -113,7 +113,7 @@ def test_weight_grad_limits():
     size = lambda p, K=128, N=128: lib.moe_expert_weight_grad_workspace_bytes(p, K, N, ctypes.byref(n))  # noqa: E731
     assert size(prob(E=64, T=16384), 4096, 4096) == B.MOE_OK and n.value == 0
     few = prob(T=16384, E=2)
-    assert size(few) == B.MOE_OK and n.value > 0 and n.value % (2 * 128 * 128 * 4) == 0
+    assert size(few) == B.MOE_OK and n.value > 2 * 2 * 128 * 128 * 4 and n.value < 300 << 20
     refused(grad(few), B.MOE_ERR_INVALID_ARG, "ws is NULL")
     refused(grad(few, ws=FAKE, n=n.value - 1), B.MOE_ERR_WORKSPACE, "workspace")
     refused(grad(few, ws=OFF8, n=n.value), B.MOE_ERR_INVALID_ARG, "ws is not 256-byte")

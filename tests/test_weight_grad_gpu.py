@@ -79,6 +79,32 @@ def test_rows_in_shares():
     check_grad([50, 5000], 1, 48, 24, B.MOE_F16, False, "add")
 
 
+@pytest.mark.parametrize("out", ["16", "f32", "add"])
+def test_skewed_rows_are_cut(out):
+    """One expert with most of the rows beside experts with few and none, in order and
+    in reverse, at more tiles than one."""
+    counts = [0, 5, 3000, 40, 0, 700, 1, 350]
+    for c in (counts, counts[::-1]):
+        check_grad(c, 4, 520, 136, B.MOE_F16, True, out)
+    check_grad([9000] + [10] * 100, 2, 264, 264, B.MOE_BF16, False, out)
+
+
+def test_plans_of_overlapping_segments_stay_inside():
+    """Counts that add up to many times the rows: every expert has all of them."""
+    say("[case] weight grad, overlapping segments")
+    T, E, N, K = 4096, 64, 24, 16
+    p = B.make_problem(T, E, 1, 8, 1, B.MOE_BF16, B.MOE_FLAG_OUT_F32)
+    a, dy = torch.ones(T, K, dtype=torch.bfloat16, device="cuda"), torch.ones(T, N, dtype=torch.bfloat16, device="cuda")
+    counts, offsets = torch.full((E,), T, dtype=torch.int32, device="cuda"), torch.zeros(E, dtype=torch.int32, device="cuda")
+    need = B.moe_expert_weight_grad_workspace_bytes(p, K, N)
+    assert need > 0
+    ws = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
+    dw = torch.empty(E, N, K, device="cuda")
+    B.moe_expert_weight_grad(p, K, N, a, None, dy, counts, offsets, False, dw, ws)
+    torch.cuda.synchronize()
+    assert (dw == T).all() and (ws[need:] == 77).all()
+
+
 def test_many_experts():
     check_grad([4] * 1024, 2, 40, 16, B.MOE_BF16, True, "f32")
     check_grad([0] * 500 + [70] * 20 + [0] * 400, 2, 72, 264, B.MOE_F16, False, "16")
