@@ -48,7 +48,10 @@ struct GradArgs {
 };
 
 // A step: 32 rows of dy's 128 columns and of a's 256, 16-byte chunk c of row r at place
-// c ^ (r % 16): the 16 rows that one transposing read takes meet all banks.
+// c ^ 2 (r % 8): a transposing read takes 16 lanes at a time, 32 bytes of each of four
+// rows, and these meet different banks (with c ^ r % 16 two rows in each four met the
+// same).
+__device__ __forceinline__ int swizzle(int row) { return (row & 7) << 1; }
 struct Shared {
   uint4 stage[kStages][kStep * (kChunksN + kChunksK)];  // dy, then a
   int source[kWindow];
@@ -118,7 +121,7 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
 #pragma unroll
   for (int i = 0; i < kDyLoads; ++i) {
     dy_row[i] = 4 * (wave + kWaves * i) + (lane >> 4);
-    const int col = tn * kTileN + ((lane & 15) ^ (dy_row[i] & 15)) * 8;
+    const int col = tn * kTileN + ((lane & 15) ^ swizzle(dy_row[i])) * 8;
     dy[i] = g.dy + (static_cast<size_t>(at) + s0 * kStep + dy_row[i]) * g.N + col;
     if (col >= g.N) dy_row[i] = 1 << 30;
   }
@@ -126,7 +129,7 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
   uint32_t a_stride[kALoads];
 #pragma unroll
   for (int i = 0; i < kALoads; ++i) {
-    const int col = tk * kTileK + ((lane & 31) ^ ((2 * (wave + kWaves * i) + (lane >> 5)) & 15)) * 8;
+    const int col = tk * kTileK + ((lane & 31) ^ swizzle(2 * (wave + kWaves * i) + (lane >> 5))) * 8;
     a0[i] = reinterpret_cast<const unsigned char*>(col < g.K ? static_cast<const void*>(g.a + col) : &zeros);
     a_stride[i] = col < g.K ? static_cast<uint32_t>(g.K) * 2 : 0;
   }
@@ -172,10 +175,10 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
   uint32_t at_k[kFragsK], at_n[kFragsN];
 #pragma unroll
   for (int f = 0; f < kFragsK; ++f)
-    at_k[f] = lds_address(&sh.stage[0][0]) + kABytes + lrow * (kChunksK * 16) + ((wk * 16 + 2 * f + (piece >> 1)) ^ lrow) * 16 + (piece & 1) * 8;
+    at_k[f] = lds_address(&sh.stage[0][0]) + kABytes + lrow * (kChunksK * 16) + ((wk * 16 + 2 * f + (piece >> 1)) ^ swizzle(lrow)) * 16 + (piece & 1) * 8;
 #pragma unroll
   for (int f = 0; f < kFragsN; ++f)
-    at_n[f] = lds_address(&sh.stage[0][0]) + lrow * (kChunksN * 16) + ((wn * 8 + 2 * f + (piece >> 1)) ^ lrow) * 16 + (piece & 1) * 8;
+    at_n[f] = lds_address(&sh.stage[0][0]) + lrow * (kChunksN * 16) + ((wn * 8 + 2 * f + (piece >> 1)) ^ swizzle(lrow)) * 16 + (piece & 1) * 8;
 
   v4f acc[kFragsK][kFragsN];
 #pragma unroll
@@ -291,11 +294,12 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
 // Where routing is skewed one expert's rows can be more than a block's share of all the
 // work, and where an expert has few tiles there are too few blocks. Then experts with
 // more than C steps of rows are cut into parts of at most that many, the longest parts
-// are first in the grid, and a kernel adds up the parts' sums in their order. C is half
-// of what a block takes if the steps of all tiles are dealt out to kSlots blocks: all
-// steps / most, most = 2 kSlots / tiles. So parts are at most `most` more than experts,
+// are first in the grid, and a kernel adds up the parts' sums in their order. C is
+// what a block takes if the steps of all tiles are dealt out to kSlots blocks: all
+// steps / most, most = kSlots / tiles. So parts are at most `most` more than experts,
 // whatever the counts are, and the parts of cut experts at most 2 most: their sums take
-// about 4 kSlots tiles of 128 x 256 at most, 268 MB.
+// about 2 kSlots tiles of 128 x 256 at most, 134 MB. (C half of that, the skewed top-6
+// batch: 664 us for 640; a quarter: 727.)
 
 constexpr int kSlots = 512;      // blocks that run at once
 constexpr int kLeastSteps = 8;   // C is no less
@@ -321,25 +325,24 @@ __global__ __launch_bounds__(kPlanThreads) void weight_grad_plan_kernel(GradArgs
   __syncthreads();
   if (e >= g.E) return;
   int units = 0, places = 0, cuts = 0;  // of the experts before this one
+  bool last = true;
+  const int mine = key[e].x;
+#pragma unroll 8
   for (int j = 0; j < g.E; ++j) {
     const int2 k = key[j];
-    if (k.x > key[e].x || (k.x == key[e].x && j < e)) {
-      units += k.y;
-      if (k.y > 1) {
-        places += k.y;
-        ++cuts;
-      }
-    }
+    const bool before = k.x > mine || (k.x == mine && j < e);
+    const int n = before ? k.y : 0, cut = n > 1 ? n : 0;
+    units += n;
+    places += cut;
+    cuts += n > 1 ? 1 : 0;
+    last = last && (before || j == e);
   }
   for (int i = 0; i < parts; ++i)
     g.unit[units + i] = make_int4(e, static_cast<int>(static_cast<long long>(steps) * i / parts),
                                   static_cast<int>(static_cast<long long>(steps) * (i + 1) / parts),
                                   parts > 1 ? places + i : -1);
   if (parts > 1) g.cut[cuts] = make_int4(e, places, parts, 0);
-  // the last expert of the order knows the sums
-  bool last = true;
-  for (int j = 0; j < g.E; ++j) last = last && !(key[j].x < key[e].x || (key[j].x == key[e].x && j > e));
-  if (last) {
+  if (last) {  // it knows the sums
     g.found[0] = units + parts;
     g.found[1] = cuts + (parts > 1);
   }
@@ -382,8 +385,8 @@ struct Plan {
     const long long tiles = static_cast<long long>(n_tiles_of(N)) * k_tiles_of(K);
     if (k * tiles >= kSlots || T < 1024) return;
     const long long steps = static_cast<long long>(T) * k / kStep + E;
-    const long long by_share = 2 * kSlots / tiles, by_least = steps / kLeastSteps;
-    most = static_cast<int>(by_share < by_least ? by_share : by_least);  // at least 2
+    const long long by_share = kSlots / tiles, by_least = steps / kLeastSteps;
+    most = static_cast<int>(by_share < by_least ? by_share : by_least);  // at least 1
     units = E + most;
     places = 2 * most;
     cuts = E < most ? E : most;
