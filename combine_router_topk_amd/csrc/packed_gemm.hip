@@ -6,6 +6,8 @@
 // for every row r of expert e's segment, r' = r or the token of the row (src[r] /
 // k). The epilogue writes z in the activation format or fp32, or takes the two halves
 // of the weights' rows as gate and up and writes silu(gate) up in 16 bits.
+#include <stddef.h>
+
 #include "device.hpp"
 #include "launch.hpp"
 #include "packed.hpp"
@@ -36,12 +38,15 @@ __device__ __forceinline__ size_t source_row(const PackedGemmArgs& g, int row) {
   return i < 0 ? 0 : min(i / g.k, g.a_rows - 1);
 }
 
+// An expert's segment, cut to the rows there are.
+__device__ __forceinline__ int2 segment_of(const PackedGemmArgs& g, int e) {
+  const int at = min(max(g.offsets[e], 0), g.rows);
+  return make_int2(at, min(max(g.counts[e], 0), g.rows - at));
+}
+
 // First tile of each expert, with `per` rows a tile: first[E] is their number.
-// A segment is cut to the rows there are.
 struct Segments {
   int first[kMaxE + 1];
-  int seg[kMaxE];
-  int have[kMaxE];
 };
 template <int NT>
 __device__ __forceinline__ void find_segments(const PackedGemmArgs& g, int per, Segments& sh, int* sums) {
@@ -50,12 +55,7 @@ __device__ __forceinline__ void find_segments(const PackedGemmArgs& g, int per, 
   for (int e0 = 0; e0 < g.E; e0 += NT) {
     const int e = e0 + tid;
     int tiles = 0;
-    if (e < g.E) {
-      const int at = min(max(g.offsets[e], 0), g.rows), have = min(max(g.counts[e], 0), g.rows - at);
-      sh.seg[e] = at;
-      sh.have[e] = have;
-      tiles = (have + per - 1) / per * g.n_tiles;
-    }
+    if (e < g.E) tiles = (segment_of(g, e).y + per - 1) / per * g.n_tiles;
     const int upto = wave_incl_scan(tiles, lane);
     if (lane == kWave - 1) sums[wave] = upto;
     __syncthreads();
@@ -111,9 +111,10 @@ __global__ __launch_bounds__(kThinThreads, 5) void packed_thin_kernel(PackedGemm
   int turn = 0;
   for (int i = blockIdx.x; i < work; i += gridDim.x, turn ^= 1) {
     const int e = __builtin_amdgcn_readfirstlane(expert_of(sh, g.E, i));
-    const int in = i - sh.first[e], m_tiles = (sh.have[e] + 15) / 16;
+    const int2 seg = segment_of(g, e);
+    const int in = i - sh.first[e], m_tiles = (seg.y + 15) / 16;
     const int n = in / m_tiles, m0 = (in % m_tiles) * 16;  // rows of the same weights follow each other
-    const int row0 = sh.seg[e] + m0, have = min(16, sh.have[e] - m0);
+    const int row0 = seg.x + m0, have = min(16, seg.y - m0);
     const int ta = SWIGLU ? n : 2 * n, tb = SWIGLU ? n + g.half / kPackedRows : min(2 * n + 1, row_tiles - 1);
     const unsigned char* wa = g.w + (static_cast<size_t>(e) * row_tiles + ta) * strip;
     const unsigned char* wb = g.w + (static_cast<size_t>(e) * row_tiles + tb) * strip;
@@ -162,20 +163,60 @@ __global__ __launch_bounds__(kThinThreads, 5) void packed_thin_kernel(PackedGemm
 }
 
 // ---- many rows an expert -----------------------------------------------------------
+//
+// A block multiplies 128 rows by 256 weight rows, its 8 waves 64 by 64 each (2 along the
+// rows, 4 along the weights). Rows, codes and scales of a step of 128 columns go to LDS
+// without passing registers, three steps in a ring. A wave takes 64 rows of a group's
+// columns into registers, then one tile of weights after the other: its codes become
+// 16-bit numbers between the products, and the group's sums are multiplied by their
+// scales under the next tile's products.
 
-constexpr int kFatThreads = 512;
+constexpr int kFatThreads = 512, kFatWaves = kFatThreads / kWave;
 constexpr int kFatRows = 128;              // of a tile: 2 waves of 64
-constexpr int kFatTiles = 4;               // of weights, a wave: 4 waves of 64 weight rows
+constexpr int kFatTiles = 4;               // of weights, a wave
 constexpr int kFatFrags = 4;               // of 16 rows, a wave
 constexpr int kFatBlocks = 256;
+constexpr int kFatStages = 3;
+constexpr int kFatLoads = 7;               // of a wave in a step: 4 of rows, 2 of codes, 1 of scales
 
-// Rows of a step in LDS: 256 bytes each, 16-byte chunk c of row r at place c ^ (r %
-// 16), so that 16 lanes that read one chunk of 16 rows meet all banks.
-struct FatShared {
-  uint4 rows[2][kFatRows * 16];
-  Segments seg;
-  int sums[kFatThreads / kWave];
+// Rows of a step: 256 bytes each, 16-byte chunk c of row r at place c ^ (r % 16), so that
+// 16 lanes that read one chunk of 16 rows meet all banks. Two tiles' scales follow each
+// other, from each 256 bytes on.
+struct FatStage {
+  uint4 rows[kFatRows * 16];
+  uint4 codes[4 * kFatTiles * 64];
+  unsigned char scales[kFatWaves * 256];
 };
+struct FatShared {
+  FatStage stage[kFatStages];
+  Segments seg;
+  int sums[kFatWaves];
+};
+constexpr uint32_t kFatStageBytes = sizeof(FatStage);
+static_assert(sizeof(FatShared) <= 160 * 1024, "LDS");
+
+// What is loaded in place of columns past the rows' end.
+__device__ const uint4 zeros = {0, 0, 0, 0};
+
+// Each lane's 16 (or 4) bytes go to LDS at byte lds + 16 (or 4) * lane without passing
+// through registers. Written as assembly because the compiler, which cannot tell the
+// stages apart, waits for every such load of its own before the next LDS read; here the
+// loop counts them. `lds` is the same in all lanes; M0 may be read one wait state after
+// it was written.
+__device__ __forceinline__ void load_lds16(const void* from, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void load_lds4(const void* from, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "{m0}"(lds) : "memory");
+}
+// Waits until at most N of this wave's loads are in flight, then for the other waves.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
+}
 
 template <int ACT, int CODES, int PER, bool SWIGLU>
 __global__ __launch_bounds__(kFatThreads, 2) void packed_fat_kernel(PackedGemmArgs g) {
@@ -190,46 +231,51 @@ __global__ __launch_bounds__(kFatThreads, 2) void packed_fat_kernel(PackedGemmAr
   const int steps = packed_col_tiles(g.K), row_tiles = packed_row_tiles(g.N);
   const size_t strip = static_cast<size_t>(steps) * TB;
   const int work = sh.seg.first[g.E];
+  // weight tile l (of 16) of block column nb; those past the end are the last one again
+  auto tile_of = [&](int nb, int l) {
+    if constexpr (SWIGLU) {
+      const int last = g.half / kPackedRows - 1, n = l & 3;
+      return min(nb * 8 + (l >> 2) * 2 + (n & 1), last) + (n >> 1) * (last + 1);
+    } else {
+      return min(nb * 16 + l, row_tiles - 1);
+    }
+  };
   for (int i = blockIdx.x; i < work; i += gridDim.x) {
     const int e = __builtin_amdgcn_readfirstlane(expert_of(sh.seg, g.E, i));
-    const int in = i - sh.seg.first[e], m_tiles = (sh.seg.have[e] + kFatRows - 1) / kFatRows;
+    const int2 seg = segment_of(g, e);
+    const int in = i - sh.seg.first[e], m_tiles = (seg.y + kFatRows - 1) / kFatRows;
     const int nb = in / m_tiles, m0 = (in % m_tiles) * kFatRows;
-    const int row0 = sh.seg.seg[e] + m0, have = min(kFatRows, sh.seg.have[e] - m0);
-    // the wave's tiles of weights; those past the end are the last one again
-    int tile[kFatTiles];
-    const unsigned char* w[kFatTiles];
-#pragma unroll
-    for (int n = 0; n < kFatTiles; ++n) {
-      if constexpr (SWIGLU) {
-        const int t = nb * 8 + wn * 2 + (n & 1), last = g.half / kPackedRows - 1;
-        tile[n] = t;
-        w[n] = g.w + (static_cast<size_t>(e) * row_tiles + min(t, last) + (n >> 1) * (last + 1)) * strip;
-      } else {
-        tile[n] = nb * 16 + wn * 4 + n;
-        w[n] = g.w + (static_cast<size_t>(e) * row_tiles + min(tile[n], row_tiles - 1)) * strip;
-      }
-    }
+    const int row0 = seg.x + m0, have = min(kFatRows, seg.y - m0);
     const bool idle = have <= wm * 64;
-    // the thread's four chunks of the rows
-    const uint16_t* from[4];
-    const int chunk = tid & 15;
+
+    // what this lane loads in each step
+    const int chunk = (lane & 15) ^ ((4 * wave + (lane >> 4)) & 15);
+    const uint16_t* row[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = (tid >> 4) + 32 * j;
-      from[j] = g.a + source_row(g, row0 + min(m, have - 1)) * g.K + chunk * 8;
+    for (int q = 0; q < 4; ++q) {
+      const int m = 4 * (wave + kFatWaves * q) + (lane >> 4);
+      row[q] = g.a + source_row(g, row0 + min(m, have - 1)) * g.K + chunk * 8;
     }
-    uint4 rows[4];
-    PackedTile<PER> t[kFatTiles];
-    auto load_rows = [&](int kb) {
+    const unsigned char* w = g.w + static_cast<size_t>(e) * row_tiles * strip;
+    const unsigned char* code[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        rows[j] = make_uint4(0, 0, 0, 0);
-        if (kb * kPackedCols + chunk * 8 < g.K) rows[j] = *reinterpret_cast<const uint4*>(from[j] + kb * kPackedCols);
+    for (int q = 0; q < 2; ++q) code[q] = w + tile_of(nb, 2 * wave + q) * strip + lane * 16;
+    constexpr int kScaleLanes = 8 * PER;  // of a tile
+    const unsigned char* scale = w + tile_of(nb, 2 * wave + (lane / kScaleLanes & 1)) * strip + kPackedCodes +
+                                 lane % kScaleLanes * 4;
+    const uint32_t lds0 = lds_address(&sh.stage[0]);
+    auto load = [&](int q, int kb, uint32_t at) {  // the q-th of a step's loads
+      if (q < 4) {
+        const uint64_t from = reinterpret_cast<uint64_t>(row[q] + kb * kPackedCols), zero = reinterpret_cast<uint64_t>(&zeros);
+        load_lds16(reinterpret_cast<const void*>(kb * kPackedCols + chunk * 8 < g.K ? from : zero),
+                   lds0 + at + (wave + kFatWaves * q) * 1024);
+      } else if (q < 6) {
+        load_lds16(code[q - 4] + static_cast<size_t>(kb) * TB,
+                   lds0 + at + static_cast<uint32_t>(offsetof(FatStage, codes)) + (2 * wave + q - 4) * 1024);
+      } else {
+        load_lds4(scale + static_cast<size_t>(kb) * TB,
+                  lds0 + at + static_cast<uint32_t>(offsetof(FatStage, scales)) + wave * 256);
       }
-    };
-    auto load_tiles = [&](int kb) {
-#pragma unroll
-      for (int n = 0; n < kFatTiles; ++n) t[n].load(w[n] + static_cast<size_t>(kb) * TB, lane);
     };
 
     v4f acc[kFatTiles][kFatFrags];
@@ -237,75 +283,132 @@ __global__ __launch_bounds__(kFatThreads, 2) void packed_fat_kernel(PackedGemmAr
     for (int n = 0; n < kFatTiles; ++n)
 #pragma unroll
       for (int f = 0; f < kFatFrags; ++f) acc[n][f] = v4f{0, 0, 0, 0};
-    __syncthreads();  // the last tile's rows have been read
-    load_rows(0);
-    load_tiles(0);
+    __syncthreads();  // the stages are free
+    for (int kb = 0; kb < min(2, steps); ++kb)
+#pragma unroll
+      for (int q = 0; q < kFatLoads; ++q) load(q, kb, kb * kFatStageBytes);
+    uint32_t now = 0, ahead = 2 * kFatStageBytes;
     for (int kb = 0; kb < steps; ++kb) {
-      uint4* stage = sh.rows[kb & 1];
+      if (kb + 1 < steps) wait_loads<kFatLoads>();
+      else wait_loads<0>();
+      if (kb + 2 < steps)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int m = (tid >> 4) + 32 * j;
-        stage[m * 16 + (chunk ^ (m & 15))] = rows[j];
-      }
-      __syncthreads();
-      PackedTile<PER> now[kFatTiles];
-#pragma unroll
-      for (int n = 0; n < kFatTiles; ++n) now[n] = t[n];
-      if (kb + 1 < steps) {
-        load_rows(kb + 1);
-        load_tiles(kb + 1);
-      }
-      if (idle) continue;
-      float s[kFatTiles][PER];
-#pragma unroll
-      for (int n = 0; n < kFatTiles; ++n) now[n].scales(g.scale_act, s[n]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // one 32 columns' operands at a time: more in flight would not fit the registers
-        __builtin_amdgcn_sched_barrier(0);
-        uint4 x[kFatFrags];
-#pragma unroll
-        for (int f = 0; f < kFatFrags; ++f) x[f] = stage[(wm * 64 + f * 16 + r) * 16 + ((4 * j + grp) ^ r)];
-        constexpr uint32_t kMinus8 = ACT == 1 ? 0xc800c800u : 0xc100c100u;
-        v4f start[kFatFrags];
-#pragma unroll
-        for (int f = 0; f < kFatFrags; ++f) {
-          start[f] = v4f{0, 0, 0, 0};
-          if constexpr (CODES == kPackedInt)
-            start[f] = mfma16<ACT>(x[f], make_uint4(kMinus8, kMinus8, kMinus8, kMinus8), start[f]);
-        }
+        for (int q = 0; q < kFatLoads; ++q) load(q, kb + 2, ahead);
+      if (!idle) {
+        const FatStage& st = *reinterpret_cast<const FatStage*>(lds + now);
+        uint4 codes[kFatTiles];
+        uint32_t raw[kFatTiles][PER == 4 ? 2 : 1];
 #pragma unroll
         for (int n = 0; n < kFatTiles; ++n) {
-          const uint32_t d = j == 0 ? now[n].codes.x : j == 1 ? now[n].codes.y : j == 2 ? now[n].codes.z : now[n].codes.w;
-          const uint4 v = packed_values<ACT, CODES>(d);
+          const int l = wn * kFatTiles + n;
+          codes[n] = st.codes[l * 64 + lane];
+          const unsigned char* s = st.scales + (l >> 1) * 256 + (l & 1) * (32 * PER) + r * (2 * PER);
+          if constexpr (PER == 1) raw[n][0] = *reinterpret_cast<const uint16_t*>(s);
+          else raw[n][0] = *reinterpret_cast<const uint32_t*>(s);
+          if constexpr (PER == 4) raw[n][1] = *reinterpret_cast<const uint32_t*>(s + 4);
+        }
+        v4f z[2][kFatFrags];
+        float sc[2];
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+          uint4 x[kIn][kFatFrags];
+#pragma unroll
+          for (int j = 0; j < kIn; ++j)
+#pragma unroll
+            for (int f = 0; f < kFatFrags; ++f)
+              x[j][f] = st.rows[(wm * 64 + f * 16 + r) * 16 + ((4 * (p * kIn + j) + grp) ^ r)];
+          v4f start[kFatFrags];
 #pragma unroll
           for (int f = 0; f < kFatFrags; ++f) {
-            const v4f z = mfma16<ACT>(x[f], v, start[f]);
+            start[f] = v4f{0, 0, 0, 0};
+            if constexpr (CODES == kPackedInt) {
+              constexpr uint32_t kMinus8 = ACT == 1 ? 0xc800c800u : 0xc100c100u;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[n][f][q] = fmaf(z[q], s[n][j / kIn], acc[n][f][q]);
+              for (int j = 0; j < kIn; ++j)
+                start[f] = mfma16<ACT>(x[j][f], make_uint4(kMinus8, kMinus8, kMinus8, kMinus8), start[f]);
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < kFatTiles; ++n) {
+            const int step = p * kFatTiles + n, b = step & 1;
+            __builtin_amdgcn_sched_barrier(0);
+            const uint32_t bits = p & 1 ? raw[n][p >> 1] >> 16 : raw[n][p >> 1] & 0xffffu;
+            const float as16 = f16_to_f32(bits), asb = bf16_to_f32(bits);
+            sc[b] = g.scale_act == 1 ? as16 : asb;
+#pragma unroll
+            for (int j = 0; j < kIn; ++j) {
+              const int c = p * kIn + j;
+              const uint4 v = packed_values<ACT, CODES>(c == 0 ? codes[n].x : c == 1 ? codes[n].y : c == 2 ? codes[n].z
+                                                                                                          : codes[n].w);
+#pragma unroll
+              for (int f = 0; f < kFatFrags; ++f) z[b][f] = mfma16<ACT>(x[j][f], v, j == 0 ? start[f] : z[b][f]);
+            }
+            if (step > 0) {
+              const int before = (step - 1) % kFatTiles;
+#pragma unroll
+              for (int f = 0; f < kFatFrags; ++f)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[before][f][q] = fmaf(z[b ^ 1][f][q], sc[b ^ 1], acc[before][f][q]);
+            }
+            // one product, then what the vector unit does meanwhile
+#pragma unroll
+            for (int m = 0; m < kIn * kFatFrags; ++m) {
+              __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x002, 2 + 4 / kIn, 0);
+            }
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < kFatFrags; ++f)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            acc[kFatTiles - 1][f][q] = fmaf(z[1][f][q], sc[1], acc[kFatTiles - 1][f][q]);
       }
+      now = now == 2 * kFatStageBytes ? 0 : now + kFatStageBytes;
+      ahead = ahead == 2 * kFatStageBytes ? 0 : ahead + kFatStageBytes;
     }
+
+    // A lane's results lie in 16 rows, one column of a tile each: they go through the
+    // wave's part of the stages, and whole pieces of a row are stored.
+    __syncthreads();
+    if (!idle) {
+      constexpr int kColumns = SWIGLU ? 32 : 64;
+      constexpr uint32_t kPart = kFatStages * kFatStageBytes / kFatWaves / 256 * 256;
+      unsigned char* const mine = reinterpret_cast<unsigned char*>(lds) + wave * kPart;
+      auto pass = [&](auto F32) {
+        constexpr bool f32 = F32;
+        constexpr int kLine = kColumns * (f32 ? 4 : 2), kPitch = kLine + 16, kLanes = kLine / 16;
+        static_assert(64 * kPitch <= kPart, "");
 #pragma unroll
-    for (int f = 0; f < kFatFrags; ++f) {
+        for (int n = 0; n < kColumns / 16; ++n)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int m = wm * 64 + f * 16 + 4 * grp + q;
-        if (m >= have) continue;
-        const size_t row = row0 + m;
-        if constexpr (SWIGLU) {
+          for (int f = 0; f < kFatFrags; ++f)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-            if (tile[n] < g.half / kPackedRows)
-              static_cast<uint16_t*>(g.y)[row * g.half + tile[n] * kPackedRows + r] =
-                  static_cast<uint16_t>(pack2<ACT>(silu(acc[n][f][q]) * acc[n + 2][f][q], 0.0f));
-        } else {
-#pragma unroll
-          for (int n = 0; n < kFatTiles; ++n)
-            if (tile[n] * kPackedRows + r < g.N) store_one<ACT>(g, row * g.N + tile[n] * kPackedRows + r, acc[n][f][q]);
+            for (int q = 0; q < 4; ++q) {
+              float v = acc[n][f][q];
+              if constexpr (SWIGLU) v = silu(v) * acc[n + 2][f][q];
+              unsigned char* to = mine + (f * 16 + 4 * grp + q) * kPitch + (n * 16 + r) * (f32 ? 4 : 2);
+              if constexpr (f32) *reinterpret_cast<float*>(to) = v;
+              else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(pack2<ACT>(v, 0.0f));
+            }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's lanes exchange them
+        const int width = SWIGLU ? g.half : g.N;
+        const int col = (nb * 4 + wn) * kColumns + lane % kLanes * (f32 ? 4 : 8);
+#pragma unroll 2
+        for (int m = 0; m < 64; m += kWave / kLanes) {
+          const int at = m + lane / kLanes, mm = wm * 64 + at;
+          const uint4 v = *reinterpret_cast<const uint4*>(mine + at * kPitch + lane % kLanes * 16);
+          if (mm < have && col < width) {
+            const size_t to = static_cast<size_t>(row0 + mm) * width + col;
+            if constexpr (f32) *reinterpret_cast<uint4*>(static_cast<float*>(g.y) + to) = v;
+            else *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.y) + to) = v;
+          }
         }
-      }
+      };
+      if constexpr (SWIGLU) pass(std::false_type{});
+      else if (g.out_f32) pass(std::true_type{});
+      else pass(std::false_type{});
     }
   }
 }
