@@ -60,6 +60,14 @@ __device__ __forceinline__ uint4 packed_values(uint32_t d) {
   }
 }
 
+// One of two scales as fp32. Both formats' conversions and a selection: a branch on
+// the format for each scale costs more than they do.
+__device__ __forceinline__ float packed_scale(int act, uint32_t two, int high) {
+  const uint32_t b = high ? two >> 16 : two & 0xffffu;
+  const float h = f16_to_f32(b), f = bf16_to_f32(b);
+  return act == 1 ? h : f;
+}
+
 // A lane's part of a tile: its 32 codes and its row's scales as they lie there.
 template <int PER>
 struct PackedTile {
@@ -78,13 +86,9 @@ struct PackedTile {
       scale[0] = v.x, scale[1] = v.y;
     }
   }
-  // `act` is the same in all lanes
   __device__ __forceinline__ void scales(int act, float (&f)[PER]) const {
 #pragma unroll
-    for (int p = 0; p < PER; ++p) {
-      const uint32_t b = p & 1 ? scale[p >> 1] >> 16 : scale[p >> 1] & 0xffffu;
-      f[p] = act == 1 ? f16_to_f32(b) : bf16_to_f32(b);
-    }
+    for (int p = 0; p < PER; ++p) f[p] = packed_scale(act, scale[p >> 1], p & 1);
   }
 };
 

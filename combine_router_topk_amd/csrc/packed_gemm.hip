@@ -332,9 +332,7 @@ __global__ __launch_bounds__(kFatThreads, 2) void packed_fat_kernel(PackedGemmAr
           for (int n = 0; n < kFatTiles; ++n) {
             const int step = p * kFatTiles + n, b = step & 1;
             __builtin_amdgcn_sched_barrier(0);
-            const uint32_t bits = p & 1 ? raw[n][p >> 1] >> 16 : raw[n][p >> 1] & 0xffffu;
-            const float as16 = f16_to_f32(bits), asb = bf16_to_f32(bits);
-            sc[b] = g.scale_act == 1 ? as16 : asb;
+            sc[b] = packed_scale(g.scale_act, raw[n][p >> 1], p & 1);
 #pragma unroll
             for (int j = 0; j < kIn; ++j) {
               const int c = p * kIn + j;

@@ -19,7 +19,6 @@ namespace {
 
 constexpr int kUpThreads = 256, kUpWaves = kUpThreads / kWave;
 constexpr int kUpBlocks = 1280;
-constexpr int kDownThreads = 512, kDownWaves = kDownThreads / kWave;
 
 struct PackedArgs : RouteArgs {
   const void* x;
@@ -69,6 +68,13 @@ __global__ __launch_bounds__(kUpThreads, 5) void packed_up_kernel(PackedArgs g) 
   if constexpr (ROUTES) {
     for (int t = wave; t < g.T; t += kUpWaves) route_any(g, t, lane, sh.idx, blockIdx.x == 0);
     build_tables<kUpThreads>(g, sh, &items);
+    if (blockIdx.x == 0) {  // for the down product
+      for (int i = tid; i < pairs; i += kUpThreads) {
+        if (i < items) g.item[i] = sh.item[i];
+        g.order[i] = sh.order[i];
+      }
+      if (tid == 0) g.head[0] = items;
+    }
   } else {
     if (tid == 0) items = g.head[0];
     for (int i = tid; i < pairs; i += kUpThreads) {  // those past the items are not used
@@ -148,45 +154,45 @@ __global__ __launch_bounds__(kUpThreads, 5) void packed_up_kernel(PackedArgs g) 
 }
 
 // ---- down product and weighted combine -------------------------------------------
+//
+// Each block owns 16 columns of the output for every token, its waves contiguous parts
+// of the (item, step of K) sequence. An item's at most 16 tokens fill the instruction
+// from its first row on, whichever they are; their sums go, times their gate weights, to
+// the wave's own sums of all tokens in LDS. (With fixed places of tokens an expert's
+// two tokens often took two instructions' rows: 32 tokens of 256 experts, 7168 x 2048,
+// 433 us for this kernel.) With several shares blockIdx.y is the share of the sequence,
+// and packed_sum_kernel adds them up.
 
-template <int TT>
-struct DownShared {
-  int idx[kMaxPairs];
-  float w[kMaxPairs];
-  int flag[kMaxE];
-  int active[kMaxPairs];
-  int n_active;
-  float4 part[kDownWaves][TT][kWave];
+struct DownTables {
+  int4* item;    // [pairs]
+  int* order;    // [pairs]
+  float* w;      // [pairs]
+  float* sum;    // [waves][T][16]
+  static size_t bytes(int pairs, int T, int waves) {
+    return pairs * (sizeof(int4) + sizeof(int) + sizeof(float)) + static_cast<size_t>(waves) * T * 16 * sizeof(float);
+  }
+  __device__ __forceinline__ DownTables(void* lds, int pairs) {
+    item = static_cast<int4*>(lds);
+    order = reinterpret_cast<int*>(item + pairs);
+    w = reinterpret_cast<float*>(order + pairs);
+    sum = w + pairs;
+  }
 };
 
-// Each block owns 16 columns of the output for every token (TT groups of 16), its
-// waves contiguous parts of the (expert, step of K) sequence. With several shares
-// blockIdx.y is the share of the sequence, and packed_sum_kernel adds them up.
-template <int ACT, int CODES, int PER, int TT>
-__global__ __launch_bounds__(kDownThreads, 4) void packed_down_kernel(PackedArgs g) {
-  __shared__ DownShared<TT> sh;
+template <int ACT, int CODES, int PER, int NT>
+__global__ __launch_bounds__(NT, 4) void packed_down_kernel(PackedArgs g) {
+  constexpr int kWaves = NT / kWave;
+  extern __shared__ __align__(16) char tables[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int pairs = g.T * g.k;
-  for (int e = tid; e < g.E; e += kDownThreads) sh.flag[e] = 0;
-  __syncthreads();
-  for (int p = tid; p < pairs; p += kDownThreads) {
-    const int e = min(max(g.idx[p], 0), g.E - 1);
-    sh.idx[p] = e;
+  const int pairs = g.T * g.k, sums = g.T * 16;
+  const DownTables sh(tables, pairs);
+  for (int p = tid; p < pairs; p += NT) {  // those past the items are not used
+    sh.item[p] = g.item[p];
+    sh.order[p] = g.order[p];
     sh.w[p] = g.w[p];
-    sh.flag[e] = 1;
   }
-  __syncthreads();
-  if (wave == 0) {
-    int n = 0;
-    for (int e0 = 0; e0 < g.E; e0 += kWave) {
-      const int e = e0 + lane;
-      const bool on = e < g.E && sh.flag[e] != 0;
-      const uint64_t m = ballot(on);
-      if (on) sh.active[n + __builtin_popcountll(m & lanemask_lt(lane))] = e;
-      n += __builtin_popcountll(m);
-    }
-    if (lane == 0) sh.n_active = n;
-  }
+  for (int i = tid; i < kWaves * sums; i += NT) sh.sum[i] = 0.0f;
+  const int items = g.head[0];
   __syncthreads();
 
   constexpr int TB = packed_tile_bytes(PER);
@@ -194,88 +200,62 @@ __global__ __launch_bounds__(kDownThreads, 4) void packed_down_kernel(PackedArgs
   const int tile = blockIdx.x, tiles = packed_row_tiles(g.H), steps = packed_col_tiles(g.I);
   const size_t strip = static_cast<size_t>(steps) * TB;
   const int shares = gridDim.y, share = blockIdx.y;
-  const int all = sh.n_active * steps;
+  const int all = items * steps;
   const int total = all / shares + (share < all % shares ? 1 : 0);
-  int q = all / shares * share + min(share, all % shares) + total / kDownWaves * wave + min(wave, total % kDownWaves);
-  const int q_end = q + total / kDownWaves + (wave < total % kDownWaves ? 1 : 0);
-
-  v4f acc[TT];
-#pragma unroll
-  for (int u = 0; u < TT; ++u) acc[u] = v4f{0, 0, 0, 0};
+  int q = all / shares * share + min(share, all % shares) + total / kWaves * wave + min(wave, total % kWaves);
+  const int q_end = q + total / kWaves + (wave < total % kWaves ? 1 : 0);
+  float* const mine = sh.sum + wave * sums + r;
   while (q < q_end) {
-    const int ei = q / steps, k0 = q % steps, k1 = min(steps, k0 + q_end - q);
+    const int i = q / steps, k0 = q % steps, k1 = min(steps, k0 + q_end - q);
     q += k1 - k0;
-    const int e = __builtin_amdgcn_readfirstlane(sh.active[ei]);
+    const int4 it = sh.item[i];
+    const int e = __builtin_amdgcn_readfirstlane(it.x), off = it.y, have = it.z;
     const unsigned char* row = g.w_down + (static_cast<size_t>(e) * tiles + tile) * strip;
-    const uint16_t* tok[TT];
-    float wt[TT];
-    bool on[TT], any[TT];
-    v4f sum[TT];
-#pragma unroll
-    for (int u = 0; u < TT; ++u) {
-      const int t = u * kPackedRows + r;
-      int pair = -1;
-      if (t < g.T)
-        for (int j = 0; j < g.k; ++j)
-          if (sh.idx[t * g.k + j] == e) pair = t * g.k + j;
-      on[u] = pair >= 0;
-      any[u] = ballot(on[u]) != 0;
-      wt[u] = on[u] ? sh.w[pair] : 0.0f;
-      tok[u] = static_cast<const uint16_t*>(g.h) + static_cast<size_t>(on[u] ? pair : 0) * g.I;
-      sum[u] = v4f{0, 0, 0, 0};
-    }
-    constexpr int D = TT == 4 ? 1 : 2;  // steps in flight
+    const uint16_t* tok = static_cast<const uint16_t*>(g.h) + static_cast<size_t>(sh.order[off + min(r, have - 1)]) * g.I;
+    const int cols = r < have ? g.I : 0;
+    v4f sum = {0, 0, 0, 0};
+    constexpr int D = 2;  // steps in flight
     for (int kb0 = k0; kb0 < k1; kb0 += D) {
       PackedTile<PER> a[D];
+      PackedRows c[D];
 #pragma unroll
-      for (int d = 0; d < D; ++d)
-        if (kb0 + d < k1) a[d].load(row + static_cast<size_t>(kb0 + d) * TB, lane);
+      for (int d = 0; d < D; ++d) {
+        if (kb0 + d < k1) {
+          a[d].load(row + static_cast<size_t>(kb0 + d) * TB, lane);
+          c[d].load(tok, kb0 + d, grp, cols);
+        }
+      }
 #pragma unroll
-      for (int u = 0; u < TT; ++u) {
-        if (!any[u]) continue;
-        PackedRows c[D];
-#pragma unroll
-        for (int d = 0; d < D; ++d)
-          if (kb0 + d < k1) c[d].load(tok[u], kb0 + d, grp, on[u] ? g.I : 0);
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-          if (kb0 + d < k1) {
-            float s[PER];
-            a[d].scales(g.scale_act, s);
-            v4f start[PER];
-            packed_start<ACT, CODES, PER>(c[d], start);
-            packed_product<ACT, CODES, PER>(c[d], a[d], s, start, sum[u]);
-          }
+      for (int d = 0; d < D; ++d) {
+        if (kb0 + d < k1) {
+          float s[PER];
+          a[d].scales(g.scale_act, s);
+          v4f start[PER];
+          packed_start<ACT, CODES, PER>(c[d], start);
+          packed_product<ACT, CODES, PER>(c[d], a[d], s, start, sum);
         }
       }
     }
-    // the gate weights of this lane's four tokens
+    // an expert's tokens are different ones
 #pragma unroll
-    for (int u = 0; u < TT; ++u) {
-      if (!any[u]) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float f = __shfl(wt[u], 4 * grp + i, kWave);
-        acc[u][i] = f != 0.0f ? fmaf(sum[u][i], f, acc[u][i]) : acc[u][i];
+    for (int j = 0; j < 4; ++j) {
+      const int m = 4 * grp + j;
+      if (m < have) {
+        const int pair = sh.order[off + m];
+        float* to = mine + pair / g.k * 16;
+        *to = fmaf(sum[j], sh.w[pair], *to);
       }
     }
   }
-#pragma unroll
-  for (int u = 0; u < TT; ++u)
-    sh.part[wave][u][lane] = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
   __syncthreads();
-  for (int o = tid; o < TT * 256; o += kDownThreads) {
-    const int u = o >> 8, v = o & 255;
-    const int t = u * kPackedRows + (v >> 6) * 4 + (v & 3), n = tile * kPackedRows + ((v >> 2) & 15);
+  for (int o = tid; o < sums; o += NT) {
     float z = 0.0f;
 #pragma unroll
-    for (int wv = 0; wv < kDownWaves; ++wv) z += reinterpret_cast<const float*>(sh.part[wv][u])[v];
-    if (t < g.T) {
-      const size_t at = static_cast<size_t>(t) * g.H + n;
-      if (shares > 1) g.part[static_cast<size_t>(share) * g.T * g.H + at] = z;
-      else if (g.out_f32) static_cast<float*>(g.out)[at] = z;
-      else static_cast<uint16_t*>(g.out)[at] = static_cast<uint16_t>(pack2<ACT>(z, 0.0f));
-    }
+    for (int wv = 0; wv < kWaves; ++wv) z += sh.sum[wv * sums + o];
+    const size_t at = static_cast<size_t>(o >> 4) * g.H + tile * kPackedRows + (o & 15);
+    if (shares > 1) g.part[static_cast<size_t>(share) * g.T * g.H + at] = z;
+    else if (g.out_f32) static_cast<float*>(g.out)[at] = z;
+    else static_cast<uint16_t*>(g.out)[at] = static_cast<uint16_t>(pack2<ACT>(z, 0.0f));
   }
 }
 
@@ -324,9 +304,12 @@ hipError_t launch(const PackedArgs& g, hipStream_t s) {
   if (err != hipSuccess) return err;
   const int shares = shares_of(g.T, g.E, g.k, g.H, g.I);
   const dim3 grid(packed_row_tiles(g.H), shares);
-  if (g.T <= 16) packed_down_kernel<ACT, CODES, PER, 1><<<grid, kDownThreads, 0, s>>>(g);
-  else if (g.T <= 32) packed_down_kernel<ACT, CODES, PER, 2><<<grid, kDownThreads, 0, s>>>(g);
-  else packed_down_kernel<ACT, CODES, PER, 4><<<grid, kDownThreads, 0, s>>>(g);
+  auto down = [&](auto N) {
+    constexpr int NT = N;
+    packed_down_kernel<ACT, CODES, PER, NT><<<grid, NT, DownTables::bytes(g.T * g.k, g.T, NT / kWave), s>>>(g);
+  };
+  if (grid.x * grid.y <= 256) down(std::integral_constant<int, 1024>{});
+  else down(std::integral_constant<int, 512>{});
   err = hipGetLastError();
   if (err != hipSuccess || shares == 1) return err;
   packed_sum_kernel<ACT><<<(g.T * g.H / 4 + 255) / 256, 256, 0, s>>>(g, shares);
