@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kUpThreads = 256, kUpWaves = kUpThreads / kWave;
 constexpr int kUpBlocks = 1280;
+constexpr int kManyTiles = 4 * kUpBlocks;  // pairs of tiles from which on a block takes two at a time
 
 struct PackedArgs : RouteArgs {
   const void* x;
@@ -56,10 +57,11 @@ __global__ __launch_bounds__(kRouteThreads) void packed_route_kernel(RouteArgs g
 // ---- gate and up products, SwiGLU ----------------------------------------------
 
 // ROUTES: every block routes the tokens itself and takes tiles in turn; else the
-// tables are there, and a block that is done takes the next tile that nobody has.
-template <int ACT, int CODES, int PER, bool ROUTES>
-__global__ __launch_bounds__(kUpThreads, 5) void packed_up_kernel(PackedArgs g) {
-  __shared__ float4 part[2][kUpWaves][2][kWave];
+// tables are there, and a block that is done takes the next tile that nobody has. A
+// block has PAIRS tiles of the gate's weight rows and the up's beside them at a time.
+template <int ACT, int CODES, int PER, bool ROUTES, int PAIRS>
+__global__ __launch_bounds__(kUpThreads, PAIRS == 1 ? 5 : 4) void packed_up_kernel(PackedArgs g) {
+  __shared__ float4 part[2][kUpWaves][2 * PAIRS][kWave];
   __shared__ int items, next_tile[2];
   extern __shared__ __align__(16) char tables[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -86,7 +88,7 @@ __global__ __launch_bounds__(kUpThreads, 5) void packed_up_kernel(PackedArgs g) 
 
   constexpr int TB = packed_tile_bytes(PER);
   const int r = lane & 15, grp = lane >> 4;
-  const int n_tiles = g.I / kPackedRows, steps = packed_col_tiles(g.H);
+  const int gate_tiles = g.I / kPackedRows, n_tiles = (gate_tiles + PAIRS - 1) / PAIRS, steps = packed_col_tiles(g.H);
   const int work = items * n_tiles, blocks = gridDim.x;
   const size_t strip = static_cast<size_t>(steps) * TB;  // a row of tiles
   int turn = 0;
@@ -96,59 +98,60 @@ __global__ __launch_bounds__(kUpThreads, 5) void packed_up_kernel(PackedArgs g) 
       if (tid == 0) next = blocks + atomicAdd(&g.head[1], 1);
     }
     const int4 it = sh.item[i / n_tiles];
-    const int tile = i % n_tiles;
+    const int tile = i % n_tiles * PAIRS;
     const int e = __builtin_amdgcn_readfirstlane(it.x), off = it.y, have = it.z;
-    const unsigned char* gate_row = g.w_up + (static_cast<size_t>(e) * 2 * n_tiles + tile) * strip;
-    const unsigned char* up_row = gate_row + n_tiles * strip;
+    const unsigned char* gate_row = g.w_up + (static_cast<size_t>(e) * 2 * gate_tiles + tile) * strip;
+    const unsigned char* up_row = gate_row + gate_tiles * strip;
+    const size_t beside = tile + 1 < gate_tiles ? strip : 0;  // of two pairs the second's
     const int my_pair = sh.order[off + min(r, have - 1)];
     const uint16_t* tok = static_cast<const uint16_t*>(g.x) + static_cast<size_t>(my_pair / g.k) * g.H;
     const int cols = r < have ? g.H : 0;
 
-    v4f gate = {0, 0, 0, 0}, up = {0, 0, 0, 0};
-    constexpr int D = 1;  // steps in flight
-    for (int kb0 = wave; kb0 < steps; kb0 += kUpWaves * D) {
-      PackedTile<PER> a[D], b[D];
-      PackedRows c[D];
+    v4f sum[2 * PAIRS];  // gate and up of each pair
 #pragma unroll
-      for (int d = 0; d < D; ++d) {
-        const int kb = kb0 + d * kUpWaves;
-        if (kb < steps) {
-          a[d].load(gate_row + static_cast<size_t>(kb) * TB, lane);
-          b[d].load(up_row + static_cast<size_t>(kb) * TB, lane);
-          c[d].load(tok, kb, grp, cols);
-        }
+    for (int n = 0; n < 2 * PAIRS; ++n) sum[n] = v4f{0, 0, 0, 0};
+    for (int kb = wave; kb < steps; kb += kUpWaves) {
+      PackedTile<PER> a[2 * PAIRS];
+      PackedRows c;
+      const size_t at = static_cast<size_t>(kb) * TB;
+#pragma unroll
+      for (int n = 0; n < PAIRS; ++n) {
+        a[2 * n].load(gate_row + n * beside + at, lane);
+        a[2 * n + 1].load(up_row + n * beside + at, lane);
       }
+      c.load(tok, kb, grp, cols);
+      v4f start[PER];
+      packed_start<ACT, CODES, PER>(c, start);
 #pragma unroll
-      for (int d = 0; d < D; ++d) {
-        if (kb0 + d * kUpWaves < steps) {
-          float sg[PER], su[PER];
-          a[d].scales(g.scale_act, sg);
-          b[d].scales(g.scale_act, su);
-          v4f start[PER];
-          packed_start<ACT, CODES, PER>(c[d], start);
-          packed_product<ACT, CODES, PER>(c[d], a[d], sg, start, gate);
-          packed_product<ACT, CODES, PER>(c[d], b[d], su, start, up);
-        }
+      for (int n = 0; n < 2 * PAIRS; ++n) {
+        float s[PER];
+        a[n].scales(g.scale_act, s);
+        packed_product<ACT, CODES, PER>(c, a[n], s, start, sum[n]);
       }
     }
-    part[turn][wave][0][lane] = make_float4(gate[0], gate[1], gate[2], gate[3]);
-    part[turn][wave][1][lane] = make_float4(up[0], up[1], up[2], up[3]);
+#pragma unroll
+    for (int n = 0; n < 2 * PAIRS; ++n)
+      part[turn][wave][n][lane] = make_float4(sum[n][0], sum[n][1], sum[n][2], sum[n][3]);
     if (!ROUTES && tid == 0) next_tile[turn] = next;
     __syncthreads();
     i = ROUTES ? next : __builtin_amdgcn_readfirstlane(next_tile[turn]);
     // thread tid sums value tid % 4 of lane tid / 4: token 4 (tid / 64) + tid % 4 of
     // the item, weight row (tid / 4) % 16 of the tile
-    const int c = (tid >> 6) * 4 + (tid & 3), n = (tid >> 2) & 15;
-    float zg = 0.0f, zu = 0.0f;
+    const int c = (tid >> 6) * 4 + (tid & 3);
 #pragma unroll
-    for (int wv = 0; wv < kUpWaves; ++wv) {
-      zg += reinterpret_cast<const float*>(part[turn][wv][0])[tid];
-      zu += reinterpret_cast<const float*>(part[turn][wv][1])[tid];
-    }
-    if (c < have) {
-      const float h = silu(zg) * zu;
-      static_cast<uint16_t*>(g.h)[static_cast<size_t>(sh.order[off + c]) * g.I + tile * kPackedRows + n] =
-          static_cast<uint16_t>(pack2<ACT>(h, 0.0f));
+    for (int p = 0; p < PAIRS; ++p) {
+      const int n = (tile + p) * kPackedRows + ((tid >> 2) & 15);
+      float zg = 0.0f, zu = 0.0f;
+#pragma unroll
+      for (int wv = 0; wv < kUpWaves; ++wv) {
+        zg += reinterpret_cast<const float*>(part[turn][wv][2 * p])[tid];
+        zu += reinterpret_cast<const float*>(part[turn][wv][2 * p + 1])[tid];
+      }
+      if (c < have && n < g.I) {
+        const float h = silu(zg) * zu;
+        static_cast<uint16_t*>(g.h)[static_cast<size_t>(sh.order[off + c]) * g.I + n] =
+            static_cast<uint16_t>(pack2<ACT>(h, 0.0f));
+      }
     }
   }
 }
@@ -167,9 +170,9 @@ struct DownTables {
   int4* item;    // [pairs]
   int* order;    // [pairs]
   float* w;      // [pairs]
-  float* sum;    // [waves][T][16]
-  static size_t bytes(int pairs, int T, int waves) {
-    return pairs * (sizeof(int4) + sizeof(int) + sizeof(float)) + static_cast<size_t>(waves) * T * 16 * sizeof(float);
+  float* sum;    // [waves][T][columns of the block]
+  static size_t bytes(int pairs, int T, int waves, int columns) {
+    return pairs * (sizeof(int4) + sizeof(int) + sizeof(float)) + sizeof(float) * waves * T * columns;
   }
   __device__ __forceinline__ DownTables(void* lds, int pairs) {
     item = static_cast<int4*>(lds);
@@ -179,12 +182,12 @@ struct DownTables {
   }
 };
 
-template <int ACT, int CODES, int PER, int NT>
+template <int ACT, int CODES, int PER, int NT, int TILES>
 __global__ __launch_bounds__(NT, 4) void packed_down_kernel(PackedArgs g) {
-  constexpr int kWaves = NT / kWave;
+  constexpr int kWaves = NT / kWave, kColumns = TILES * kPackedRows;
   extern __shared__ __align__(16) char tables[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int pairs = g.T * g.k, sums = g.T * 16;
+  const int pairs = g.T * g.k, sums = g.T * kColumns;
   const DownTables sh(tables, pairs);
   for (int p = tid; p < pairs; p += NT) {  // those past the items are not used
     sh.item[p] = g.item[p];
@@ -197,8 +200,9 @@ __global__ __launch_bounds__(NT, 4) void packed_down_kernel(PackedArgs g) {
 
   constexpr int TB = packed_tile_bytes(PER);
   const int r = lane & 15, grp = lane >> 4;
-  const int tile = blockIdx.x, tiles = packed_row_tiles(g.H), steps = packed_col_tiles(g.I);
+  const int tile = blockIdx.x * TILES, tiles = packed_row_tiles(g.H), steps = packed_col_tiles(g.I);
   const size_t strip = static_cast<size_t>(steps) * TB;
+  const size_t next = tile + 1 < tiles ? strip : 0;  // of a block's two tiles
   const int shares = gridDim.y, share = blockIdx.y;
   const int all = items * steps;
   const int total = all / shares + (share < all % shares ? 1 : 0);
@@ -213,26 +217,32 @@ __global__ __launch_bounds__(NT, 4) void packed_down_kernel(PackedArgs g) {
     const unsigned char* row = g.w_down + (static_cast<size_t>(e) * tiles + tile) * strip;
     const uint16_t* tok = static_cast<const uint16_t*>(g.h) + static_cast<size_t>(sh.order[off + min(r, have - 1)]) * g.I;
     const int cols = r < have ? g.I : 0;
-    v4f sum = {0, 0, 0, 0};
-    constexpr int D = 2;  // steps in flight
+    v4f sum[TILES];
+#pragma unroll
+    for (int n = 0; n < TILES; ++n) sum[n] = v4f{0, 0, 0, 0};
+    constexpr int D = 2 / TILES;  // steps in flight
     for (int kb0 = k0; kb0 < k1; kb0 += D) {
-      PackedTile<PER> a[D];
+      PackedTile<PER> a[D][TILES];
       PackedRows c[D];
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         if (kb0 + d < k1) {
-          a[d].load(row + static_cast<size_t>(kb0 + d) * TB, lane);
+#pragma unroll
+          for (int n = 0; n < TILES; ++n) a[d][n].load(row + n * next + static_cast<size_t>(kb0 + d) * TB, lane);
           c[d].load(tok, kb0 + d, grp, cols);
         }
       }
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         if (kb0 + d < k1) {
-          float s[PER];
-          a[d].scales(g.scale_act, s);
           v4f start[PER];
           packed_start<ACT, CODES, PER>(c[d], start);
-          packed_product<ACT, CODES, PER>(c[d], a[d], s, start, sum);
+#pragma unroll
+          for (int n = 0; n < TILES; ++n) {
+            float s[PER];
+            a[d][n].scales(g.scale_act, s);
+            packed_product<ACT, CODES, PER>(c[d], a[d][n], s, start, sum[n]);
+          }
         }
       }
     }
@@ -242,8 +252,9 @@ __global__ __launch_bounds__(NT, 4) void packed_down_kernel(PackedArgs g) {
       const int m = 4 * grp + j;
       if (m < have) {
         const int pair = sh.order[off + m];
-        float* to = mine + pair / g.k * 16;
-        *to = fmaf(sum[j], sh.w[pair], *to);
+        float* to = mine + pair / g.k * kColumns;
+#pragma unroll
+        for (int n = 0; n < TILES; ++n) to[n * 16] = fmaf(sum[n][j], sh.w[pair], to[n * 16]);
       }
     }
   }
@@ -252,7 +263,9 @@ __global__ __launch_bounds__(NT, 4) void packed_down_kernel(PackedArgs g) {
     float z = 0.0f;
 #pragma unroll
     for (int wv = 0; wv < kWaves; ++wv) z += sh.sum[wv * sums + o];
-    const size_t at = static_cast<size_t>(o >> 4) * g.H + tile * kPackedRows + (o & 15);
+    const int col = tile * kPackedRows + o % kColumns;
+    if (TILES > 1 && col >= g.H) continue;
+    const size_t at = static_cast<size_t>(o / kColumns) * g.H + col;
     if (shares > 1) g.part[static_cast<size_t>(share) * g.T * g.H + at] = z;
     else if (g.out_f32) static_cast<float*>(g.out)[at] = z;
     else static_cast<uint16_t*>(g.out)[at] = static_cast<uint16_t>(pack2<ACT>(z, 0.0f));
@@ -273,7 +286,7 @@ __global__ __launch_bounds__(256) void packed_sum_kernel(PackedArgs g, int share
   else static_cast<uint2*>(g.out)[i] = make_uint2(pack2<ACT>(z.x, z.y), pack2<ACT>(z.z, z.w));
 }
 
-constexpr int kShares = 4;
+constexpr int kShares = 8;
 int shares_of(int T, int E, int k, int H, int I) {
   const int tiles = packed_row_tiles(H);
   const long long experts = T * k < E ? T * k : E;
@@ -289,27 +302,41 @@ size_t table_bytes(int T, int k) {
 template <int ACT, int CODES, int PER>
 hipError_t launch(const PackedArgs& g, hipStream_t s) {
   const int per_token = g.E * ((g.T + 15) / 16);
-  const long long items = static_cast<long long>(g.T * g.k < per_token ? g.T * g.k : per_token) * (g.I / kPackedRows);
-  const int blocks = items < kUpBlocks ? static_cast<int>(items) : kUpBlocks;
+  const long long items = g.T * g.k < per_token ? g.T * g.k : per_token;
   const size_t lds = Tables::bytes(g.T * g.k, g.E);
+  auto up = [&](auto R, auto P) {
+    constexpr bool ROUTES = R;
+    constexpr int PAIRS = P;
+    const long long work = items * ((g.I / kPackedRows + PAIRS - 1) / PAIRS);
+    const int blocks = work < kUpBlocks ? static_cast<int>(work) : kUpBlocks;
+    packed_up_kernel<ACT, CODES, PER, ROUTES, PAIRS>
+        <<<blocks, kUpThreads, ROUTES ? lds : Tables::bytes(g.T * g.k, 0), s>>>(g);
+  };
+  auto pairs = [&](auto R) {
+    if (items * (g.I / kPackedRows) >= kManyTiles) up(R, std::integral_constant<int, 2>{});
+    else up(R, std::integral_constant<int, 1>{});
+  };
   if (g.T * g.k <= kFewPairs) {
-    packed_up_kernel<ACT, CODES, PER, true><<<blocks, kUpThreads, lds, s>>>(g);
+    pairs(std::true_type{});
   } else {
     packed_route_kernel<<<1, kRouteThreads, lds, s>>>(g);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    packed_up_kernel<ACT, CODES, PER, false><<<blocks, kUpThreads, Tables::bytes(g.T * g.k, 0), s>>>(g);
+    pairs(std::false_type{});
   }
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int shares = shares_of(g.T, g.E, g.k, g.H, g.I);
-  const dim3 grid(packed_row_tiles(g.H), shares);
-  auto down = [&](auto N) {
-    constexpr int NT = N;
-    packed_down_kernel<ACT, CODES, PER, NT><<<grid, NT, DownTables::bytes(g.T * g.k, g.T, NT / kWave), s>>>(g);
+  auto down = [&](auto N, auto M) {
+    constexpr int NT = N, TILES = M;
+    const dim3 grid((packed_row_tiles(g.H) + TILES - 1) / TILES, shares);
+    packed_down_kernel<ACT, CODES, PER, NT, TILES>
+        <<<grid, NT, DownTables::bytes(g.T * g.k, g.T, NT / kWave, TILES * kPackedRows), s>>>(g);
   };
-  if (grid.x * grid.y <= 256) down(std::integral_constant<int, 1024>{});
-  else down(std::integral_constant<int, 512>{});
+  using One = std::integral_constant<int, 1>;
+  if (shares > 1) down(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
+  else if (packed_row_tiles(g.H) <= 256) down(std::integral_constant<int, 1024>{}, One{});
+  else down(std::integral_constant<int, 512>{}, One{});
   err = hipGetLastError();
   if (err != hipSuccess || shares == 1) return err;
   packed_sum_kernel<ACT><<<(g.T * g.H / 4 + 255) / 256, 256, 0, s>>>(g, shares);

@@ -98,6 +98,14 @@ def test_wide_and_deep():
     check_gemm([40] * 1000, 2, 40, 16, B.MOE_F16, O.INT, 64, True)
 
 
+@pytest.mark.parametrize("codes,group", [(O.INT, 64), (O.E2M1, 32)])
+def test_many_tiles_of_few_rows(codes, group):
+    """Blocks of four tiles, the last of an expert past its end, rows of 17 too."""
+    counts = [1, 0, 17, 2] * 256
+    check_gemm(counts, 2, 72, 168, B.MOE_F16, codes, group, True)
+    check_gemm(counts, 2, 264, 112, B.MOE_BF16, codes, group, False, swiglu=True)
+
+
 @pytest.mark.parametrize("counts", [[5, 8, 3], [300, 100, 4]])
 @pytest.mark.parametrize("codes", [O.INT, O.E2M1])
 def test_rows_are_their_own(counts, codes):

@@ -101,6 +101,13 @@ def test_layer_many_experts_wide_rows_and_around_224_pairs(T, E, k, H, I):
     check_layer(T, E, k, H, I, B.MOE_F16, O.E2M1, 32)
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [(64, 128, 8, 144, 176), (28, 256, 8, 144, 400)])
+def test_layer_of_many_tiles(T, E, k, H, I):
+    """Blocks of two pairs of tiles, the last one of an expert without its second."""
+    check_layer(T, E, k, H, I, B.MOE_BF16, O.INT, 128)
+    check_layer(T, E, k, H, I, B.MOE_F16, O.E2M1, 32)
+
+
 @pytest.mark.parametrize("codes,group", FORMATS)
 def test_layer_fp32_output_and_scales_of_the_other_format(codes, group):
     check_layer(9, 8, 2, 144, 80, B.MOE_F16, codes, group, B.MOE_FLAG_OUT_F32, scale_act=B.MOE_BF16)
