@@ -422,9 +422,27 @@ __global__ __launch_bounds__(kFatThreads, 2) void packed_fat_kernel(PackedGemmAr
   }
 }
 
+// Which kernel: the thin one takes every 16 rows (half of an expert's last ones are not
+// there on average) through the expert's weights, at 8.5e12 weights a second. A tile of
+// the fat one takes 1.55 us a step with up to 64 rows and 2.2 with more, on each of 256
+// CUs. Measured, us of both (int4, groups of 128; rows an expert on average):
+//   experts, K, N             8         16        24        32        64        128
+//   64, 2048, 2048        34,  55   55,  53   76,  52   82,  52  157,  77  300, 157
+//   256, 2048, 4096      255, 389  352, 393  433, 399  531, 409  950, 546 1857, 917
+//   32, 1024, 7168        27,  57   41,  55   56,  55   66,  55  123,  72  218, 122
+//   8, 4096, 2048         12,  44   16,  45   21,  45   25,  46   41,  69   75,  71
+//   4, 1024, 1024         11,  14   11,  15   11,  15   12,  15   11,  21   11,  21
+bool few_rows(int rows, int E, int K, int n) {
+  const double experts = rows < E ? rows : E, average = rows / experts;
+  const double thin = (rows / 16.0 + experts / 2) * n * K / 8.5e6;
+  const double tiles = ceil(experts * (average <= 128 ? 1 : average / 128 + 0.5) * ((n + 255) / 256) / 256);
+  const double fat = 5 + tiles * packed_col_tiles(K) * (average <= 48 ? 1.55 : 2.2);
+  return thin <= fat;
+}
+
 template <int ACT, int CODES, int PER, bool SWIGLU>
 hipError_t launch(PackedGemmArgs& g, hipStream_t s) {
-  if (g.rows <= 32ll * g.E) {
+  if (few_rows(g.rows, g.E, g.K, g.N)) {
     const int y_tiles = packed_row_tiles(SWIGLU ? g.half : g.N);
     auto thin = [&](auto N) {
       constexpr int TILES = N, kApart = SWIGLU ? TILES / 2 : TILES;

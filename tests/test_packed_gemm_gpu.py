@@ -91,6 +91,86 @@ def test_fp32_rows_and_scales_of_the_other_format(codes, group):
             check_gemm(counts, 2, 200, 72, act, codes, group, False, flags=B.MOE_FLAG_OUT_F32, scale_act=3 - act)
 
 
+# Enough rows and weights for the kernel of many rows; its tiles have 128 rows (two halves)
+# and 256 weight rows.
+LARGE = [129, 0, 64, 1, 300, 65, 127, 128] * 3
+
+
+def few_rows(rows, E, K, n):
+    """The library's choice between its two kernels (its thin one if true)."""
+    experts = min(rows, E)
+    average = rows / experts
+    thin = (rows / 16 + experts / 2) * n * K / 8.5e6
+    tiles = np.ceil(experts * (1 if average <= 128 else average / 128 + 0.5) * -(-n // 256) / 256)
+    return thin <= 5 + tiles * -(-K // 128) * (1.55 if average <= 48 else 2.2)
+
+
+@pytest.mark.parametrize("codes,group", FORMATS)
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("K,N,swiglu", [(264, 4104, False), (392, 4112, False), (264, 2064, True)])
+def test_many_rows(K, N, swiglu, act, codes, group):
+    assert not few_rows(sum(LARGE), len(LARGE), K, 2 * N if swiglu else N)
+    check_gemm(LARGE, 2, K, N, act, codes, group, gather=True, swiglu=swiglu)
+
+
+def test_many_rows_fp32_in_send_order_and_one_step():
+    for codes, group in FORMATS[::2]:
+        check_gemm(LARGE, 1, 264, 4104, B.MOE_F16, codes, group, False, flags=B.MOE_FLAG_OUT_F32, scale_act=B.MOE_BF16)
+    counts = [40] * 300
+    assert not few_rows(12000, 300, 128, 2056) and not few_rows(12000, 300, 104, 2056)
+    check_gemm(counts, 2, 128, 2056, B.MOE_BF16, O.E2M1, 64, True)
+    check_gemm(counts, 3, 104, 2056, B.MOE_BF16, O.INT, 32, True)
+
+
+def test_many_rows_are_their_own_repeat_and_replay():
+    rng = np.random.default_rng(1)
+    counts = np.asarray(LARGE, np.int32)
+    n, K, N, act, E = int(counts.sum()), 264, 4104, B.MOE_BF16, len(LARGE)
+    offsets = (np.cumsum(counts) - counts).astype(np.int32)
+    p = B.make_problem(n, E, 1, 8, 1, act)
+    a = bits16(rng, (n, K), act)
+    w = Weights(rng, E, N, K, O.INT, 64, act)
+
+    def run(a, counts, stream=None):
+        y = torch.full((n, N), -7.0, dtype=torch.bfloat16, device="cuda")
+        args = dev(a, act), None, w.dev, dev(counts), dev(offsets), y
+        torch.cuda.synchronize()
+        B.moe_expert_gemm_packed(p, w.format, K, N, *args, stream)
+        torch.cuda.synchronize()
+        return y
+
+    want = run(a, counts)
+    bad = a.copy()
+    bad[2, K - 1], bad[600, 3] = 0x7fc0, 0x7f80
+    got = run(bad, counts, torch.cuda.Stream())
+    rest = [r for r in range(n) if r not in (2, 600)]
+    assert torch.equal(got[rest], want[rest]) and torch.isnan(got[2]).all() and not torch.isfinite(got[600]).any()
+    fewer = counts.copy()
+    fewer[0] -= 70
+    got = run(a, fewer)
+    gap = list(range(int(counts[0]) - 70, int(counts[0])))
+    rest = [r for r in range(n) if r not in gap]
+    assert torch.equal(got[rest], want[rest]) and (got[gap] == -7).all()
+    av, cv, ov, y = dev(a, act), dev(counts), dev(offsets), torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.moe_expert_gemm_packed(p, w.format, K, N, av, None, w.dev, cv, ov, y)
+    for _ in range(3):
+        y.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+    # segments that reach beyond the rows are cut, sources clamped
+    src = torch.full((n,), 1 << 30, dtype=torch.int32, device="cuda")
+    src[0] = -5
+    far = torch.full((E,), 1 << 30, dtype=torch.int32, device="cuda")
+    y = torch.full((n + 8, N), -7.0, dtype=torch.bfloat16, device="cuda")
+    B.moe_expert_gemm_packed(p, w.format, K, N, av, src, w.dev, far, ov, y)
+    torch.cuda.synchronize()
+    assert (y[n:] == -7).all() and torch.isfinite(y[:n]).all()
+
+
 def test_wide_and_deep():
     check_gemm([2, 1, 4, 1], 1, 4104, 1048, B.MOE_F16, O.INT, 128, False)
     check_gemm([260, 1, 40, 83], 2, 2056, 1048, B.MOE_BF16, O.E2M1, 32, True)
