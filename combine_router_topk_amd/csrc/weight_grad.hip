@@ -58,8 +58,6 @@ struct Shared {
 };
 constexpr uint32_t kStageBytes = kStep * (kChunksN + kChunksK) * 16, kABytes = kStep * kChunksN * 16;
 
-constexpr int kWaveBytes = kStages * kStageBytes / kWaves;  // for a wave's results
-
 // What is loaded in place of rows past the segment's end and columns past the matrix's.
 __device__ const uint4 zeros = {0, 0, 0, 0};
 
@@ -84,6 +82,14 @@ __device__ __forceinline__ uint2 read_transposed(uint32_t at) {
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
+}
+
+// Among lanes l, l + 16, l + 32, l + 48 (g = 0 .. 3) with values (a, g) and (b, g): lane
+// g gets what lanes 2 (g % 2) and 2 (g % 2) + 1 had of a (g < 2) or b.
+__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
+  const auto s = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  const auto t = __builtin_amdgcn_permlane16_swap(s[0], s[1], false, false);
+  a = t[0], b = t[1];
 }
 
 // Tile `in` of an expert. Neighbouring blocks go to the eight dies in turn, so each die
@@ -232,61 +238,40 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
     ahead = ahead == 2 * kStageBytes ? 0 : ahead + kStageBytes;
   }
 
-  // A lane's four results of a fragment are four neighbouring k of one n, so that stores
-  // straight from there would take 16 rows' lines for 32 or 64 bytes each. The wave's
-  // results go through its part of the stages instead, and whole lines of a row are
-  // stored: without that 64 experts of 4096 x 4096 take 1650 us.
-  __syncthreads();  // all waves have read the last step
-  unsigned char* const mine = reinterpret_cast<unsigned char*>(lds) + wave * kWaveBytes;
-  const bool whole = slot >= 0 || g.out_f32;  // fp32
+  // A lane's four results of a fragment are four neighbouring k of one n: 16 bytes in
+  // fp32, 64 of a row by four lanes. In 16 bits these four exchange the results of two
+  // fragments, so that each has 8 neighbours: stores of 32 bytes of a row instead took
+  // 1650 us for 64 experts of 4096 x 4096.
   const size_t matrix = static_cast<size_t>(e) * g.N * g.K;
-  const int k0 = tk * kTileK + wk * 128;
-  auto pass = [&](auto F32) {
-    constexpr bool f32 = F32;
-    constexpr int kFrags = f32 ? 2 : 4;  // along N at a time
-    constexpr int kLine = 128 * (f32 ? 4 : 2), kPitch = kLine + 16;
-    constexpr int kLanes = kLine / 16;  // of a row
-    static_assert(16 * kFrags * kPitch <= kWaveBytes, "");
 #pragma unroll
-    for (int j0 = 0; j0 < kFragsN; j0 += kFrags) {
+  for (int j = 0; j < kFragsN; ++j) {
+    const int n = tn * kTileN + wn * 64 + j * 16 + (lane & 15);
+    const size_t line = static_cast<size_t>(n) * g.K;
+    if (slot >= 0 || g.out_f32) {
 #pragma unroll
-      for (int j = 0; j < kFrags; ++j) {
-#pragma unroll
-        for (int i = 0; i < kFragsK; ++i) {
-          const v4f v = acc[i][j0 + j];
-          unsigned char* to = mine + (16 * j + (lane & 15)) * kPitch + (16 * i + 4 * grp) * (f32 ? 4 : 2);
-          if constexpr (f32) *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
-          else *reinterpret_cast<uint2*>(to) = make_uint2(pack2<ACT>(v[0], v[1]), pack2<ACT>(v[2], v[3]));
-        }
-      }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's lanes exchange them
-#pragma unroll
-      for (int r = 0; r < 16 * kFrags; r += kWave / kLanes) {
-        const int row = r + lane / kLanes, n = tn * kTileN + wn * 64 + 16 * j0 + row;
-        const int k = k0 + lane % kLanes * (f32 ? 4 : 8);
-        const uint4 v = *reinterpret_cast<const uint4*>(mine + row * kPitch + lane % kLanes * 16);
+      for (int i = 0; i < kFragsK; ++i) {
+        const int k = tk * kTileK + wk * 128 + i * 16 + grp * 4;
         if (n >= g.N || k >= g.K) continue;
-        const size_t at = matrix + static_cast<size_t>(n) * g.K + k;
-        if constexpr (!f32) {
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.dw) + at) = v;
-        } else if (slot >= 0) {
-          *reinterpret_cast<uint4*>(g.part + static_cast<size_t>(slot) * g.N * g.K + at - matrix) = v;
-        } else {
-          float4 f = __builtin_bit_cast(float4, v);
-          float4* to = reinterpret_cast<float4*>(static_cast<float*>(g.dw) + at);
-          if (g.add) {
-            const float4 o = *to;
-            f = make_float4(o.x + f.x, o.y + f.y, o.z + f.z, o.w + f.w);
-          }
-          // 131 MB in odd rows 60 us with ordinary stores, 49 (rows in 16 bits: 1547 for 1434)
-          __builtin_nontemporal_store(__builtin_bit_cast(v4f, f), reinterpret_cast<v4f*>(to));
-        }
+        v4f v = acc[i][j];
+        v4f* to = reinterpret_cast<v4f*>(slot >= 0 ? g.part + static_cast<size_t>(slot) * g.N * g.K + line + k
+                                                   : static_cast<float*>(g.dw) + matrix + line + k);
+        if (slot < 0 && g.add) v += *to;
+        __builtin_nontemporal_store(v, to);
       }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < kFragsK; i += 2) {
+        const v4f a = acc[i][j], b = acc[i + 1][j];
+        uint2 p = make_uint2(pack2<ACT>(a[0], a[1]), pack2<ACT>(a[2], a[3]));
+        uint2 q = make_uint2(pack2<ACT>(b[0], b[1]), pack2<ACT>(b[2], b[3]));
+        exchange(p.x, q.x);
+        exchange(p.y, q.y);
+        const int k = tk * kTileK + wk * 128 + i * 16 + grp * 8;
+        if (n < g.N && k < g.K)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.dw) + matrix + line + k) = make_uint4(p.x, p.y, q.x, q.y);
+      }
     }
-  };
-  if (whole) pass(std::true_type{});
-  else pass(std::false_type{});
+  }
 }
 
 // ---- the plan ------------------------------------------------------------------------
