@@ -192,9 +192,8 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
 #pragma unroll
     for (int j = 0; j < kFragsN; ++j) acc[i][j] = v4f{0, 0, 0, 0};
 
-  // Two steps' loads are in flight while a third is multiplied. A step's are issued
-  // between the products, their rows' sources read from LDS a step before that: all at
-  // the step's beginning they kept the products waiting for 800 of its 1600 cycles.
+  // Two steps' loads are in flight while a third is multiplied, issued between the
+  // products, their rows' sources read from LDS a step before.
   uint32_t now = 0, ahead = 2 * kStageBytes;
   if (s0 < s1) {
     fill(s0);

@@ -105,6 +105,38 @@ def test_plans_of_overlapping_segments_stay_inside():
     assert (dw == T).all() and (ws[need:] == 77).all()
 
 
+@pytest.mark.parametrize("E,k,K,N,counts,act,out", [
+    (1024, 2, 520, 264, [0, 1, 33, 64, 65, 100, 7, 32], B.MOE_BF16, "add"),
+    (1024, 1, 776, 264, [0, 40, 1100, 0, 0, 96, 0, 0], B.MOE_F16, "16"),
+    (16, 2, 4096, 4096, [0, 1, 33, 64, 65, 100, 1090, 33], B.MOE_BF16, "16"),
+    (16, 2, 4104, 4096, [70, 35, 64, 65], B.MOE_F16, "f32")])
+def test_thousands_of_tiles(E, k, K, N, counts, act, out):
+    """Rows of no step, one, two and more, and more than have their sources in LDS."""
+    say(f"[case] weight grad of many tiles E={E} K={K} N={N} {out}")
+    rng = np.random.default_rng(K)
+    counts = np.asarray(counts * (E // len(counts)), np.int32)
+    T, src, offsets = segments_of(rng, counts, k)
+    p = B.make_problem(T, E, k, 8, 1, act, 0 if out == "16" else B.MOE_FLAG_OUT_F32)
+    torch.manual_seed(K)
+    dt = torch.float16 if act == B.MOE_F16 else torch.bfloat16
+    a, dy = torch.randn(T, K, device="cuda").to(dt), torch.randn(T * k, N, device="cuda").to(dt)
+    dw = torch.full((E, N, K), 0.5, dtype=dt if out == "16" else torch.float32, device="cuda")
+    grad(p, K, N, a, dev(src), dy, dev(counts), dev(offsets), out == "add", dw)
+    torch.cuda.synchronize()
+    rows = torch.from_numpy(src // k).cuda().long()
+    for e in range(E) if E < 100 else [*range(16), *range(500, 508), *range(E - 8, E)]:
+        r = slice(int(offsets[e]), int(offsets[e] + counts[e]))
+        av, dv = a[rows[r]].double(), dy[r].double()
+        want, size = dv.T @ av, dv.abs().T @ av.abs()
+        bound = (int(counts[e]) + 24) * 2 * U * size
+        if out == "add":
+            want = want + 0.5
+            bound = bound + U * want.abs() * 1.01
+        elif out == "16":
+            bound = bound + HALF[act] * (want.abs() + bound) * 1.01 + 2.0 ** -25
+        assert ((dw[e].double() - want).abs() <= bound + 1e-30).all(), e
+
+
 def test_many_experts():
     check_grad([4] * 1024, 2, 40, 16, B.MOE_BF16, True, "f32")
     check_grad([0] * 500 + [70] * 20 + [0] * 400, 2, 72, 264, B.MOE_F16, False, "16")
