@@ -240,7 +240,9 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
   // A lane's four results of a fragment are four neighbouring k of one n: 16 bytes in
   // fp32, 64 of a row by four lanes. In 16 bits these four exchange the results of two
   // fragments, so that each has 8 neighbours: stores of 32 bytes of a row instead took
-  // 1650 us for 64 experts of 4096 x 4096.
+  // 1650 us for 64 experts of 4096 x 4096, this 1455. (Whole lines by way of LDS, 1440
+  // there and 560 for 457 where fp32 sums are added up in 2048 x 2048; stores past the
+  // caches, 62 for 22 us in 110 MB of odd rows.)
   const size_t matrix = static_cast<size_t>(e) * g.N * g.K;
 #pragma unroll
   for (int j = 0; j < kFragsN; ++j) {
@@ -255,7 +257,7 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs g) {
         v4f* to = reinterpret_cast<v4f*>(slot >= 0 ? g.part + static_cast<size_t>(slot) * g.N * g.K + line + k
                                                    : static_cast<float*>(g.dw) + matrix + line + k);
         if (slot < 0 && g.add) v += *to;
-        __builtin_nontemporal_store(v, to);
+        *to = v;
       }
     } else {
 #pragma unroll
