@@ -3,7 +3,7 @@
 //   m = b1 m + (1 - b1) g          v = b2 v + (1 - b2) g^2
 //   w = w - lr decay w - lr (m / c1) / (sqrt(v / c2) + eps),   ci = 1 - bi^step
 //
-// A block takes 2048 or 4096 elements of one tensor, a thread 8 neighbours at a time
+// A block takes 2048 elements of one tensor, a thread 8 neighbours at a time
 // (whole 16-byte loads of every array). The tensors come as kernel arguments,
 // up to 56 a launch, with each one's first block: the lanes of a wave compare
 // those with their block's number at once. Nothing is read that a later call

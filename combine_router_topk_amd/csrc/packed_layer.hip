@@ -7,6 +7,13 @@
 // The tokens are the matrix instruction's first operand here and the weight rows
 // its second, so that a lane's results belong to one weight row and take one
 // scale.
+//
+// The weights' bytes bound it: 32 tokens of 256 experts, 7168 x 2048, read 4.0 GB and
+// take 746 us, 5.4 TB/s where a large copy reaches 4.85. A few tokens are bound by two
+// dependent launches instead: one token of 256 experts, 4096 x 2048, top-8, 102 MB,
+// takes 30 us, 17 for the first and 10 to 12 for the second. (The down product needs
+// all of h; a grid that waits inside one launch would need every block to be there at
+// once.)
 #include "device.hpp"
 #include "few_tokens.hpp"
 #include "launch.hpp"
@@ -19,7 +26,11 @@ namespace {
 
 constexpr int kUpThreads = 256, kUpWaves = kUpThreads / kWave;
 constexpr int kUpBlocks = 1280;
-constexpr int kManyTiles = 4 * kUpBlocks;  // pairs of tiles from which on a block takes two at a time
+// Pairs of tiles from which on a block takes two at a time, which share the loads of the
+// tokens' rows: 32 tokens of 256 experts, 7168 x 2048, 795 us one at a time and 747 so.
+// Below, each block of the grid has no more than four turns, and half of them as long
+// leave more of the CUs idle at the end.
+constexpr int kManyTiles = 4 * kUpBlocks;
 
 struct PackedArgs : RouteArgs {
   const void* x;
@@ -286,6 +297,11 @@ __global__ __launch_bounds__(256) void packed_sum_kernel(PackedArgs g, int share
   else static_cast<uint2*>(g.out)[i] = make_uint2(pack2<ACT>(z.x, z.y), pack2<ACT>(z.z, z.w));
 }
 
+// One block on a column tile at a time is enough while the tiles fill the 256 CUs or are
+// few. Where they fill them unevenly (448 of 7168 columns: one CU in four has one, the
+// others two) and the weights are large, the sequence is split and blocks become many:
+// 32 tokens of 256 experts, 7168 x 2048, 795 us with 8 shares, 819 with 4, 866 without;
+// 5 and 12 as 8. Below 2^30 weights the extra launch takes longer than it saves.
 constexpr int kShares = 8;
 int shares_of(int T, int E, int k, int H, int I) {
   const int tiles = packed_row_tiles(H);
@@ -333,6 +349,9 @@ hipError_t launch(const PackedArgs& g, hipStream_t s) {
     packed_down_kernel<ACT, CODES, PER, NT, TILES>
         <<<grid, NT, DownTables::bytes(g.T * g.k, g.T, NT / kWave, TILES * kPackedRows), s>>>(g);
   };
+  // Up to 256 tiles a CU has one block, which then has 16 waves to keep loads in flight:
+  // one token of 256 experts, 4096 x 2048, 30.2 us for 31.8 with 8. With more tiles
+  // two blocks of 8 waves are better: 934 us for 966 in the large case.
   using One = std::integral_constant<int, 1>;
   if (shares > 1) down(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
   else if (packed_row_tiles(g.H) <= 256) down(std::integral_constant<int, 1024>{}, One{});

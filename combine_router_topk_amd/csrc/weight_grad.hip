@@ -7,6 +7,18 @@
 // memory. Rows go to LDS as they are, and the LDS reads transpose: four lanes read
 // 16 neighbouring values of one row, and each lane of 16 gets four rows of one
 // column.
+//
+// A block sums 128 x 256 weights over one expert's rows, 32 at a time, its four waves
+// 64 x 128 each, so that a step's 24 reads of 64 lanes x 8 bytes feed 32 products of a
+// wave; two blocks run on a CU. (256 x 256 with one block on a CU, through registers:
+// 2129 us for the second case below; steps of 64 rows the same.) With long segments the
+// loop bounds it: 16384 rows an expert reach 1015 TFLOP/s (a library product of 8192^3
+// with the first operand transposed 1096). With 512 rows an expert, 64 experts of 4096 x
+// 4096 in bf16, it takes 1455 us, 756 TFLOP/s: without its 2.1 GB of stores 1099, so
+// the two blocks of a CU hide little of them. 16384 tokens of a skewed top-6, 64 experts
+// of 2048 x 1024 into fp32 with what is there added, take 600 to 620 us, of which their
+// bytes take 346 at a large copy's rate; 1021 tokens of top-2, 8 experts of 2872 x 1424
+// into fp32 46 us for 30.
 #include <limits.h>
 
 #include "device.hpp"
@@ -93,7 +105,9 @@ __device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
 }
 
 // Tile `in` of an expert. Neighbouring blocks go to the eight dies in turn, so each die
-// takes a run of tiles, in panels of four along N: they share rows in its cache.
+// takes a run of tiles, in panels of eight along N: they share rows in its cache. (Panels
+// of 4 and of 16: 1453 and 1431 us for the 1442 of 64 experts of 4096 x 4096, 593 and 600
+// for 600 of the skewed batch.)
 __device__ __forceinline__ void tile_of(const GradArgs& g, int in, int& tn, int& tk) {
   const int tiles = g.n_tiles * g.k_tiles;
   if (tiles % kXcds == 0) in = in % kXcds * (tiles / kXcds) + in / kXcds;
