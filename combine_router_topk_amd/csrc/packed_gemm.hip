@@ -44,18 +44,26 @@ __device__ __forceinline__ int2 segment_of(const PackedGemmArgs& g, int e) {
   return make_int2(at, min(max(g.counts[e], 0), g.rows - at));
 }
 
-// First tile of each expert, with `per` rows a tile: first[E] is their number.
+// First tile of each expert, with `per` rows a tile: first[E] is their number. Segments
+// that do not overlap, as moe_layout writes them, have rows / per + E times n_tiles of
+// them at most, which fits 32 bits; where counts say more, the tiles end there. (Without
+// n_tiles, all experts with all rows are 2^30 at most.)
 struct Segments {
   int first[kMaxE + 1];
 };
 template <int NT>
 __device__ __forceinline__ void find_segments(const PackedGemmArgs& g, int per, Segments& sh, int* sums) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  auto first_tile = [&](int m_tiles) {
+    const long long n = static_cast<long long>(m_tiles) * g.n_tiles;
+    const int most = (g.rows / per + g.E) * g.n_tiles;
+    return n < most ? static_cast<int>(n) : most;
+  };
   int base = 0;
   for (int e0 = 0; e0 < g.E; e0 += NT) {
     const int e = e0 + tid;
     int tiles = 0;
-    if (e < g.E) tiles = (segment_of(g, e).y + per - 1) / per * g.n_tiles;
+    if (e < g.E) tiles = (segment_of(g, e).y + per - 1) / per;
     const int upto = wave_incl_scan(tiles, lane);
     if (lane == kWave - 1) sums[wave] = upto;
     __syncthreads();
@@ -64,10 +72,10 @@ __device__ __forceinline__ void find_segments(const PackedGemmArgs& g, int per, 
       if (w < wave) before += sums[w];
       base += sums[w];
     }
-    if (e < g.E) sh.first[e] = before + upto - tiles;
+    if (e < g.E) sh.first[e] = first_tile(before + upto - tiles);
     __syncthreads();
   }
-  if (tid == 0) sh.first[g.E] = base;
+  if (tid == 0) sh.first[g.E] = first_tile(base);
   __syncthreads();
 }
 // The expert of tile i: the last one whose first tile is not behind it (experts

@@ -288,3 +288,33 @@ def test_weights_past_four_gigabytes():
         z, dz = av @ v[-64:].T, (K + K / 32 + 8) * 2 * U * (np.abs(av) @ mag[-64:].T)
         assert_within(f64(y[rows - 3:, -64:]), z, dz + round_bound(np.abs(z) + dz, act), f"{rows} rows")
         assert not y[:rows - 3].any()
+
+
+def test_counts_of_all_rows_for_all_experts_end_with_the_grid():
+    """Tiles of 1024 experts that each claim all of 2^24 rows are more than 32 bits
+    hold; the call ends with what segments side by side could have, in bounds."""
+    T, E, k, K, N, act = (1 << 20) - 1, 1024, 16, 8, 192, B.MOE_BF16
+    n = T * k
+    say(f"[case] overlapping segments rows={n} E={E}")
+    assert E * (-(-n // 16)) * (N // 64) > 1 << 31 and few_rows(n, E, K, N)
+    p = B.make_problem(T, E, k, 8, 1, act)
+    w = Weights(np.random.default_rng(5), E, N, K, O.INT, 128, act)
+    a = torch.ones(T, K, dtype=torch.bfloat16, device="cuda")
+    src = torch.arange(n, dtype=torch.int32, device="cuda")
+    y = torch.full((n + 1, N), -7.0, dtype=torch.bfloat16, device="cuda")
+    counts = torch.full((E,), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    offsets = torch.zeros(E, dtype=torch.int32, device="cuda")
+    B.moe_expert_gemm_packed(p, w.format, K, N, a, src, w.dev, counts, offsets, y)
+    torch.cuda.synchronize()
+    assert (y[n] == -7).all()
+    counts = torch.zeros(E, dtype=torch.int32, device="cuda")
+    counts[7] = n  # and counts that the rows allow are all served
+    B.moe_expert_gemm_packed(p, w.format, K, N, a, src, w.dev, counts, offsets, y)
+    torch.cuda.synchronize()
+    v, mag = w.both(7)
+    z, dz = v.sum(1), (K + 9) * 2 * U * mag.sum(1)
+    want = torch.from_numpy(z).cuda()
+    bound = torch.from_numpy(dz + round_bound(np.abs(z) + dz, act)).cuda()
+    for part in y[:n].split(1 << 20):
+        assert ((part.double() - want).abs() <= bound).all()
+    assert (y[n] == -7).all()
