@@ -297,24 +297,30 @@ __global__ __launch_bounds__(256) void packed_sum_kernel(PackedArgs g, int share
   else static_cast<uint2*>(g.out)[i] = make_uint2(pack2<ACT>(z.x, z.y), pack2<ACT>(z.z, z.w));
 }
 
-// One block on a column tile at a time is enough while the tiles fill the 256 CUs or are
-// few. Where they fill them unevenly (448 of 7168 columns: one CU in four has one, the
-// others two) and the weights are large, the sequence is split and blocks, with two
-// tiles each then, become many. Whole layer, us without and with 8 shares (integers,
-// groups of 128; 4 shares 3 % slower in the first, 5 and 12 the same):
+// With many weights one block on a column tile at a time leaves CUs without work at the
+// end (448 tiles of 7168 columns: one CU in four has one, the others two), and waves'
+// parts are long. The sequence is split then, and blocks, with two tiles each, become
+// many. Whole layer, us without and with 8 shares (integers, groups of 128; 4 shares
+// 3 % slower in the first, 5 and 12 the same):
 //   tokens, experts, top-k, H, I    weights of the down product
 //   32, 256, 8, 7168, 2048          2^31.8    734, 633
+//   32, 256, 8, 4096, 2048          2^31.0    411, 376
 //   16, 128, 8, 7168, 2048          2^30.8    420, 369
 //   32, 64, 8, 7168, 2048           2^29.8    331, 289
 //   32, 64, 8, 4112, 2048           2^29.0    256, 188
-//   8, 64, 2, 7168, 2048            2^27.8     81, 78
-//   32, 32, 4, 5120, 1024           2^27.3     67, 58
-//   1, 64, 8, 7168, 2048            2^26.8     39, 40
+//   8, 64, 8, 4096, 2048            2^29.0    125, 118
+//   16, 160, 6, 2064, 1424          2^28.1    120, 102
+//   8, 64, 2, 7168, 2048            2^27.8     81,  78
+//   32, 64, 8, 2048, 1408           2^27.5    106,  82
+//   32, 32, 4, 5120, 1024           2^27.3     67,  58
+//   64, 64, 4, 1024, 2048           2^27.0    124,  83
+//   8, 64, 2, 4096, 2048            2^27.0     40,  42
+//   1, 64, 8, 7168, 2048            2^26.8     39,  40
+//   5, 64, 6, 2064, 1424            2^26.4     39,  39
 constexpr int kShares = 8;
 int shares_of(int T, int E, int k, int H, int I) {
-  const int tiles = packed_row_tiles(H);
   const long long experts = T * k < E ? T * k : E;
-  return tiles > 256 && tiles % 256 != 0 && experts * H * I >= 1ll << 27 ? kShares : 1;
+  return experts * H * I >= (T * k >= 64 ? 1ll << 27 : 3ll << 26) ? kShares : 1;
 }
 
 size_t whole(size_t bytes) { return (bytes + 255) / 256 * 256; }

@@ -131,6 +131,17 @@ def test_layer_with_a_down_product_in_shares(T, k, flags):
     check_layer(T, E, k, 4112, 2048, B.MOE_BF16, O.E2M1, 64, flags, logits)
 
 
+@pytest.mark.parametrize("T,k,H,I,flags", [(64, 1, 2064, 1024, 0), (11, 6, 2064, 1040, B.MOE_FLAG_OUT_F32),
+                                           (9, 8, 16, 131072, 0)])
+def test_layer_in_shares_of_few_tiles(T, k, H, I, flags):
+    """An odd number of tiles, fewer than CUs, one with the inner rows alone."""
+    rng = np.random.default_rng(T)
+    E = 65
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    logits[:, rng.permutation(E)[:9]] += 20
+    check_layer(T, E, k, H, I, B.MOE_F16, O.INT, 32, flags, logits)
+
+
 def test_ties_nan_and_infinite_logits_route_as_the_router_does():
     rng = np.random.default_rng(3)
     for E, k in ((16, 5), (100, 7), (256, 8), (1000, 16)):
