@@ -372,8 +372,9 @@ __global__ __launch_bounds__(256) void weight_grad_sum_kernel(GradArgs g) {
   }
 }
 
-int n_tiles_of(int N) { return (N + kTileN - 1) / kTileN; }
-int k_tiles_of(int K) { return (K + kTileK - 1) / kTileK; }
+// Of N and K from 1 up to the end of 32 bits.
+int n_tiles_of(int N) { return (N - 1) / kTileN + 1; }
+int k_tiles_of(int K) { return (K - 1) / kTileK + 1; }
 
 // The plan's sizes; `units` 0 for no plan. A token chooses an expert once, so no tile has
 // more than T rows; with k tiles >= kSlots that is no more than a block's share of the
