@@ -335,11 +335,24 @@ def _packed_places(f: B.PackedFormat, device) -> tuple[torch.Tensor, torch.Tenso
     return g, 8 * j + inner
 
 
+def _lay_out(q: torch.Tensor, scale: torch.Tensor, f: B.PackedFormat) -> torch.Tensor:
+    """One matrix's tiles from the codes 0 .. 15 and the 16-bit scales of whole tiles' rows."""
+    nt, kt, per = q.shape[0] // 16, q.shape[1] // 128, 128 // f.group
+    q = q.view(nt, 16, kt, 128).to(torch.uint8)
+    g, nibble = _packed_places(f, q.device)
+    codes = torch.zeros(nt, kt, 4, 16, 32, dtype=torch.uint8, device=q.device)
+    codes[:, :, g, :, nibble] = q.permute(3, 0, 2, 1)
+    codes = codes[..., ::2] | codes[..., 1::2] << 4
+    scale = scale.view(nt, 16, kt, per).transpose(1, 2).contiguous()
+    return torch.cat([codes.reshape(nt, kt, 1024), scale.view(torch.uint8).view(nt, kt, -1)], 2).view(-1)
+
+
 def pack_weights(w: torch.Tensor, f: B.PackedFormat) -> torch.Tensor:
     """Weights [..., rows, cols] in 4 bits (see include/moe_route.h), each group of
     columns with the scale that takes its largest magnitude to the largest code (7
     or 6), each value to the nearest code (ties to the even one). Done once for a
-    model, in torch operations on w's device; returns uint8 [..., bytes]."""
+    model, in torch operations on w's device; returns uint8 [..., bytes]. Weights that
+    are in 4 bits already keep their codes and scales with pack_codes."""
     if w.dim() < 2 or f.group not in (32, 64, 128):
         raise ValueError("weights [..., rows, cols] and groups of 32, 64 or 128 columns")
     lead, (rows, cols) = w.shape[:-2], w.shape[-2:]
@@ -365,14 +378,43 @@ def pack_weights(w: torch.Tensor, f: B.PackedFormat) -> torch.Tensor:
             for n, b in enumerate(borders[1:].tolist(), 1):
                 q += (a >= b) if n % 2 else (a > b)
             q += 8.0 * (t < 0)
-        q = q.view(nt, 16, kt, 128).to(torch.uint8)
-        g, nibble = _packed_places(f, w.device)
-        codes = torch.zeros(nt, kt, 4, 16, 32, dtype=torch.uint8, device=w.device)
-        codes[:, :, g, :, nibble] = q.permute(3, 0, 2, 1)
-        codes = codes[..., ::2] | codes[..., 1::2] << 4
-        scale = scale.view(nt, 16, kt, per).transpose(1, 2).contiguous()
-        out.append(torch.cat([codes.reshape(nt, kt, 1024), scale.view(torch.uint8).view(nt, kt, -1)], 2).view(-1))
+        out.append(_lay_out(q.view(nt * 16, kt * 128), scale, f))
     return torch.stack(out).view(*lead, -1) if out else w.new_zeros((*lead, 0), dtype=torch.uint8)
+
+
+def pack_codes(codes: torch.Tensor, scale: torch.Tensor, f: B.PackedFormat) -> torch.Tensor:
+    """Weights that are in 4 bits already, laid out with the codes and scales that they
+    have: codes [..., rows, cols] of any whole-number type, -8 .. 7 for integers or
+    the e2m1 patterns 0 .. 15, and scale [..., rows, ceil(cols / group)] in the
+    format's 16 bits, the first of each row for its first `group` columns. Returns
+    uint8 [..., bytes], as pack_weights does."""
+    if codes.dim() < 2 or 0 in codes.shape[-2:] or f.group not in (32, 64, 128) \
+            or f.codes not in (B.MOE_PACKED_INT, B.MOE_PACKED_E2M1):
+        raise ValueError("codes [..., rows, cols], integers or e2m1, and groups of 32, 64 or 128 columns")
+    if codes.dtype.is_floating_point or codes.dtype.is_complex or codes.dtype == torch.bool:
+        raise ValueError(f"codes: dtype {codes.dtype}, expected whole numbers")
+    lead, (rows, cols) = codes.shape[:-2], codes.shape[-2:]
+    groups = -(-cols // f.group)
+    if tuple(scale.shape) != (*lead, rows, groups) or scale.dtype != B._TORCH_ACT[f.scale_dtype]:
+        raise ValueError(f"scale: {list(scale.shape)} {scale.dtype}, codes {list(codes.shape)} in groups of {f.group} "
+                         f"need {[*lead, rows, groups]} {B._TORCH_ACT[f.scale_dtype]}")
+    nt, kt, per = -(-rows // 16), -(-cols // 128), 128 // f.group
+    zero = 8 if f.codes == B.MOE_PACKED_INT else 0
+    out = []
+    for c, s in zip(codes.reshape(-1, rows, cols), scale.reshape(-1, rows, groups)):
+        lo, hi = (int(x) for x in c.aminmax())
+        if lo < -zero or hi > 15 - zero:
+            raise ValueError(f"codes outside {-zero} .. {15 - zero}")
+        if not bool(torch.isfinite(s).all()):
+            raise ValueError("a group's scale is not finite")
+        q = torch.full((nt * 16, kt * 128), zero, dtype=torch.uint8, device=codes.device)
+        q[:rows, :cols] = (c.to(torch.int16) + zero).to(torch.uint8)
+        whole = torch.zeros(nt * 16, kt * per, dtype=s.dtype, device=codes.device)
+        whole[:rows, :groups] = s
+        out.append(_lay_out(q, whole, f))
+    if not out:
+        return torch.zeros(*lead, B.moe_packed_weight_bytes(f, 1, rows, cols), dtype=torch.uint8, device=codes.device)
+    return torch.stack(out).view(*lead, -1)
 
 
 def unpack_weights(packed: torch.Tensor, rows: int, cols: int, f: B.PackedFormat) -> torch.Tensor:
