@@ -837,11 +837,14 @@ moe_status moe_adamw_step(const moe_adamw* h, const moe_adamw_tensor* tensors, i
   const char* fn = "moe_adamw_step";
   if (h == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: h is NULL", fn);
   if (n < 0) return fail(MOE_ERR_INVALID_ARG, "%s: n=%d < 0", fn, n);
-  if (!std::isfinite(h->lr)) return fail(MOE_ERR_INVALID_ARG, "%s: lr=%g is not finite", fn, h->lr);
+  // the kernel takes both as fp32
+  if (!std::isfinite(static_cast<float>(h->lr))) return fail(MOE_ERR_INVALID_ARG, "%s: lr=%g is not finite in fp32", fn, h->lr);
   if (!(h->beta1 >= 0.0 && h->beta1 < 1.0)) return fail(MOE_ERR_INVALID_ARG, "%s: beta1=%g outside [0, 1)", fn, h->beta1);
   if (!(h->beta2 >= 0.0 && h->beta2 < 1.0)) return fail(MOE_ERR_INVALID_ARG, "%s: beta2=%g outside [0, 1)", fn, h->beta2);
-  if (!(h->eps >= 0.0) || !std::isfinite(h->eps))
-    return fail(MOE_ERR_INVALID_ARG, "%s: eps=%g is not finite and >= 0", fn, h->eps);
+  if (!(h->eps >= 0.0) || !std::isfinite(static_cast<float>(h->eps)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: eps=%g is not finite in fp32 and >= 0", fn, h->eps);
+  if (h->eps > 0.0 && static_cast<float>(h->eps) == 0.0f)
+    return fail(MOE_ERR_INVALID_ARG, "%s: eps=%g is 0 in fp32", fn, h->eps);
   if (h->step < 1) return fail(MOE_ERR_INVALID_ARG, "%s: step=%d < 1", fn, h->step);
   for (const int32_t d : {h->w_dtype, h->g_dtype})
     if (d != MOE_F32 && d != MOE_F16 && d != MOE_BF16)

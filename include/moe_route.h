@@ -689,8 +689,10 @@ moe_status moe_expert_weight_grad(const moe_problem* p, int32_t K, int32_t N, co
                                   size_t ws_bytes, void* stream);
 
 /* One AdamW step.
- *   lr, beta1, beta2, eps  finite, eps >= 0, 0 <= beta < 1; in 64 bits, as 1 -
- *               0.999 is off by 1.3e-5 of itself in 32
+ *   lr, beta1, beta2, eps  eps >= 0, 0 <= beta < 1; in 64 bits, as 1 - 0.999 is
+ *               off by 1.3e-5 of itself in 32. lr and eps are rounded to fp32, where
+ *               they are finite and an eps above 0 stays above it. (With eps = 0 a
+ *               weight whose m and v are 0 becomes NaN, 0 / 0.)
  *   step        1 for the first one
  *   w_dtype     MOE_F32, MOE_F16 or MOE_BF16, of every tensor's w
  *   g_dtype     of every tensor's g: MOE_F32, or 16 bits (with 16-bit w the same
@@ -741,8 +743,8 @@ typedef struct {
  * gradient that is not finite makes m and v of its 128 elements NaN for good;
  * control's scale can skip such a step.
  * `tensors` is a HOST array, read during the call; nothing of it is kept. Up to 56
- * tensors go into one launch. A tensor has fewer than 2^35 elements
- * (MOE_ERR_UNSUPPORTED).
+ * tensors go into one launch. A tensor has at most 2^35 - 2048
+ * elements (MOE_ERR_UNSUPPORTED).
  *   control  f32 [3] on the device (read) or NULL: learning rate, step number and a
  *            factor for the gradients in place of h->lr, h->step and 1, for
  *            schedules and clipping under graph replay. A factor that is NaN or
