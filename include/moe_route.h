@@ -614,8 +614,10 @@ moe_status moe_packed_weight_bytes(const moe_packed_format* f, int32_t E, int32_
  * activation format, or written as fp32 with MOE_FLAG_OUT_F32. Codes become 16-bit
  * numbers exactly, products are exact, sums of 32 columns or more and their
  * multiplication by the scale are in fp32. Integer codes are summed as 0 .. 15 with 8
- * times the sum of the row's values taken off, so an infinity in a row makes its
- * results NaN.
+ * times the sum of the row's values taken off: an infinity in a row makes its results
+ * NaN, sums are off by fp32 steps of (code + 8) times the values, and bf16 rows whose
+ * 15-fold values' sum over a group passes fp32's range before the scale is applied
+ * become NaN or infinite (e2m1: 6-fold).
  *   K   columns of a and w, a multiple of 8     N  rows of w, a multiple of 8
  *   a   16-bit [rows, K] (read): T k rows in send order, or with src T token rows
  *   src             i32 [T*k] (read) from moe_layout, or NULL
@@ -728,20 +730,22 @@ typedef struct {
   float weight_decay;
 } moe_adamw_tensor;
 
-/* An AdamW step over n tensors at once, the way the routed layer's weights (the
- * experts', gamma of the norm, the router's) are trained from their gradients:
+/* An AdamW step over n tensors at once, weights of any kind with their gradients (those
+ * of moe_expert_weight_grad and moe_rms_norm_backward's dgamma as they are written):
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2, in fp32
  *   w = w - lr weight_decay w - lr (m / c1) / (sqrt(v / c2) + eps)
  *   c1 = 1 - beta1^step,  c2 = 1 - beta2^step
  * w is taken from master where that is given, updated in fp32 and rounded once.
  * m and v are sums of products each rounded to fp32, with no multiply-add in their
- * place, an 8-bit state's scale is its largest magnitude times the rounded 1 / 448,
+ * place (the gradient with its factor first, (1 - beta2) g g from the left), an 8-bit
+ * state's scale is its largest magnitude, at least 2^-100, times the rounded 1 / 448,
  * and its code the rounded quotient of value and scale: the states are those of the
  * same formulas in elementary fp32 operations, bit for bit.
  * With 8-bit states the step uses m and v before they are rounded to 8 bits; a
  * root of v above 0 takes at least the smallest code, so that it stays above 0. A
- * gradient that is not finite makes m and v of its 128 elements NaN for good;
- * control's scale can skip such a step.
+ * gradient that is not finite makes m, v and w of its element NaN or infinite for
+ * good, and with 8-bit states m and v of its 128 elements NaN; one whose (1 - beta2)
+ * g g is beyond fp32 makes v so. control's scale can skip such a step.
  * `tensors` is a HOST array, read during the call; nothing of it is kept. Up to 56
  * tensors go into one launch. A tensor has at most 2^35 - 2048
  * elements (MOE_ERR_UNSUPPORTED).
