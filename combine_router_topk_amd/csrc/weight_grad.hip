@@ -47,7 +47,7 @@ struct GradArgs {
   const int32_t* src;
   const int32_t* counts;
   const int32_t* offsets;
-  int rows, a_rows, E, K, N, n_tiles, k_tiles;
+  int rows, E, K, N, n_tiles, k_tiles;
   uint32_t inverse;  // 2^32 / k, rounded up: i / k is the product's high half (i < 2^24, k <= 16); 0 for k = 1
   bool out_f32, add;
   void* dw;
@@ -416,7 +416,6 @@ hipError_t launch_weight_grad(const void* a, const int32_t* src, const void* dy,
   g.counts = counts;
   g.offsets = offsets;
   g.rows = T * k;
-  g.a_rows = src != nullptr ? T : T * k;
   g.E = E;
   g.K = K;
   g.N = N;
