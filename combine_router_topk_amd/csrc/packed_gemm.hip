@@ -192,7 +192,10 @@ __global__ __launch_bounds__(kThinThreads, TILES == 2 ? 5 : 4) void packed_thin_
 //
 // The vector unit bounds it beside the matrix cores: 8 codes take 4 to 7 of its
 // instructions, each group's sums of a fragment four more, and a fragment's product
-// occupies the matrix cores for 16 cycles at best. Measured with 8192 tokens of a top-6
+// occupies the matrix cores for 16 cycles at best. With e2m1 in groups of 32 the vector
+// unit issues in 61 % (K = 1024) to 69 % (gate and up, K = 2048) of the cycles and the
+// matrix cores are busy in 31 to 33 %: together nearly all of them, so the two waves of a
+// SIMD, which pass the same barrier in each step, hardly run them at once. Measured with 8192 tokens of a top-6
 // over 64 experts, N = 2048, TFLOP/s: K = 4096, e2m1 955 in groups of 128 and 766 in
 // groups of 32, integers 811 and 672; K = 1024 (8 steps a tile, where a tile's first
 // loads and its results take a sixth) 812, 670, 701 and 595. (Operands through
@@ -443,7 +446,8 @@ __global__ __launch_bounds__(kFatThreads, 2) void packed_fat_kernel(PackedGemmAr
 // Which kernel: the thin one takes every 16 rows (half of an expert's last ones are not
 // there on average) through the expert's weights, at 8.5e12 weights a second. A tile of
 // the fat one takes 1.55 us a step with up to 64 rows and 2.2 with more, on each of 256
-// CUs. Measured, us of both (int4, groups of 128; rows an expert on average):
+// CUs. Measured, us of both (int4, groups of 128; rows an expert on average), the same
+// inputs again and again: all but the second case's weights stay in the last-level cache:
 //   experts, K, N             8         16        24        32        64        128
 //   64, 2048, 2048        34,  55   55,  53   76,  52   82,  52  157,  77  300, 157
 //   256, 2048, 4096      255, 389  352, 393  433, 399  531, 409  950, 546 1857, 917

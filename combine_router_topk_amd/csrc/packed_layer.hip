@@ -9,7 +9,7 @@
 // scale.
 //
 // The weights' bytes bound it: 32 tokens of 256 experts, 7168 x 2048, read 4.0 GB and
-// take 746 us, 5.4 TB/s where a large copy reaches 4.85. A few tokens are bound by two
+// take 746 to 777 us, 5.2 to 5.4 TB/s where a large copy reaches 4.85. A few tokens are bound by two
 // dependent launches instead: one token of 256 experts, 4096 x 2048, top-8, 102 MB,
 // takes 30 us, 17 for the first and 10 to 12 for the second. (The down product needs
 // all of h; a grid that waits inside one launch would need every block to be there at
@@ -301,7 +301,9 @@ __global__ __launch_bounds__(256) void packed_sum_kernel(PackedArgs g, int share
 // end (448 tiles of 7168 columns: one CU in four has one, the others two), and waves'
 // parts are long. The sequence is split then, and blocks, with two tiles each, become
 // many. Whole layer, us without and with 8 shares (integers, groups of 128; 4 shares
-// 3 % slower in the first, 5 and 12 the same):
+// 3 % slower in the first, 5 and 12 the same), the same inputs again and again: where
+// they have under 256 MB, the weights come from the last-level cache (the last case takes
+// 44 us with three sets in turn, the one before 48; no width under 1024 was measured):
 //   tokens, experts, top-k, H, I    weights of the down product
 //   32, 256, 8, 7168, 2048          2^31.8    734, 633
 //   32, 256, 8, 4096, 2048          2^31.0    411, 376
@@ -365,7 +367,8 @@ hipError_t launch(const PackedArgs& g, hipStream_t s) {
   };
   // Up to 256 tiles a CU has one block, which then has 16 waves to keep loads in flight:
   // one token of 256 experts, 4096 x 2048, 30.2 us for 31.8 with 8. With more tiles
-  // two blocks of 8 waves are better: 934 us for 966 in the large case.
+  // two blocks of 8 waves are better: one token's top-8 in 7168 x 2048 (64 experts) 48.3
+  // us for 50.2 with 16, in 7168 x 1024 (256 experts) 31.8 for 33.5, inputs in turn.
   using One = std::integral_constant<int, 1>;
   if (shares > 1) down(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
   else if (packed_row_tiles(g.H) <= 256) down(std::integral_constant<int, 1024>{}, One{});

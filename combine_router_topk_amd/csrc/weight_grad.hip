@@ -14,11 +14,13 @@
 // 2129 us for the second case below; steps of 64 rows the same.) With long segments the
 // loop bounds it: 16384 rows an expert reach 1015 TFLOP/s (a library product of 8192^3
 // with the first operand transposed 1096). With 512 rows an expert, 64 experts of 4096 x
-// 4096 in bf16, it takes 1455 us, 756 TFLOP/s: without its 2.1 GB of stores 1099, so
-// the two blocks of a CU hide little of them. 16384 tokens of a skewed top-6, 64 experts
-// of 2048 x 1024 into fp32 with what is there added, take 600 to 620 us, of which their
-// bytes take 346 at a large copy's rate; 1021 tokens of top-2, 8 experts of 2872 x 1424
-// into fp32 46 us for 30.
+// 4096 in bf16, it takes 1437 to 1455 us, 756 to 765 TFLOP/s: without its 2.1 GB of
+// stores 1099, so the two blocks of a CU hide little of them. 16384 tokens of a skewed
+// top-6, 64 experts of 2048 x 1024 into fp32 with what is there added, take 595 to 620
+// us, 508 without the addition and 470 into bf16: the results' reads and stores behind
+// the products are what is left over the 346 of its bytes at a large copy's rate. 1021
+// tokens of top-2, 8 experts of 2872 x 1424 into fp32, 50 us again and again and 55 to 57
+// with inputs that change, for 30.
 #include <limits.h>
 
 #include "device.hpp"
