@@ -335,6 +335,12 @@ def _packed_places(f: B.PackedFormat, device) -> tuple[torch.Tensor, torch.Tenso
     return g, 8 * j + inner
 
 
+def _check_format(f: B.PackedFormat) -> None:
+    if f.codes not in (B.MOE_PACKED_INT, B.MOE_PACKED_E2M1) or f.group not in (32, 64, 128) \
+            or f.scale_dtype not in B._TORCH_ACT:
+        raise ValueError(f"{f}: a format has integers or e2m1, groups of 32, 64 or 128 columns and 16-bit scales")
+
+
 def _lay_out(q: torch.Tensor, scale: torch.Tensor, f: B.PackedFormat) -> torch.Tensor:
     """One matrix's tiles from the codes 0 .. 15 and the 16-bit scales of whole tiles' rows."""
     nt, kt, per = q.shape[0] // 16, q.shape[1] // 128, 128 // f.group
@@ -353,8 +359,9 @@ def pack_weights(w: torch.Tensor, f: B.PackedFormat) -> torch.Tensor:
     or 6), each value to the nearest code (ties to the even one). Done once for a
     model, in torch operations on w's device; returns uint8 [..., bytes]. Weights that
     are in 4 bits already keep their codes and scales with pack_codes."""
-    if w.dim() < 2 or f.group not in (32, 64, 128):
-        raise ValueError("weights [..., rows, cols] and groups of 32, 64 or 128 columns")
+    _check_format(f)
+    if w.dim() < 2 or 0 in w.shape[-2:]:
+        raise ValueError("weights [..., rows, cols], one row and column at least")
     lead, (rows, cols) = w.shape[:-2], w.shape[-2:]
     nt, kt, per = -(-rows // 16), -(-cols // 128), 128 // f.group
     ints = f.codes == B.MOE_PACKED_INT
@@ -379,7 +386,9 @@ def pack_weights(w: torch.Tensor, f: B.PackedFormat) -> torch.Tensor:
                 q += (a >= b) if n % 2 else (a > b)
             q += 8.0 * (t < 0)
         out.append(_lay_out(q.view(nt * 16, kt * 128), scale, f))
-    return torch.stack(out).view(*lead, -1) if out else w.new_zeros((*lead, 0), dtype=torch.uint8)
+    if not out:
+        return torch.zeros(*lead, B.moe_packed_weight_bytes(f, 1, rows, cols), dtype=torch.uint8, device=w.device)
+    return torch.stack(out).view(*lead, -1)
 
 
 def pack_codes(codes: torch.Tensor, scale: torch.Tensor, f: B.PackedFormat) -> torch.Tensor:
@@ -388,9 +397,9 @@ def pack_codes(codes: torch.Tensor, scale: torch.Tensor, f: B.PackedFormat) -> t
     the e2m1 patterns 0 .. 15, and scale [..., rows, ceil(cols / group)] in the
     format's 16 bits, the first of each row for its first `group` columns. Returns
     uint8 [..., bytes], as pack_weights does."""
-    if codes.dim() < 2 or 0 in codes.shape[-2:] or f.group not in (32, 64, 128) \
-            or f.codes not in (B.MOE_PACKED_INT, B.MOE_PACKED_E2M1):
-        raise ValueError("codes [..., rows, cols], integers or e2m1, and groups of 32, 64 or 128 columns")
+    _check_format(f)
+    if codes.dim() < 2 or 0 in codes.shape[-2:]:
+        raise ValueError("codes [..., rows, cols], one row and column at least")
     if codes.dtype.is_floating_point or codes.dtype.is_complex or codes.dtype == torch.bool:
         raise ValueError(f"codes: dtype {codes.dtype}, expected whole numbers")
     lead, (rows, cols) = codes.shape[:-2], codes.shape[-2:]
@@ -419,6 +428,9 @@ def pack_codes(codes: torch.Tensor, scale: torch.Tensor, f: B.PackedFormat) -> t
 
 def unpack_weights(packed: torch.Tensor, rows: int, cols: int, f: B.PackedFormat) -> torch.Tensor:
     """The fp32 values [..., rows, cols] that packed weights stand for."""
+    _check_format(f)
+    if packed.dtype != torch.uint8 or rows < 1 or cols < 1 or packed.shape[-1] != B.moe_packed_weight_bytes(f, 1, rows, cols):
+        raise ValueError(f"{packed.dtype} [..., {packed.shape[-1]}] are not the bytes of [{rows}, {cols}] in {f}")
     lead, nt, kt, per = packed.shape[:-1], -(-rows // 16), -(-cols // 128), 128 // f.group
     p = packed.reshape(-1, nt, kt, 1024 + 32 * per)
     b = p[..., :1024].reshape(-1, nt, kt, 4, 16, 16)

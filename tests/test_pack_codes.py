@@ -85,9 +85,38 @@ def test_refusals():
         with pytest.raises(ValueError, match="not finite"):
             P.pack_codes(c, s + v, f)
     for fmt in (B.make_packed_format(B.MOE_PACKED_INT, 16, B.MOE_F16), B.make_packed_format(5, 32, B.MOE_F16)):
-        with pytest.raises(ValueError, match="groups of 32"):
+        with pytest.raises(ValueError, match="32, 64 or 128"):
             P.pack_codes(c, s, fmt)
     with pytest.raises(ValueError):
         P.pack_codes(c[0], s[0], f)
     with pytest.raises(ValueError):
         P.pack_codes(c[:, :0], s[:, :0], f)
+
+
+@pytest.mark.parametrize("codes,group,scale", [(0, 32, B.MOE_F16), (7, 32, B.MOE_F16), (B.MOE_PACKED_INT, 16, B.MOE_F16),
+                                               (B.MOE_PACKED_E2M1, 256, B.MOE_F16), (B.MOE_PACKED_INT, 32, B.MOE_F32),
+                                               (B.MOE_PACKED_E2M1, 32, 0)])
+def test_formats_that_the_calls_refuse_are_not_packed(codes, group, scale):
+    """None of them is taken for another one."""
+    f = B.make_packed_format(codes, group, scale)
+    with pytest.raises(ValueError, match="format"):
+        P.pack_weights(torch.ones(16, 128), f)
+    with pytest.raises(ValueError, match="format"):
+        P.pack_codes(torch.zeros(16, 128, dtype=torch.int8), torch.zeros(16, 4).half(), f)
+    with pytest.raises(ValueError, match="format"):
+        P.unpack_weights(torch.zeros(1152, dtype=torch.uint8), 16, 128, f)
+
+
+def test_sizes_are_checked():
+    f = B.make_packed_format(B.MOE_PACKED_INT, 32, B.MOE_F16)
+    for shape in ((2, 0, 128), (2, 16, 0)):
+        with pytest.raises(ValueError, match="rows, cols"):
+            P.pack_weights(torch.zeros(shape), f)
+    w = P.pack_weights(torch.ones(2, 32, 256), f)
+    for rows, cols in ((32, 384), (16, 256), (48, 256), (32, 128), (0, 256)):
+        with pytest.raises(ValueError, match="bytes"):
+            P.unpack_weights(w, rows, cols, f)
+    with pytest.raises(ValueError, match="bytes"):
+        P.unpack_weights(w.view(torch.int8), 32, 256, f)
+    assert torch.equal(P.unpack_weights(w, 32, 256, f), torch.full((2, 32, 256), 7 * float(np.float16(1 / 7))))
+    assert P.unpack_weights(P.pack_weights(torch.zeros(0, 16, 32), f), 16, 32, f).shape == (0, 16, 32)
